@@ -322,6 +322,129 @@ int64_t llvq_quantize_noalloc_max_blocks(void);
  * Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_pack_fields(const llvq_desc* d, const uint64_t* fields, void* packed, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving: a paged key/value cache that is quantised as it is written, the attention of new
+ * tokens over it, and the check of drafted tokens.  With the weights at 2 bits the cache is the
+ * larger part of what a decoding step reads, and the batch 2..16 of llvq_gemv is the shape of a
+ * step that checks drafts.
+ *
+ * The cache of one layer is one device buffer, the pool: [pages][kv_heads] blocks.  A block
+ * holds page_tokens tokens of one key head:
+ *     key codes   [page_tokens][row]     row = 2 * head_dim, head_dim or head_dim / 2 bytes
+ *     value codes [page_tokens][row]
+ *     key scales  [page_tokens][head_dim / 32]   (not in the bf16 kind)
+ *     value scales [page_tokens][head_dim / 32]
+ * rounded up to 16 bytes.  In the quantised kinds 32 consecutive channels share one power of
+ * two: value = code * 2^e, the scale byte holds e + 127.  Codes are e4m3 (LLVQ_KV_FP8) or e2m1, the
+ * even channel in the low half of a byte (LLVQ_KV_FP4).  e is the smallest integer in [-100, 119]
+ * (FP8) or [-100, 125] (FP4) with max|x| <= top * 2^e, top = 448 or 6; x / 2^e is rounded to the nearest code,
+ * ties to even (past the limits of e it saturates).  A group with a value that is not finite
+ * has the scale byte 255 and stands for NaN.  Every other value is exact in bf16. */
+enum { LLVQ_KV_BF16 = 0, LLVQ_KV_FP8 = 1, LLVQ_KV_FP4 = 2 };
+
+#define LLVQ_MAX_HEAD_DIM 256
+#define LLVQ_MAX_PAGE 4096
+#define LLVQ_MAX_SEQS 32768
+#define LLVQ_MAX_DRAFTS 63
+
+typedef struct {
+  int32_t kind;        /* LLVQ_KV_*                                               */
+  int32_t kv_heads;    /* key heads, 1..1024                                      */
+  int32_t head_dim;    /* 32..256, a multiple of 32                               */
+  int32_t page_tokens; /* tokens of a page, 1..4096                               */
+  int32_t pages;       /* pages of the pool, >= 1                                 */
+} llvq_kv_desc;
+
+/* New tokens of several sequences, packed row after row, and where their caches lie.  The
+ * arrays are device memory (4-byte aligned).  Sequence b's new tokens are rows starts[b] ..
+ * starts[b+1]-1 and the last of its lens[b] cached tokens: row starts[b] + i has position
+ * lens[b] - (starts[b+1] - starts[b]) + i.  Position p lies in slot p % page_tokens of page
+ * table[b][p / page_tokens].
+ * The host knows only the sizes; what the arrays hold is bounded on the device: starts are cut
+ * to 0 .. tokens, lens to what the table can hold (and to 2^30), page numbers outside the pool are never followed. */
+typedef struct {
+  const int32_t* starts; /* [batch + 1], ascending, starts[0] = 0, starts[batch] = tokens */
+  const int32_t* lens;   /* [batch]                                                       */
+  const int32_t* table;  /* [batch][max_pages]; entries past a sequence's pages are not read */
+  int32_t batch;         /* 0..LLVQ_MAX_SEQS (0: nothing to do)                           */
+  int32_t max_pages;     /* >= 0                                                          */
+  int32_t tokens;        /* rows of new tokens, >= 0 (0: nothing to do)                   */
+} llvq_batch;
+
+/* Bytes of a pool, or LLVQ_EINVAL.  Host only. */
+int64_t llvq_kv_pool_bytes(const llvq_kv_desc* d);
+
+/* Write the new tokens' keys and values into the cache.
+ *   pool   : llvq_kv_pool_bytes(d) bytes, 16-byte aligned.
+ *   k, v   : [tokens][kv_heads][head_dim], LLVQ_X_F32 or LLVQ_X_BF16 (`dtype`, both), channels
+ *            contiguous; k_token, k_head, v_token, v_head: strides in elements, >= 0 (rows that 16
+ *            bytes divide are moved 16 bytes at a time).
+ *   err_count : nullable; + 1 for every group that is not finite (quantised kinds), and for every token that has
+ *            no place (negative position, page outside the pool, row outside its sequence: not
+ *            written) or whose sequence's starts or length had to be cut.
+ * No two tokens may have the same place.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_kv_write(const llvq_kv_desc* d, void* pool, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                  int64_t v_token, int64_t v_head, int32_t dtype, const llvq_batch* batch, int32_t* err_count,
+                  void* stream);
+
+/* Read cached tokens back: the same rows and positions as llvq_kv_write (starts = running sums
+ * of lens reads whole sequences).  bf16 and f32 outputs hold the cached values exactly; a token
+ * that has no place reads as zeros and is counted.  Arguments as for llvq_kv_write. */
+int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_token, int64_t k_head, void* v,
+                 int64_t v_token, int64_t v_head, int32_t dtype, const llvq_batch* batch, int32_t* err_count,
+                 void* stream);
+
+/* Attention of the new tokens over their sequences' caches (their own keys and values
+ * included: write them first).
+ *     out[i][h] = sum_j p_j V_j / sum_j p_j,  p_j = exp(scale * q[i][h] . K_j),
+ * over the positions j < lens[b] with j <= pos_i if causal != 0 and j > pos_i - window if window > 0;
+ * K and V are key head h / (heads / kv_heads).  A row that sees nothing is zero.  Keys and values at places
+ * that a row does not see have no effect on it, whatever they hold.
+ *   q, out : [tokens][heads][head_dim], LLVQ_X_F32 or LLVQ_X_BF16 (`dtype`, both), channels contiguous; strides in
+ *            elements, >= 0; out aligned to 4 elements, its strides multiples of 4.
+ *   heads  : a multiple of kv_heads.
+ *   max_chunk : at least the new tokens of any sequence (rows of a sequence past it may be left unwritten: counted).
+ *   max_len : at least 1; about the longest length: it decides only how the keys are split, not
+ *            what is computed.
+ *   scale  : > 0 and finite.   window : 0 (none) .. 2^30.
+ *   workspace : llvq_attn_workspace_bytes(...) bytes for the same arguments, 16-byte aligned
+ *            (may be NULL if that is 0), contents not kept.
+ *   err_count : nullable; + 1 or more if a page number outside the pool was met (its tokens'
+ *            keys and values are then taken as zeros), starts or lengths had to be cut, or a sequence has more rows than max_chunk.
+ * Sums, maxima and outputs are f32; bf16 queries take P in bf16, f32 queries take Q and P in three
+ * bf16 terms.  Deterministic.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
+              int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
+              int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,
+              int32_t* err_count, void* stream);
+
+/* Bytes of llvq_attn's workspace, or LLVQ_EINVAL.  Host only. */
+int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch,
+                                  int32_t max_chunk, int32_t max_len);
+
+/* Check drafted tokens against the target's probabilities.  With n = counts[b] (or drafts),
+ * draft i < n is accepted while uniforms[b][i] * draft[b][i][x_i] < target[b][i][x_i] and all before it were,
+ * x_i = tokens[b][i].  At the first a < n that is not, one token is drawn from max(target[b][a] - draft[b][a], 0)
+ * (from target[b][a] if that is zero everywhere); after n accepted ones, one from target[b][n].  A draw from
+ * weights w takes the v of the largest w_v / noise[b][v] (correctly rounded division) among w_v > 0, the lowest v of
+ * equals.
+ *   target : [batch][drafts + 1][vocab], draft: [batch][drafts][vocab] or NULL (every draft was certain: 1 at
+ *            its token), LLVQ_X_F32 or LLVQ_X_BF16 (`dtype`, both).  NaN and negative weights are never drawn.
+ *   tokens : [batch][drafts]; a token outside the vocabulary is not accepted, and counted.
+ *   counts : [batch] or NULL.   uniforms : [batch][drafts] in [0, 1).
+ *   noise  : [batch][vocab], exponential, >= 0 (a NaN or negative one is never drawn).
+ *   accepted : [batch]: a.   out : [batch][drafts + 1]: the accepted tokens, the drawn one (-1 if
+ *            no weight is positive: counted), then -1.
+ *   drafts : 0..LLVQ_MAX_DRAFTS.   workspace : llvq_draft_workspace_bytes(batch, vocab) bytes, 8-byte aligned.
+ * All arrays contiguous.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
+                      const int32_t* counts, const float* uniforms, const float* noise, int32_t batch,
+                      int32_t drafts, int32_t vocab, int32_t* accepted, int32_t* out, void* workspace,
+                      int32_t* err_count, void* stream);
+
+/* Bytes of llvq_draft_verify's workspace, or LLVQ_EINVAL.  Host only. */
+int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,10 @@ X_BF16 = 1
 SEARCH_ANGULAR = 0
 SEARCH_EUCLID = 1
 MAX_BATCH = 16
+KV_BF16 = 0
+KV_FP8 = 1
+KV_FP4 = 2
+MAX_DRAFTS = 63
 
 _ERRORS = {0: "ok", -1: "invalid argument", -2: "unsupported request", -3: "HIP launch error",
            -4: "request larger than the library's fixed workspace"}
@@ -30,7 +34,9 @@ EXPORTED_SYMBOLS = ("llvq_index_count", "llvq_packed_bytes", "llvq_error_string"
                     "llvq_quantize", "llvq_pack_fields", "llvq_decode_many",
                     "llvq_index_count_wide", "llvq_encode_wide", "llvq_quantize_noalloc",
                     "llvq_quantize_noalloc_max_blocks", "llvq_gptq_workspace_bytes", "llvq_gptq_factor",
-                    "llvq_gptq_begin", "llvq_gptq_column", "llvq_device_checks")
+                    "llvq_gptq_begin", "llvq_gptq_column", "llvq_device_checks", "llvq_kv_pool_bytes",
+                    "llvq_kv_write", "llvq_kv_read", "llvq_attn", "llvq_attn_workspace_bytes",
+                    "llvq_draft_verify", "llvq_draft_workspace_bytes")
 
 
 class LlvqError(RuntimeError):
@@ -47,6 +53,22 @@ class Desc(ctypes.Structure):
     def __repr__(self):
         return (f"Desc(mode={self.mode}, rows={self.rows}, cols={self.cols}, max_shell={self.max_shell}, "
                 f"shape_bits={self.shape_bits}, gain_bits={self.gain_bits})")
+
+
+class KvDesc(ctypes.Structure):
+    """llvq_kv_desc: the paged key/value cache of one layer."""
+    _fields_ = [("kind", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"KvDesc(kind={self.kind}, kv_heads={self.kv_heads}, head_dim={self.head_dim}, "
+                f"page_tokens={self.page_tokens}, pages={self.pages})")
+
+
+class Batch(ctypes.Structure):
+    """llvq_batch: rows of new tokens and where their sequences' caches lie."""
+    _fields_ = [("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int32)]
 
 
 _libs = {}
@@ -109,6 +131,20 @@ def load_library(path=LIB_PATH):
     lib.llvq_pack_fields.restype = ctypes.c_int
     lib.llvq_decode_many.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp]
     lib.llvq_decode_many.restype = ctypes.c_int
+    kp, bp, f32 = ctypes.POINTER(KvDesc), ctypes.POINTER(Batch), ctypes.c_float
+    lib.llvq_kv_pool_bytes.argtypes = [kp]
+    lib.llvq_kv_pool_bytes.restype = i64
+    for name in ("llvq_kv_write", "llvq_kv_read"):
+        getattr(lib, name).argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, bp, vp, vp]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.llvq_attn.argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, i32, bp, i32, i32, f32, i32, i32, vp, vp, vp]
+    lib.llvq_attn.restype = ctypes.c_int
+    lib.llvq_attn_workspace_bytes.argtypes = [kp, i32, i64, i32, i32, i32]
+    lib.llvq_attn_workspace_bytes.restype = i64
+    lib.llvq_draft_verify.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.llvq_draft_verify.restype = ctypes.c_int
+    lib.llvq_draft_workspace_bytes.argtypes = [i32, i32]
+    lib.llvq_draft_workspace_bytes.restype = i64
     _libs[path] = lib
     return lib
 
@@ -332,3 +368,167 @@ def encode_wide(points, max_shell, indices, err_count=None, stream=None):
     n = _check_points(points, indices, err_count, 2, "llvq_encode_wide")
     _check(load_library().llvq_encode_wide(_ptr(points), n, max_shell, _ptr(indices),
                                            _ptr(err_count), _stream(stream)), "llvq_encode_wide")
+
+
+# ---------------------------------------------------------------------------
+# serving: the paged key/value cache, the attention over it, the check of drafts
+
+def make_kv_desc(kind, kv_heads, head_dim, page_tokens, pages) -> KvDesc:
+    return KvDesc(kind, kv_heads, head_dim, page_tokens, pages)
+
+
+def kv_pool_bytes(desc: KvDesc) -> int:
+    """Bytes of the pool [pages][kv_heads][block] (include/llvq.h gives a block's layout)."""
+    n = load_library().llvq_kv_pool_bytes(ctypes.byref(desc))
+    if n < 0:
+        raise LlvqError(int(n), "llvq_kv_pool_bytes")
+    return n
+
+
+def _pool_nbytes(desc):
+    bits = {KV_BF16: 16, KV_FP8: 8, KV_FP4: 4}.get(desc.kind)
+    if bits is None or desc.pages < 1 or desc.kv_heads < 1 or desc.head_dim < 1 or desc.page_tokens < 1:
+        raise ValueError(f"invalid cache descriptor: {desc!r}")
+    token = desc.head_dim * bits // 8 + (0 if desc.kind == KV_BF16 else desc.head_dim // 32)
+    return desc.pages * desc.kv_heads * ((2 * desc.page_tokens * token + 15) // 16 * 16)
+
+
+def _batch(starts, lens, table, tokens, what):
+    """llvq_batch from starts [B + 1], lens [B] and table [B][max_pages] (int32)."""
+    import torch
+    for t, name in ((starts, "starts"), (lens, "lens"), (table, "table")):
+        _tensor(t, f"{what}: {name}", (torch.int32,))
+    n = lens.numel()
+    if lens.dim() != 1 or starts.dim() != 1 or starts.numel() != n + 1 or table.dim() != 2 or table.shape[0] != n:
+        raise ValueError(f"{what}: starts, lens and table must be [B + 1], [B] and [B][max_pages], got "
+                         f"{tuple(starts.shape)}, {tuple(lens.shape)} and {tuple(table.shape)}")
+    return Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), n, table.shape[1], tokens)
+
+
+def _rows(t, name, heads, dim):
+    """Checks rows [tokens][heads][dim] of fp32 or bf16 with contiguous channels; their (token,
+    head) strides in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must have dtype torch.float32 or torch.bfloat16, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(shape)}")
+    if stride[2] != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous channels (strides {stride})")
+    return stride[0], stride[1]
+
+
+def _apart(t, name, strides):
+    """Refuses an output whose rows lie over each other (a broadcast or overlapping view)."""
+    token, head = strides
+    n, heads, dim = t.shape
+    lo, hi = sorted(((token, n), (head, heads)))
+    if t.numel() and not ((heads == 1 or head >= dim) and (n == 1 or token >= dim) and
+                          (n == 1 or heads == 1 or hi[0] >= (lo[1] - 1) * lo[0] + dim)):
+        raise ValueError(f"{name} has rows that overlap (strides {tuple(t.stride())})")
+
+
+def _kv_call(call, desc, pool, k, v, starts, lens, table, err_count, stream):
+    import torch
+    ks = _rows(k, f"{call}: k", desc.kv_heads, desc.head_dim)
+    vs = _rows(v, f"{call}: v", desc.kv_heads, desc.head_dim)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError(f"{call}: k and v must have one shape and dtype, got {tuple(k.shape)} {k.dtype} and "
+                         f"{tuple(v.shape)} {v.dtype}")
+    if call == "llvq_kv_read":
+        _apart(k, f"{call}: k", ks)
+        _apart(v, f"{call}: v", vs)
+    _tensor(pool, f"{call}: pool", (torch.uint8,), _pool_nbytes(desc))
+    _tensor(err_count, f"{call}: err_count", (torch.int32,), 4, nullable=True)
+    batch = _batch(starts, lens, table, k.shape[0], call)
+    _check(getattr(load_library(), call)(ctypes.byref(desc), _ptr(pool), _ptr(k), *ks, _ptr(v), *vs,
+                                         X_F32 if k.dtype == torch.float32 else X_BF16, ctypes.byref(batch),
+                                         _ptr(err_count), _stream(stream)), call)
+
+
+def kv_write(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
+    """Quantise the new tokens' keys and values [tokens][kv_heads][head_dim] (fp32 or bf16, any token and
+    head strides) into the pool: sequence b's rows are starts[b]..starts[b + 1] and the last of its
+    lens[b] cached tokens; table [B][max_pages] names its pages."""
+    _kv_call("llvq_kv_write", desc, pool, k, v, starts, lens, table, err_count, stream)
+
+
+def kv_read(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
+    """Read the same rows back into k and v (fp32 or bf16), as the values they stand for."""
+    _kv_call("llvq_kv_read", desc, pool, k, v, starts, lens, table, err_count, stream)
+
+
+def attn_workspace_bytes(desc, heads, tokens, batch, max_chunk, max_len) -> int:
+    n = load_library().llvq_attn_workspace_bytes(ctypes.byref(desc), heads, tokens, batch, max_chunk, max_len)
+    if n < 0:
+        raise LlvqError(int(n), "llvq_attn_workspace_bytes")
+    return n
+
+
+def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, scale=None, causal=True, window=0,
+         err_count=None, stream=None):
+    """out[i][h] = softmax(scale * q[i][h] . K) V over the cached tokens that new token i sees.
+    q and out: [tokens][heads][head_dim], fp32 or bf16; scale: 1 / sqrt(head_dim) if None; max_chunk: at least any
+    sequence's new tokens; max_len: about the longest length (decides only how the keys are split);
+    workspace: attn_workspace_bytes(...) bytes (None if that is 0)."""
+    import torch
+    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    if heads < 1 or heads % desc.kv_heads:
+        raise ValueError(f"llvq_attn: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
+    qs = _rows(q, "llvq_attn: q", heads, desc.head_dim)
+    os_ = _rows(out, "llvq_attn: out", heads, desc.head_dim)
+    if q.shape != out.shape or q.dtype != out.dtype:
+        raise ValueError(f"llvq_attn: q and out must have one shape and dtype, got {tuple(q.shape)} {q.dtype} and "
+                         f"{tuple(out.shape)} {out.dtype}")
+    _apart(out, "llvq_attn: out", os_)
+    _tensor(pool, "llvq_attn: pool", (torch.uint8,), _pool_nbytes(desc))
+    _tensor(err_count, "llvq_attn: err_count", (torch.int32,), 4, nullable=True)
+    batch = _batch(starts, lens, table, q.shape[0], "llvq_attn")
+    need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
+    _tensor(workspace, "llvq_attn: workspace", None, need, nullable=need == 0)
+    if scale is None:
+        scale = desc.head_dim ** -0.5
+    _check(load_library().llvq_attn(ctypes.byref(desc), _ptr(pool), _ptr(q), *qs, _ptr(out), *os_,
+                                    X_F32 if q.dtype == torch.float32 else X_BF16, heads, ctypes.byref(batch), max_chunk,
+                                    max_len, scale, int(bool(causal)), window, _ptr(workspace), _ptr(err_count),
+                                    _stream(stream)), "llvq_attn")
+
+
+def draft_workspace_bytes(batch, vocab) -> int:
+    n = load_library().llvq_draft_workspace_bytes(batch, vocab)
+    if n < 0:
+        raise LlvqError(int(n), "llvq_draft_workspace_bytes")
+    return n
+
+
+def draft_verify(target, draft, tokens, uniforms, noise, accepted, out, workspace, counts=None, err_count=None,
+                 stream=None):
+    """Check drafts tokens [B][S] against target [B][S + 1][V] (fp32 or bf16 probabilities; draft [B][S][V] or None for
+    certain drafts) with uniforms [B][S] and exponential noise [B][V]: accepted [B] and out [B][S + 1]
+    (accepted tokens, one drawn token, then -1), int32."""
+    import torch
+    _tensor(target, "llvq_draft_verify: target", (torch.float32, torch.bfloat16))
+    if target.dim() != 3 or target.shape[1] < 1:
+        raise ValueError(f"llvq_draft_verify: target must be [B][drafts + 1][vocab], got {tuple(target.shape)}")
+    b, s, v = target.shape[0], target.shape[1] - 1, target.shape[2]
+    _tensor(draft, "llvq_draft_verify: draft", (target.dtype,), nullable=True)
+    for t, name, dtype, shape in ((draft, "draft", target.dtype, (b, s, v)), (tokens, "tokens", torch.int32, (b, s)),
+                                  (uniforms, "uniforms", torch.float32, (b, s)), (noise, "noise", torch.float32, (b, v)),
+                                  (accepted, "accepted", torch.int32, (b,)), (out, "out", torch.int32, (b, s + 1)),
+                                  (counts, "counts", torch.int32, (b,))):
+        if t is None and name in ("draft", "counts"):
+            continue
+        _tensor(t, f"llvq_draft_verify: {name}", (dtype,))
+        if tuple(t.shape) != shape:
+            raise ValueError(f"llvq_draft_verify: {name} must be {list(shape)}, got {tuple(t.shape)}")
+    _tensor(workspace, "llvq_draft_verify: workspace", None, draft_workspace_bytes(b, v))
+    _tensor(err_count, "llvq_draft_verify: err_count", (torch.int32,), 4, nullable=True)
+    _check(load_library().llvq_draft_verify(_ptr(target), _ptr(draft), X_F32 if target.dtype == torch.float32 else X_BF16,
+                                            _ptr(tokens), _ptr(counts), _ptr(uniforms), _ptr(noise), b, s, v,
+                                            _ptr(accepted), _ptr(out), _ptr(workspace), _ptr(err_count),
+                                            _stream(stream)), "llvq_draft_verify")

@@ -5,7 +5,8 @@ Steps:
   2. run it to write the table header (and a JSON dump of the same tables), the
      generated device code of the nearest-point search, and the class records of the
      general decoder (shells beyond 10, fields beyond 64 bits; also dumped as JSON);
-  3. compile csrc/llvq.hip for gfx950 with hipcc into weight_decompression_amd/libllvq.so.
+  3. compile csrc/llvq.hip and csrc_serve/llvq_serve.hip for gfx950 with hipcc into
+     weight_decompression_amd/libllvq.so.
 
 Generated files go to <repo>/_build/ (not committed).  Packed-fp32 VALU instructions
 are switched off for all device code.
@@ -19,6 +20,7 @@ import sys
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
+CSRC_SERVE = os.path.join(PKG_DIR, "csrc_serve")
 INCLUDE = os.path.join(REPO_DIR, "include")
 BUILD_DIR = os.path.join(REPO_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libllvq.so")
@@ -89,6 +91,7 @@ def build(verbose=True, device_checks=False):
         "-I", BUILD_DIR,
         "-o", tmp,
         os.path.join(CSRC, "llvq.hip"),
+        os.path.join(CSRC_SERVE, "llvq_serve.hip"),
     ]
     if device_checks:
         cmd.insert(1, "-DLLVQ_DEVICE_CHECKS")

@@ -1,0 +1,296 @@
+// Host side of the serving calls of include/llvq.h: the paged key/value cache, the attention over it
+// and the check of drafted tokens.  Arguments are validated here, before any launch; kernels bound every
+// index that they read from device memory by what the host was told.
+#include <math.h>
+
+#include "attn.h"
+#include "draft.h"
+#include "kv_cache.h"
+#include "serve_common.h"
+
+#define LLVQ_API extern "C" __attribute__((visibility("default")))
+
+using namespace serve;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int launch_status() { return hipGetLastError() == hipSuccess ? LLVQ_OK : LLVQ_EHIP; }
+
+int64_t block_bytes(const llvq_kv_desc* d) {
+  const int64_t groups = d->kind == LLVQ_KV_BF16 ? 0 : d->head_dim / kGroup;
+  return (2 * d->page_tokens * (code_bytes(d->kind, d->head_dim) + groups) + 15) / 16 * 16;
+}
+
+int check_desc(const llvq_kv_desc* d) {
+  if (!d || d->kind < LLVQ_KV_BF16 || d->kind > LLVQ_KV_FP4) return LLVQ_EINVAL;
+  if (d->kv_heads < 1 || d->kv_heads > 1024 || d->pages < 1) return LLVQ_EINVAL;
+  if (d->head_dim < kGroup || d->head_dim > LLVQ_MAX_HEAD_DIM || d->head_dim % kGroup) return LLVQ_EINVAL;
+  if (d->page_tokens < 1 || d->page_tokens > LLVQ_MAX_PAGE) return LLVQ_EINVAL;
+  return LLVQ_OK;
+}
+
+int make_cache(const llvq_kv_desc* d, const void* pool, const llvq_batch* n, Cache* c) {
+  const int st = check_desc(d);
+  if (st != LLVQ_OK) return st;
+  if (!n || n->batch < 0 || n->batch > LLVQ_MAX_SEQS || n->tokens < 0 || n->max_pages < 0) return LLVQ_EINVAL;
+  if (n->batch > 0 && n->tokens > 0) {
+    if (!pool || !n->starts || !n->lens || (n->max_pages > 0 && !n->table)) return LLVQ_EINVAL;
+    if (!aligned(pool, 16) || !aligned(n->starts, 4) || !aligned(n->lens, 4) || !aligned(n->table, 4)) return LLVQ_EINVAL;
+  }
+  *c = Cache{};
+  c->pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  c->starts = n->starts;
+  c->lens = n->lens;
+  c->table = n->table;
+  c->block = block_bytes(d);
+  c->page = make_divider((uint32_t)d->page_tokens);
+  c->heads = d->kv_heads;
+  c->dim = d->head_dim;
+  c->pages = d->pages;
+  c->batch = n->batch;
+  c->max_pages = n->max_pages;
+  c->tokens = n->tokens;
+  c->row = code_bytes(d->kind, d->head_dim);
+  c->groups = d->kind == LLVQ_KV_BF16 ? 0 : d->head_dim / kGroup;
+  c->v_off = d->page_tokens * c->row;
+  c->ks_off = 2 * c->v_off;
+  c->vs_off = c->ks_off + d->page_tokens * c->groups;
+  return LLVQ_OK;
+}
+
+// Whether rows of `bytes`-wide elements can be moved 16 bytes at a time.
+bool wide(const void* p, int64_t token, int64_t head, int bytes) {
+  return aligned(p, 16) && (token * bytes) % 16 == 0 && (head * bytes) % 16 == 0;
+}
+
+template <int KIND, bool WRITE>
+int launch_kv(const Cache& c, const KvRows& r, bool f32, bool vec, int32_t* err, hipStream_t s) {
+  const int items = 2 * c.heads * (c.dim / 8);
+  // One token a wave while that leaves compute units idle, four after that
+  const int per_wave = c.tokens >= 16384 ? 4 : 1;
+  const unsigned gx = (unsigned)((c.tokens + 4ll * per_wave - 1) / (4ll * per_wave));
+  const unsigned parts = (unsigned)((items + kWave - 1) / kWave);
+  const unsigned gy = c.tokens >= 4096 ? (parts + 3) / 4 : parts;
+  const dim3 grid(gx, gy > 65535 ? 65535 : gy);
+#define LLVQ_KV_CASE(F32, VEC)                                                                              \
+  if (f32 == F32 && vec == VEC) {                                                                           \
+    if constexpr (WRITE)                                                                                    \
+      hipLaunchKernelGGL((k_kv_write<KIND, F32, VEC>), grid, dim3(256), 0, s, c, r, per_wave, items, err);  \
+    else                                                                                                    \
+      hipLaunchKernelGGL((k_kv_read<KIND, F32, VEC>), grid, dim3(256), 0, s, c, r, per_wave, items, err);   \
+  }
+  LLVQ_KV_CASE(false, false) LLVQ_KV_CASE(false, true) LLVQ_KV_CASE(true, false) LLVQ_KV_CASE(true, true)
+#undef LLVQ_KV_CASE
+  return launch_status();
+}
+
+template <bool WRITE>
+int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_token, int64_t k_head, const void* v,
+            int64_t v_token, int64_t v_head, int32_t dtype, const llvq_batch* n, int32_t* err, void* stream) {
+  Cache c;
+  const int st = make_cache(d, pool, n, &c);
+  if (st != LLVQ_OK) return st;
+  if (dtype != LLVQ_X_F32 && dtype != LLVQ_X_BF16) return LLVQ_EINVAL;
+  if (err && !aligned(err, 4)) return LLVQ_EINVAL;
+  if (c.tokens == 0 || c.batch == 0) return LLVQ_OK;
+  const bool f32 = dtype == LLVQ_X_F32;
+  const int size = f32 ? 4 : 2;
+  if (!k || !v || !aligned(k, size) || !aligned(v, size)) return LLVQ_EINVAL;
+  if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0) return LLVQ_EINVAL;
+  const bool vec = wide(k, k_token, k_head, size) && wide(v, v_token, v_head, size);
+  const KvRows r = {k, v, k_token, k_head, v_token, v_head};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (d->kind) {
+    case LLVQ_KV_BF16: return launch_kv<LLVQ_KV_BF16, WRITE>(c, r, f32, vec, err, s);
+    case LLVQ_KV_FP8: return launch_kv<LLVQ_KV_FP8, WRITE>(c, r, f32, vec, err, s);
+    default: return launch_kv<LLVQ_KV_FP4, WRITE>(c, r, f32, vec, err, s);
+  }
+}
+
+// How a call is cut up: waves that share out a tile's keys, row blocks and splits of the keys.
+struct Cut {
+  int wk, row_blocks, splits;
+};
+
+int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, Cut* cut) {
+  const int64_t rows = (int64_t)max_chunk * share;
+  cut->wk = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  const int64_t per = 32 * (4 / cut->wk);
+  const int64_t blocks = (rows + per - 1) / per;
+  const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
+  if (base > (1ll << 30)) return LLVQ_EINVAL;
+  const int64_t want = (1024 + base - 1) / base;
+  const int64_t most = ((int64_t)max_len + 511) / 512;
+  int64_t s = want < most ? want : most;
+  cut->splits = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+  cut->row_blocks = (int)blocks;
+  return base * cut->splits > 0x7fffffff ? LLVQ_EINVAL : LLVQ_OK;
+}
+
+int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch, int32_t max_chunk, int32_t max_len) {
+  const int st = check_desc(d);
+  if (st != LLVQ_OK) return st;
+  if (heads < d->kv_heads || heads % d->kv_heads || heads > 65536) return LLVQ_EINVAL;
+  if (tokens < 0 || tokens * heads > 0x7fffffff || batch < 0 || batch > LLVQ_MAX_SEQS) return LLVQ_EINVAL;
+  if (max_chunk < 1 || max_len < 1 || max_len > kMaxLen || (int64_t)max_chunk * heads > 0x7fffffff) return LLVQ_EINVAL;
+  return LLVQ_OK;
+}
+
+template <int KIND, int DP, int NT, int WK>
+int launch_attn(const AttnArgs& a, unsigned grid, hipStream_t s) {
+  hipLaunchKernelGGL((k_attn<KIND, DP, NT, WK>), dim3(grid), dim3(256), 0, s, a);
+  return launch_status();
+}
+template <int KIND, int DP, int NT>
+int launch_attn_wk(const AttnArgs& a, int wk, unsigned grid, hipStream_t s) {
+  return wk == 4 ? launch_attn<KIND, DP, NT, 4>(a, grid, s) : wk == 2 ? launch_attn<KIND, DP, NT, 2>(a, grid, s)
+                                                                      : launch_attn<KIND, DP, NT, 1>(a, grid, s);
+}
+template <int KIND, int DP>
+int launch_attn_nt(const AttnArgs& a, bool f32, int wk, unsigned grid, hipStream_t s) {
+  return f32 ? launch_attn_wk<KIND, DP, 3>(a, wk, grid, s) : launch_attn_wk<KIND, DP, 1>(a, wk, grid, s);
+}
+template <int KIND>
+int launch_attn_dp(const AttnArgs& a, bool f32, int wk, unsigned grid, hipStream_t s) {
+  return a.c.dim <= 64    ? launch_attn_nt<KIND, 64>(a, f32, wk, grid, s)
+         : a.c.dim <= 128 ? launch_attn_nt<KIND, 128>(a, f32, wk, grid, s)
+                          : launch_attn_nt<KIND, 256>(a, f32, wk, grid, s);
+}
+
+int draft_parts(int32_t batch, int32_t vocab) {
+  // about 1024 workgroups in all, each of at least 2048 entries
+  const int64_t most = ((int64_t)vocab + 2047) / 2048, want = (1024 + (batch > 0 ? batch : 1) - 1) / (batch > 0 ? batch : 1);
+  return (int)(want < most ? want : most);
+}
+
+}  // namespace
+
+LLVQ_API int64_t llvq_kv_pool_bytes(const llvq_kv_desc* d) {
+  const int st = check_desc(d);
+  return st != LLVQ_OK ? st : (int64_t)d->pages * d->kv_heads * block_bytes(d);
+}
+
+LLVQ_API int llvq_kv_write(const llvq_kv_desc* d, void* pool, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                           int64_t v_token, int64_t v_head, int32_t dtype, const llvq_batch* batch, int32_t* err_count,
+                           void* stream) {
+  return kv_call<true>(d, pool, k, k_token, k_head, v, v_token, v_head, dtype, batch, err_count, stream);
+}
+
+LLVQ_API int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_token, int64_t k_head, void* v,
+                          int64_t v_token, int64_t v_head, int32_t dtype, const llvq_batch* batch, int32_t* err_count,
+                          void* stream) {
+  return kv_call<false>(d, pool, k, k_token, k_head, v, v_token, v_head, dtype, batch, err_count, stream);
+}
+
+LLVQ_API int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch,
+                                           int32_t max_chunk, int32_t max_len) {
+  int st = check_attn(d, heads, tokens, batch, max_chunk, max_len);
+  if (st != LLVQ_OK) return st;
+  Cut cut;
+  st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, &cut);
+  if (st != LLVQ_OK) return st;
+  return cut.splits == 1 ? 0 : (int64_t)cut.splits * tokens * heads * (d->head_dim + 2) * 4;
+}
+
+LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
+                       int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
+                       int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,
+                       int32_t* err_count, void* stream) {
+  Cache c;
+  int st = make_cache(d, pool, batch, &c);
+  if (st != LLVQ_OK) return st;
+  st = check_attn(d, heads, batch->tokens, batch->batch, max_chunk, max_len);
+  if (st != LLVQ_OK) return st;
+  if (dtype != LLVQ_X_F32 && dtype != LLVQ_X_BF16) return LLVQ_EINVAL;
+  if (!(scale > 0.0f) || !(scale < INFINITY) || window < 0 || window > kMaxLen) return LLVQ_EINVAL;
+  if (err_count && !aligned(err_count, 4)) return LLVQ_EINVAL;
+  if (c.tokens == 0 || c.batch == 0) return LLVQ_OK;
+  const bool f32 = dtype == LLVQ_X_F32;
+  const int size = f32 ? 4 : 2;
+  if (!q || !out || !aligned(q, size) || !aligned(out, 4 * size)) return LLVQ_EINVAL;
+  if (q_token < 0 || q_head < 0 || out_token < 0 || out_head < 0 || out_token % 4 || out_head % 4) return LLVQ_EINVAL;
+  Cut cut;
+  st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, &cut);
+  if (st != LLVQ_OK) return st;
+  if (cut.splits > 1 && (!workspace || !aligned(workspace, 16))) return LLVQ_EINVAL;
+  AttnArgs a = {};
+  a.c = c;
+  a.q = q;
+  a.out = out;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.out_token = out_token;
+  a.out_head = out_head;
+  a.share = make_divider((uint32_t)(heads / d->kv_heads));
+  a.row_blocks = cut.row_blocks;
+  a.splits = cut.splits;
+  a.window = window;
+  a.causal = causal != 0;
+  a.q_vec = wide(q, q_token, q_head, size);
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.err = err_count;
+  if (cut.splits > 1) {
+    a.part = static_cast<float*>(workspace);
+    a.stats = a.part + (int64_t)cut.splits * c.tokens * heads * c.dim;
+  }
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const unsigned grid = (unsigned)((int64_t)c.batch * cut.row_blocks * cut.splits * c.heads);
+  switch (d->kind) {
+    case LLVQ_KV_BF16: st = launch_attn_dp<LLVQ_KV_BF16>(a, f32, cut.wk, grid, s); break;
+    case LLVQ_KV_FP8: st = launch_attn_dp<LLVQ_KV_FP8>(a, f32, cut.wk, grid, s); break;
+    default: st = launch_attn_dp<LLVQ_KV_FP4>(a, f32, cut.wk, grid, s); break;
+  }
+  if (st != LLVQ_OK || cut.splits == 1) return st;
+  const unsigned joins = (unsigned)(((int64_t)c.tokens * heads + 3) / 4);
+  if (f32)
+    hipLaunchKernelGGL((k_attn_join<true>), dim3(joins), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_attn_join<false>), dim3(joins), dim3(256), 0, s, a);
+  return launch_status();
+}
+
+LLVQ_API int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab) {
+  if (batch < 0 || batch > LLVQ_MAX_SEQS || vocab < 1) return LLVQ_EINVAL;
+  return (int64_t)batch * draft_parts(batch, vocab) * 16;
+}
+
+LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
+                               const int32_t* counts, const float* uniforms, const float* noise, int32_t batch,
+                               int32_t drafts, int32_t vocab, int32_t* accepted, int32_t* out, void* workspace,
+                               int32_t* err_count, void* stream) {
+  if (batch < 0 || batch > LLVQ_MAX_SEQS || drafts < 0 || drafts >= kMaxDrafts || vocab < 1) return LLVQ_EINVAL;
+  if (dtype != LLVQ_X_F32 && dtype != LLVQ_X_BF16) return LLVQ_EINVAL;
+  if (err_count && !aligned(err_count, 4)) return LLVQ_EINVAL;
+  if (batch == 0) return LLVQ_OK;
+  const int size = dtype == LLVQ_X_F32 ? 4 : 2;
+  if (!target || !noise || !accepted || !out || !workspace || (drafts > 0 && (!tokens || !uniforms))) return LLVQ_EINVAL;
+  if (!aligned(target, size) || !aligned(draft, size) || !aligned(tokens, 4) || !aligned(counts, 4) || !aligned(uniforms, 4) ||
+      !aligned(noise, 4) || !aligned(accepted, 4) || !aligned(out, 4) || !aligned(workspace, 8))
+    return LLVQ_EINVAL;
+  DraftArgs a = {};
+  a.target = target;
+  a.draft = draft;
+  a.tokens = tokens;
+  a.counts = counts;
+  a.uniforms = uniforms;
+  a.noise = noise;
+  a.keys = static_cast<uint64_t*>(workspace);
+  a.accepted = accepted;
+  a.out = out;
+  a.err = err_count;
+  a.batch = batch;
+  a.drafts = drafts;
+  a.vocab = vocab;
+  a.parts = draft_parts(batch, vocab);
+  a.per = (vocab + a.parts - 1) / a.parts;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == LLVQ_X_F32) {
+    hipLaunchKernelGGL((k_draft_part<true>), dim3(a.parts, batch), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_draft_pick<true>), dim3(batch), dim3(64), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_draft_part<false>), dim3(a.parts, batch), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_draft_pick<false>), dim3(batch), dim3(64), 0, s, a);
+  }
+  return launch_status();
+}
