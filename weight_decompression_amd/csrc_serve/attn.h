@@ -123,6 +123,450 @@ __device__ __forceinline__ bool drop_nonfinite(u32x4* w) {
   return true;
 }
 
+// The sum of a lane's eight p.  bf16 queries: of the rounded values, two at a time, so that what all of a
+// row's roundings have in common cancels.
+template <int NT>
+__device__ __forceinline__ float sum_p(const float* x, const bf16x8& rounded, float l) {
+  if constexpr (NT == 1) {
+    const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{rounded[2 * e], rounded[2 * e + 1]}, one, l, false);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) l += x[e];
+  }
+  return l;
+}
+
+// Four channels of a cached value where they are not finite, zero where they are.
+template <int KIND>
+__device__ __forceinline__ f32x4 nonfinite4(const Cache& c, const uint8_t* blk, int slot, int ch) {
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (ch >= c.dim) return x;
+  if constexpr (KIND == LLVQ_KV_BF16) {
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(blk + c.v_off + slot * c.row) + ch;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((v[i] & 0x7f80u) == 0x7f80u) x[i] = bf16_f32(v[i]);
+  } else if (blk[c.vs_off + slot * c.groups + ch / kGroup] == 255) {
+    x = f32x4{NAN, NAN, NAN, NAN};
+  }
+  return x;
+}
+
+// The keys of a workgroup: [first_key, last_key), those that every row of it sees, and its share of the
+// tiles of `keys` keys (tile indices from key 0).
+struct Span {
+  int first_key, last_key, all_lo, all_hi, tile_lo, tile_hi;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int row0, int block_rows, int keys, int split) {
+  const int rows = s.n * (int)a.share.by;
+  const int t0 = (int)divide((uint32_t)row0, a.share);
+  const int t1 = (int)divide((uint32_t)(min(row0 + block_rows, rows) - 1), a.share);
+  const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
+  Span w;
+  w.last_key = a.causal ? min(max(p1 + 1, 0), s.len) : s.len;
+  w.first_key = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+  w.all_hi = a.causal ? p0 + 1 : s.len;
+  w.all_lo = a.window > 0 ? max(p1 - a.window + 1, 0) : 0;
+  const int tile0 = w.first_key / keys;
+  const int tiles = w.last_key > w.first_key ? (w.last_key + keys - 1) / keys - tile0 : 0;
+  const int per = (tiles + a.splits - 1) / a.splits;
+  w.tile_lo = tile0 + min(split * per, tiles);
+  w.tile_hi = min(w.tile_lo + per, tile0 + tiles);
+  return w;
+}
+
+// The keys that token t sees: [lo, lo + seen).
+__device__ __forceinline__ void seen_of(const AttnArgs& a, const Seq& s, int t, bool live, int* lo, int* seen) {
+  const int pos = s.len - s.n + t;
+  const int hi = a.causal ? min(max(pos + 1, 0), s.len) : s.len;
+  *lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+  *seen = live ? max(hi - *lo, 0) : 0;
+}
+
+// 8 channels of a query row as NT bf16 terms.
+template <int NT>
+__device__ __forceinline__ void load_query(const AttnArgs& a, int64_t at, int ch, bool live, bf16x8* terms) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  if (live && ch < a.c.dim) {
+    if (a.q_vec)
+      load8<NT == 3, true>(a.q, at + ch, x);
+    else
+      load8<NT == 3, false>(a.q, at + ch, x);
+  }
+  split_terms<NT>(x, terms);
+}
+
+// Four channels of one row: to the workspace if the keys are split (unnormalised), else to the output.
+template <int NT>
+__device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t row, int64_t out_at, int split, int ch, f32x4 x, float inv) {
+  const Cache& c = a.c;
+  if (ch >= c.dim) return;
+  if (a.splits > 1) {
+    const int64_t rows = (int64_t)c.tokens * c.heads * a.share.by;
+    *reinterpret_cast<f32x4*>(a.part + (split * rows + row) * c.dim + ch) = x;
+  } else if constexpr (NT == 1) {
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + out_at + ch) =
+        u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + out_at + ch) = x * inv;
+  }
+}
+
+// Scores of keys that a row does not see do not count.
+__device__ __forceinline__ float masked(float s, int j, int lo, int seen) {
+  return (uint32_t)(j - lo) < (uint32_t)seen ? s : -INFINITY;
+}
+
+// Few rows: up to 64 rows of a (sequence, key head), in CT tiles of 16 columns.
+//
+// A decode step reads each cached byte for a handful of rows, so HBM bounds it and what counts is loads
+// in flight.  Every wave therefore runs by itself: it takes every fourth 32-key piece of the workgroup's
+// share, stages it in its own 64 * DP bytes of LDS (the keys, then the values in the same place) and waits for
+// nothing but its own loads, which are issued a piece ahead (page numbers two pieces ahead).  With 16x16x32
+// instructions a lane holds 8 scores of a piece, and a tile of outputs takes DP / 4 registers of a lane.
+// In S^T's layout a lane (column lane % 16, g = lane / 16) holds keys 4 g + i and 16 + 4 g + i, which are
+// taken as the eight consecutive keys of its place in the second product; the transposing load reads
+// V's rows in the same order.
+// Rows in LDS are padded, so that every address is one register and a constant: by 16 bytes for the keys
+// (16 rows at one 16-byte chunk fall on 16 different slots of 256 bytes), by 32 for the values (the eight
+// rows that half a wave takes at 32 bytes of channels fall on eight different segments).
+template <int DP>
+struct FewLds {
+  static constexpr int kKeyRow = DP * 2 + 16, kValueRow = DP * 2 + 32;
+  static constexpr int kWaveBytes = 32 * kValueRow;
+};
+
+__device__ __forceinline__ float quad_max(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// LDS that only one wave uses: its operations complete in order, so it is enough that the compiler
+// keeps them in order.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Waves a SIMD that k_attn_few is compiled for: 512 registers over what it holds (queries, outputs, a piece
+// in flight and what goes with it).
+constexpr int few_waves(int kind, int dp, int nt, int ct) {
+  const int held = nt * ct * (dp / 8 + 4) + ct * (dp / 4 + 15) + code_bytes(kind, dp) / 32 * 14 + 36;
+  return held <= 128 ? 4 : held <= 168 ? 3 : held <= 256 ? 2 : 1;
+}
+// Two column tiles share a staged piece where two waves a SIMD still fit.
+constexpr bool few_pairs(int kind, int dp, int nt) { return few_waves(kind, dp, nt, 2) >= 2; }
+
+template <int KIND, int DP, int NT, int CT>
+__global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
+  constexpr int kRaw = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
+  constexpr int kLoads = 32 * kRaw / kWave;        // chunks a lane loads of a piece
+  constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
+  constexpr int kSteps = DP / 32, kOut = DP / 16;
+  constexpr int32_t kNoKey = INT32_MIN;
+  const Cache& c = a.c;
+  using Lds = FewLds<DP>;
+  __shared__ __align__(16) uint8_t lds[4 * Lds::kWaveBytes];
+  __shared__ float wave_m[4][16], wave_l[4][16];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  uint8_t* mine = lds + wave * Lds::kWaveBytes;
+
+  int id = blockIdx.x;
+  const int head = id % c.heads;
+  id /= c.heads;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int rb = id % a.row_blocks;
+  const int b = id / a.row_blocks;
+  const Seq s = sequence(c, b);
+  const int share = (int)a.share.by, rows = s.n * share;
+  if (a.err && tid == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * 16 * CT)) atomicAdd(a.err, 1);
+  const int row0 = rb * 16 * CT;
+  if (row0 >= rows) return;
+  const Span w = span_of(a, s, row0, 16 * CT, 128, split);
+
+  int lo[CT], seen[CT], t[CT], qhead[CT];
+  bool live[CT];
+  bf16x8 q[NT][CT][kSteps];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int row = row0 + ct * 16 + col;
+    live[ct] = row < rows;
+    t[ct] = live[ct] ? (int)divide((uint32_t)row, a.share) : 0;
+    qhead[ct] = head * share + (live[ct] ? row - t[ct] * share : 0);
+    seen_of(a, s, t[ct], live[ct], &lo[ct], &seen[ct]);
+    const int64_t at = (int64_t)(s.first + t[ct]) * a.q_token + (int64_t)qhead[ct] * a.q_head;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      bf16x8 terms[NT];
+      load_query<NT>(a, at, st * 32 + g * 8, live[ct], terms);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) q[n][ct][st] = terms[n];
+    }
+  }
+
+  f32x4 acc[CT][kOut];
+  float m[CT], l[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    m[ct] = -INFINITY;
+    l[ct] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) acc[ct][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
+  const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  const int ch = lane % kRaw;  // this lane's chunk of every row that it loads
+  const bool in_row = ch * 16 < c.row;
+  bool lost = false;
+  // the page number of this lane's key of a piece (lanes 32..63 as 0..31)
+  auto page_of = [&](int tile) -> int32_t {
+    const int j = (tile * 4 + wave) * 32 + (lane & 31);
+    if (tile >= w.tile_hi || j < w.first_key || j >= w.last_key) return kNoKey;
+    return table[divide((uint32_t)j, c.page)];
+  };
+  // codes and scale bytes of a piece: row i of a lane is key (i * 64 + lane) / kRaw
+  int64_t base[kLoads];
+  int slot[kLoads];
+  bool ok[kLoads];
+  u32x4 raw[2][kLoads];
+  uint32_t sc[2][kLoads];
+  auto locate = [&](int tile, int32_t ids) {
+    lost |= ids >= c.pages || (ids < 0 && ids != kNoKey);
+    const uint32_t j = (uint32_t)((tile * 4 + wave) * 32 + (lane & 31));
+    const int my_slot = (int)(j - divide(j, c.page) * c.page.by);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int key = (i * kWave + lane) / kRaw;
+      const int32_t page = __shfl(ids, key);
+      slot[i] = __shfl(my_slot, key);
+      ok[i] = page >= 0 && page < c.pages && in_row;
+      // a place that is not there is read from the pool's start and left out when it is staged
+      if (!ok[i]) slot[i] = 0;
+      base[i] = ok[i] ? (int64_t)page * page_bytes + head_off : 0;
+    }
+  };
+  auto fetch = [&](int is_v) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint8_t* blk = c.pool + base[i];
+      raw[is_v][i] = *reinterpret_cast<const u32x4*>(blk + (is_v ? c.v_off : 0) + slot[i] * c.row + (ok[i] ? ch * 16 : 0));
+      if constexpr (KIND != LLVQ_KV_BF16)
+        sc[is_v][i] = blk[(is_v ? c.vs_off : c.ks_off) + slot[i] * c.groups + (ok[i] ? ch * kOf / 4 : 0)];
+      else
+        sc[is_v][i] = 127;
+    }
+  };
+  bool part_k = false, part_v = false;  // whether a place of the loaded piece is not there
+
+  int32_t ids = page_of(w.tile_lo);
+  bool there_k[kLoads], there_v[kLoads];
+  auto note = [&](bool* there, bool* part) {
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      there[i] = ok[i];
+      all &= ok[i];
+    }
+    *part = !__all(all);
+  };
+  if (w.tile_lo < w.tile_hi) {
+    locate(w.tile_lo, ids);
+    note(there_k, &part_k);
+    note(there_v, &part_v);
+    fetch(0);
+    fetch(1);
+    ids = page_of(w.tile_lo + 1);
+  }
+  for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
+    const int key_base = (tile * 4 + wave) * 32;
+    const bool more = tile + 1 < w.tile_hi;
+    // the keys
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int key = (i * kWave + lane) / kRaw;
+      u32x4 r = raw[0][i];
+      uint32_t sb = sc[0][i];
+      if (part_k && !there_k[i]) r = u32x4{0, 0, 0, 0}, sb = 127;
+      u32x4 o[kOf];
+      expand<KIND>(r, sb, o);
+#pragma unroll
+      for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(mine + key * Lds::kKeyRow + (ch * kOf + n) * 16) = o[n];
+    }
+    wave_order();
+    if (more) {
+      locate(tile + 1, ids);
+      ids = page_of(tile + 2);
+      note(there_k, &part_k);
+      fetch(0);
+    }
+    f32x4 score[CT][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) score[ct][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(mine + (u * 16 + col) * Lds::kKeyRow + (st * 4 + g) * 16);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int n = NT - 1; n >= 0; --n) score[ct][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][ct][st], score[ct][u], 0, 0, 0);
+      }
+    }
+    const bool whole = key_base >= w.all_lo && key_base + 32 <= w.all_hi && key_base + 32 <= s.len;
+    bf16x8 p[NT][CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      if (!whole) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) score[ct][u][i] = masked(score[ct][u][i], key_base + u * 16 + 4 * g + i, lo[ct], seen[ct]);
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, score[ct][i / 4][i & 3]);
+      top = quad_max(top) * a.scale_log2;
+      if (__any(top > m[ct] + kRescaleStep)) {
+        const float next = fmaxf(m[ct], top);
+        const float f = m[ct] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[ct] - next);
+        m[ct] = next;
+        l[ct] *= f;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) acc[ct][d] *= f;
+      }
+      const float ms = m[ct] == -INFINITY ? 0.0f : m[ct];
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(score[ct][i / 4][i & 3], a.scale_log2, -ms));
+      bf16x8 terms[NT];
+      split_terms<NT>(x, terms);
+      l[ct] = sum_p<NT>(x, terms[0], l[ct]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) p[n][ct] = terms[n];
+    }
+    // the values, in the keys' place
+    uint32_t bad = 0;
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int key = (i * kWave + lane) / kRaw;
+      u32x4 r = raw[1][i];
+      uint32_t sb = sc[1][i];
+      if (part_v && !there_v[i]) r = u32x4{0, 0, 0, 0}, sb = 127;
+      u32x4 o[kOf];
+      bool spoilt;
+      if constexpr (KIND == LLVQ_KV_BF16) {
+        spoilt = drop_nonfinite(&r);
+      } else {
+        spoilt = sb == 255;
+        if (spoilt) r = u32x4{0, 0, 0, 0}, sb = 127;
+      }
+      if (spoilt) bad |= 1u << key;
+      expand<KIND>(r, sb, o);
+#pragma unroll
+      for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(mine + key * Lds::kValueRow + (ch * kOf + n) * 16) = o[n];
+    }
+    wave_order();
+    if (more) {
+      note(there_v, &part_v);
+      fetch(1);
+    }
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) {
+      const uint8_t* at = mine + (4 * g + ((lane & 15) >> 2)) * Lds::kValueRow + d * 32 + (lane & 3) * 8;
+      union {
+        s16x4 h[2];
+        bf16x8 v;
+      } vf;
+      vf.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+      vf.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 16 * Lds::kValueRow));
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n) acc[ct][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf.v, p[n][ct], acc[ct][d], 0, 0, 0);
+    }
+    // values that are not finite were left out (0 * NaN would spoil rows that do not see them) and are
+    // added to the rows that do
+    if (__any(bad != 0)) {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) bad |= (uint32_t)__shfl_xor((int)bad, d);
+      while (bad) {
+        const int key = __builtin_ctz(bad), j = key_base + key;
+        bad &= bad - 1;
+        const uint32_t page = divide((uint32_t)j, c.page);
+        const int at = j - (int)(page * c.page.by);
+        const uint8_t* blk = c.pool + (int64_t)table[page] * page_bytes + head_off;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) {
+          const f32x4 x = nonfinite4<KIND>(c, blk, at, d * 16 + 4 * g);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            if ((uint32_t)(j - lo[ct]) < (uint32_t)seen[ct]) acc[ct][d] += x;
+        }
+      }
+    }
+  }
+  if (a.err && lost) atomicAdd(a.err, 1);
+
+  // the four waves' parts are joined through LDS under their common maximum and added in the waves' order
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    l[ct] = quad_sum(l[ct]);
+    __syncthreads();
+    if (g == 0) wave_m[wave][col] = m[ct];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, wave_m[i][col]);
+    const float f = m[ct] == -INFINITY ? (l[ct] == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(m[ct] - top);
+    if (g == 0) wave_l[wave][col] = l[ct] * f;
+    float* sums = reinterpret_cast<float*>(lds);  // [wave][16 columns][DP], quads of channels swizzled by the column
+#pragma unroll
+    for (int d = 0; d < kOut; ++d)
+      *reinterpret_cast<f32x4*>(sums + (wave * 16 + col) * DP + (((d * 4 + g) ^ (col & 7)) << 2)) = acc[ct][d] * f;
+    __syncthreads();
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total += wave_l[i][col];
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // no visible key: the row is zero
+    if (live[ct]) {
+      const int64_t row = (int64_t)(s.first + t[ct]) * c.heads * share + qhead[ct];
+      const int64_t out_at = (int64_t)(s.first + t[ct]) * a.out_token + (int64_t)qhead[ct] * a.out_head;
+      if (a.splits > 1 && wave == 0 && g == 0) {
+        const int64_t all = (int64_t)c.tokens * c.heads * share;
+        a.stats[(split * all + row) * 2] = top;
+        a.stats[(split * all + row) * 2 + 1] = total;
+      }
+      if (a.splits == 1 || w.tile_lo < w.tile_hi) {
+#pragma unroll
+        for (int d4 = 0; d4 < kOut / 4; ++d4) {
+          const int d = d4 * 4 + wave;  // each wave writes a quarter of the channels
+          f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x += *reinterpret_cast<const f32x4*>(sums + (i * 16 + col) * DP + (((d * 4 + g) ^ (col & 7)) << 2));
+          store_row4<NT>(a, row, out_at, split, d * 16 + g * 4, x, inv);
+        }
+      }
+    }
+  }
+}
+
+// Many rows: the tiles are shared by the workgroup's four waves, each with 32 columns of its own.
 template <int KIND, int DP, int NT, int WK>
 struct AttnShape {
   static constexpr int kWaveCols = 4 / WK;

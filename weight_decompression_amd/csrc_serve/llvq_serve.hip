@@ -108,19 +108,22 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
   }
 }
 
-// How a call is cut up: waves that share out a tile's keys, row blocks and splits of the keys.
+// How a call is cut up: columns of 16 a workgroup of the kernel for few rows holds (0: the kernel for many
+// rows), row blocks and splits of the keys.
 struct Cut {
-  int wk, row_blocks, splits;
+  int cols, row_blocks, splits;
 };
 
-int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, Cut* cut) {
+int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, bool f32, Cut* cut) {
   const int64_t rows = (int64_t)max_chunk * share;
-  cut->wk = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-  const int64_t per = 32 * (4 / cut->wk);
+  cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1) ? 1 : 2;
+  const int64_t per = cut->cols ? 16 * cut->cols : 128;
   const int64_t blocks = (rows + per - 1) / per;
   const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
   if (base > (1ll << 30)) return LLVQ_EINVAL;
-  const int64_t want = (1024 + base - 1) / base;
+  const int64_t want = ((cut->cols ? 2048 : 1024) + base - 1) / base;
   const int64_t most = ((int64_t)max_len + 511) / 512;
   int64_t s = want < most ? want : most;
   cut->splits = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
@@ -137,25 +140,27 @@ int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t bat
   return LLVQ_OK;
 }
 
-template <int KIND, int DP, int NT, int WK>
-int launch_attn(const AttnArgs& a, unsigned grid, hipStream_t s) {
-  hipLaunchKernelGGL((k_attn<KIND, DP, NT, WK>), dim3(grid), dim3(256), 0, s, a);
+template <int KIND, int DP, int NT>
+int launch_attn(const AttnArgs& a, int cols, unsigned grid, hipStream_t s) {
+  if (cols == 1)
+    hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
+  else if (cols == 0)
+    hipLaunchKernelGGL((k_attn<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
+  else if constexpr (few_pairs(KIND, DP, NT))
+    hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 2>), dim3(grid), dim3(256), 0, s, a);
   return launch_status();
 }
-template <int KIND, int DP, int NT>
-int launch_attn_wk(const AttnArgs& a, int wk, unsigned grid, hipStream_t s) {
-  return wk == 4 ? launch_attn<KIND, DP, NT, 4>(a, grid, s) : wk == 2 ? launch_attn<KIND, DP, NT, 2>(a, grid, s)
-                                                                      : launch_attn<KIND, DP, NT, 1>(a, grid, s);
-}
 template <int KIND, int DP>
-int launch_attn_nt(const AttnArgs& a, bool f32, int wk, unsigned grid, hipStream_t s) {
-  return f32 ? launch_attn_wk<KIND, DP, 3>(a, wk, grid, s) : launch_attn_wk<KIND, DP, 1>(a, wk, grid, s);
+int launch_attn_nt(const AttnArgs& a, bool f32, int cols, unsigned grid, hipStream_t s) {
+  return f32 ? launch_attn<KIND, DP, 3>(a, cols, grid, s) : launch_attn<KIND, DP, 1>(a, cols, grid, s);
 }
 template <int KIND>
-int launch_attn_dp(const AttnArgs& a, bool f32, int wk, unsigned grid, hipStream_t s) {
-  return a.c.dim <= 64    ? launch_attn_nt<KIND, 64>(a, f32, wk, grid, s)
-         : a.c.dim <= 128 ? launch_attn_nt<KIND, 128>(a, f32, wk, grid, s)
-                          : launch_attn_nt<KIND, 256>(a, f32, wk, grid, s);
+int launch_attn_dp(const AttnArgs& a, bool f32, int cols, unsigned grid, hipStream_t s) {
+  switch (padded_dim(a.c.dim)) {
+    case 64: return launch_attn_nt<KIND, 64>(a, f32, cols, grid, s);
+    case 128: return launch_attn_nt<KIND, 128>(a, f32, cols, grid, s);
+    default: return launch_attn_nt<KIND, 256>(a, f32, cols, grid, s);
+  }
 }
 
 int draft_parts(int32_t batch, int32_t vocab) {
@@ -187,10 +192,14 @@ LLVQ_API int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads,
                                            int32_t max_chunk, int32_t max_len) {
   int st = check_attn(d, heads, tokens, batch, max_chunk, max_len);
   if (st != LLVQ_OK) return st;
-  Cut cut;
-  st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, &cut);
-  if (st != LLVQ_OK) return st;
-  return cut.splits == 1 ? 0 : (int64_t)cut.splits * tokens * heads * (d->head_dim + 2) * 4;
+  int splits = 1;
+  for (const bool f32 : {false, true}) {  // either type of query
+    Cut cut;
+    st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, f32, &cut);
+    if (st != LLVQ_OK) return st;
+    if (cut.splits > splits) splits = cut.splits;
+  }
+  return splits == 1 ? 0 : (int64_t)splits * tokens * heads * (d->head_dim + 2) * 4;
 }
 
 LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
@@ -211,7 +220,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   if (!q || !out || !aligned(q, size) || !aligned(out, 4 * size)) return LLVQ_EINVAL;
   if (q_token < 0 || q_head < 0 || out_token < 0 || out_head < 0 || out_token % 4 || out_head % 4) return LLVQ_EINVAL;
   Cut cut;
-  st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, &cut);
+  st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, f32, &cut);
   if (st != LLVQ_OK) return st;
   if (cut.splits > 1 && (!workspace || !aligned(workspace, 16))) return LLVQ_EINVAL;
   AttnArgs a = {};
@@ -237,9 +246,9 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const unsigned grid = (unsigned)((int64_t)c.batch * cut.row_blocks * cut.splits * c.heads);
   switch (d->kind) {
-    case LLVQ_KV_BF16: st = launch_attn_dp<LLVQ_KV_BF16>(a, f32, cut.wk, grid, s); break;
-    case LLVQ_KV_FP8: st = launch_attn_dp<LLVQ_KV_FP8>(a, f32, cut.wk, grid, s); break;
-    default: st = launch_attn_dp<LLVQ_KV_FP4>(a, f32, cut.wk, grid, s); break;
+    case LLVQ_KV_BF16: st = launch_attn_dp<LLVQ_KV_BF16>(a, f32, cut.cols, grid, s); break;
+    case LLVQ_KV_FP8: st = launch_attn_dp<LLVQ_KV_FP8>(a, f32, cut.cols, grid, s); break;
+    default: st = launch_attn_dp<LLVQ_KV_FP4>(a, f32, cut.cols, grid, s); break;
   }
   if (st != LLVQ_OK || cut.splits == 1) return st;
   const unsigned joins = (unsigned)(((int64_t)c.tokens * heads + 3) / 4);
