@@ -81,6 +81,8 @@ def load_library(path=LIB_PATH):
     library must bind to the same runtime as the streams and device pointers it is
     handed (loaded first, it would bind to the system runtime and every launch on a
     torch stream would fail)."""
+    if path in _libs:
+        return _libs[path]
     path = os.path.abspath(path)
     if path in _libs:
         return _libs[path]
@@ -163,6 +165,15 @@ def _stream(stream):
         return ctypes.c_void_p(stream)
     import torch
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _raw_stream(stream, device):
+    """The handle of `stream`, or of torch's current stream on a device, without a Stream object
+    (which costs 3 us, as much as a launch)."""
+    if stream is not None:
+        return stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 # ---------------------------------------------------------------------------
@@ -386,69 +397,93 @@ def kv_pool_bytes(desc: KvDesc) -> int:
 
 
 def _pool_nbytes(desc):
-    bits = {KV_BF16: 16, KV_FP8: 8, KV_FP4: 4}.get(desc.kind)
-    if bits is None or desc.pages < 1 or desc.kv_heads < 1 or desc.head_dim < 1 or desc.page_tokens < 1:
+    kind, heads, dim, page, pages = desc.kind, desc.kv_heads, desc.head_dim, desc.page_tokens, desc.pages
+    if kind not in (KV_BF16, KV_FP8, KV_FP4) or pages < 1 or heads < 1 or dim < 1 or page < 1:
         raise ValueError(f"invalid cache descriptor: {desc!r}")
-    token = desc.head_dim * bits // 8 + (0 if desc.kind == KV_BF16 else desc.head_dim // 32)
-    return desc.pages * desc.kv_heads * ((2 * desc.page_tokens * token + 15) // 16 * 16)
+    token = 2 * dim if kind == KV_BF16 else (dim if kind == KV_FP8 else dim // 2) + dim // 32
+    return pages * heads * ((2 * page * token + 15) // 16 * 16)
 
 
-def _batch(starts, lens, table, tokens, what):
-    """llvq_batch from starts [B + 1], lens [B] and table [B][max_pages] (int32)."""
-    import torch
-    for t, name in ((starts, "starts"), (lens, "lens"), (table, "table")):
-        _tensor(t, f"{what}: {name}", (torch.int32,))
-    n = lens.numel()
-    if lens.dim() != 1 or starts.dim() != 1 or starts.numel() != n + 1 or table.dim() != 2 or table.shape[0] != n:
-        raise ValueError(f"{what}: starts, lens and table must be [B + 1], [B] and [B][max_pages], got "
-                         f"{tuple(starts.shape)}, {tuple(lens.shape)} and {tuple(table.shape)}")
-    return Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), n, table.shape[1], tokens)
-
-
-def _rows(t, name, heads, dim):
-    """Checks rows [tokens][heads][dim] of fp32 or bf16 with contiguous channels; their (token,
-    head) strides in elements."""
+def _buffer(t, call, name, dtype=None, nbytes=0):
+    """Checks a contiguous device buffer (dtype None: any); returns its address.  The checks of _tensor;
+    messages are only made when one fails, since these calls run many times a token."""
     import torch
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+        raise TypeError(f"{call}: {name} must be a torch tensor, got {type(t).__name__}")
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name} must have dtype torch.float32 or torch.bfloat16, got {t.dtype}")
+        raise ValueError(f"{call}: {name} must be a GPU tensor (got device {t.device})")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{call}: {name} must have dtype {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{call}: {name} must be contiguous")
+    if nbytes and t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{call}: {name} holds {t.numel() * t.element_size()} bytes; the call needs at least {nbytes}")
+    return t.data_ptr()
+
+
+def _count(err_count, call):
+    if err_count is None:
+        return None
+    import torch
+    return _buffer(err_count, call, "err_count", torch.int32, 4)
+
+
+def _batch(starts, lens, table, tokens, call):
+    """llvq_batch from starts [B + 1], lens [B] and table [B][max_pages] (int32)."""
+    import torch
+    i32 = torch.int32
+    at = _buffer(starts, call, "starts", i32), _buffer(lens, call, "lens", i32), _buffer(table, call, "table", i32)
+    n, shape = lens.shape, table.shape
+    if len(n) != 1 or len(shape) != 2 or shape[0] != n[0] or starts.shape != (n[0] + 1,):
+        raise ValueError(f"{call}: starts, lens and table must be [B + 1], [B] and [B][max_pages], got "
+                         f"{tuple(starts.shape)}, {tuple(n)} and {tuple(shape)}")
+    return Batch(*at, n[0], shape[1], tokens)
+
+
+def _rows(t, call, name, heads, dim):
+    """Checks rows [tokens][heads][dim] of fp32 or bf16 with contiguous channels; returns the address
+    and the (token, head) strides in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{call}: {name} must be a torch tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{call}: {name} must be a GPU tensor (got device {t.device})")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise TypeError(f"{call}: {name} must have dtype torch.float32 or torch.bfloat16, got {t.dtype}")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(shape)}")
-    if stride[2] != 1 and t.numel():
-        raise ValueError(f"{name} must have contiguous channels (strides {stride})")
-    return stride[0], stride[1]
+        raise ValueError(f"{call}: {name} must be [tokens][{heads}][{dim}], got {tuple(shape)}")
+    if stride[2] != 1 and shape[0]:
+        raise ValueError(f"{call}: {name} must have contiguous channels (strides {stride})")
+    return t.data_ptr(), stride[0], stride[1]
 
 
-def _apart(t, name, strides):
+def _apart(t, call, name):
     """Refuses an output whose rows lie over each other (a broadcast or overlapping view)."""
-    token, head = strides
-    n, heads, dim = t.shape
+    if t.is_contiguous():
+        return
+    (n, heads, dim), (token, head, _) = t.shape, t.stride()
     lo, hi = sorted(((token, n), (head, heads)))
-    if t.numel() and not ((heads == 1 or head >= dim) and (n == 1 or token >= dim) and
-                          (n == 1 or heads == 1 or hi[0] >= (lo[1] - 1) * lo[0] + dim)):
-        raise ValueError(f"{name} has rows that overlap (strides {tuple(t.stride())})")
+    if n and not ((heads == 1 or head >= dim) and (n == 1 or token >= dim) and
+                  (n == 1 or heads == 1 or hi[0] >= (lo[1] - 1) * lo[0] + dim)):
+        raise ValueError(f"{call}: {name} has rows that overlap (strides {t.stride()})")
 
 
 def _kv_call(call, desc, pool, k, v, starts, lens, table, err_count, stream):
     import torch
-    ks = _rows(k, f"{call}: k", desc.kv_heads, desc.head_dim)
-    vs = _rows(v, f"{call}: v", desc.kv_heads, desc.head_dim)
-    if k.shape != v.shape or k.dtype != v.dtype:
+    ks = _rows(k, call, "k", desc.kv_heads, desc.head_dim)
+    vs = _rows(v, call, "v", desc.kv_heads, desc.head_dim)
+    if k.shape != v.shape or k.dtype is not v.dtype:
         raise ValueError(f"{call}: k and v must have one shape and dtype, got {tuple(k.shape)} {k.dtype} and "
                          f"{tuple(v.shape)} {v.dtype}")
     if call == "llvq_kv_read":
-        _apart(k, f"{call}: k", ks)
-        _apart(v, f"{call}: v", vs)
-    _tensor(pool, f"{call}: pool", (torch.uint8,), _pool_nbytes(desc))
-    _tensor(err_count, f"{call}: err_count", (torch.int32,), 4, nullable=True)
+        _apart(k, call, "k")
+        _apart(v, call, "v")
+    at = _buffer(pool, call, "pool", torch.uint8, _pool_nbytes(desc))
+    err = _count(err_count, call)
     batch = _batch(starts, lens, table, k.shape[0], call)
-    _check(getattr(load_library(), call)(ctypes.byref(desc), _ptr(pool), _ptr(k), *ks, _ptr(v), *vs,
-                                         X_F32 if k.dtype == torch.float32 else X_BF16, ctypes.byref(batch),
-                                         _ptr(err_count), _stream(stream)), call)
+    _check(getattr(load_library(), call)(desc, at, *ks, *vs, X_F32 if k.dtype is torch.float32 else X_BF16, batch, err,
+                                         _raw_stream(stream, k.get_device())), call)
 
 
 def kv_write(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
@@ -464,7 +499,7 @@ def kv_read(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
 
 
 def attn_workspace_bytes(desc, heads, tokens, batch, max_chunk, max_len) -> int:
-    n = load_library().llvq_attn_workspace_bytes(ctypes.byref(desc), heads, tokens, batch, max_chunk, max_len)
+    n = load_library().llvq_attn_workspace_bytes(desc, heads, tokens, batch, max_chunk, max_len)
     if n < 0:
         raise LlvqError(int(n), "llvq_attn_workspace_bytes")
     return n
@@ -477,26 +512,26 @@ def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len,
     sequence's new tokens; max_len: about the longest length (decides only how the keys are split);
     workspace: attn_workspace_bytes(...) bytes (None if that is 0)."""
     import torch
+    call = "llvq_attn"
     heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-    if heads < 1 or heads % desc.kv_heads:
-        raise ValueError(f"llvq_attn: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
-    qs = _rows(q, "llvq_attn: q", heads, desc.head_dim)
-    os_ = _rows(out, "llvq_attn: out", heads, desc.head_dim)
-    if q.shape != out.shape or q.dtype != out.dtype:
-        raise ValueError(f"llvq_attn: q and out must have one shape and dtype, got {tuple(q.shape)} {q.dtype} and "
+    if heads < 1 or desc.kv_heads < 1 or heads % desc.kv_heads:
+        raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
+    qs = _rows(q, call, "q", heads, desc.head_dim)
+    os_ = _rows(out, call, "out", heads, desc.head_dim)
+    if q.shape != out.shape or q.dtype is not out.dtype:
+        raise ValueError(f"{call}: q and out must have one shape and dtype, got {tuple(q.shape)} {q.dtype} and "
                          f"{tuple(out.shape)} {out.dtype}")
-    _apart(out, "llvq_attn: out", os_)
-    _tensor(pool, "llvq_attn: pool", (torch.uint8,), _pool_nbytes(desc))
-    _tensor(err_count, "llvq_attn: err_count", (torch.int32,), 4, nullable=True)
-    batch = _batch(starts, lens, table, q.shape[0], "llvq_attn")
+    _apart(out, call, "out")
+    at = _buffer(pool, call, "pool", torch.uint8, _pool_nbytes(desc))
+    err = _count(err_count, call)
+    batch = _batch(starts, lens, table, q.shape[0], call)
     need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
-    _tensor(workspace, "llvq_attn: workspace", None, need, nullable=need == 0)
+    ws = None if workspace is None and need == 0 else _buffer(workspace, call, "workspace", None, need)
     if scale is None:
         scale = desc.head_dim ** -0.5
-    _check(load_library().llvq_attn(ctypes.byref(desc), _ptr(pool), _ptr(q), *qs, _ptr(out), *os_,
-                                    X_F32 if q.dtype == torch.float32 else X_BF16, heads, ctypes.byref(batch), max_chunk,
-                                    max_len, scale, int(bool(causal)), window, _ptr(workspace), _ptr(err_count),
-                                    _stream(stream)), "llvq_attn")
+    _check(load_library().llvq_attn(desc, at, *qs, *os_, X_F32 if q.dtype is torch.float32 else X_BF16, heads, batch, max_chunk,
+                                    max_len, scale, 1 if causal else 0, window, ws, err, _raw_stream(stream, q.get_device())),
+           call)
 
 
 def draft_workspace_bytes(batch, vocab) -> int:
@@ -512,23 +547,30 @@ def draft_verify(target, draft, tokens, uniforms, noise, accepted, out, workspac
     certain drafts) with uniforms [B][S] and exponential noise [B][V]: accepted [B] and out [B][S + 1]
     (accepted tokens, one drawn token, then -1), int32."""
     import torch
-    _tensor(target, "llvq_draft_verify: target", (torch.float32, torch.bfloat16))
+    call = "llvq_draft_verify"
+    dtype = target.dtype if isinstance(target, torch.Tensor) else None
+    at = _buffer(target, call, "target")
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"{call}: target must have dtype torch.float32 or torch.bfloat16, got {dtype}")
     if target.dim() != 3 or target.shape[1] < 1:
-        raise ValueError(f"llvq_draft_verify: target must be [B][drafts + 1][vocab], got {tuple(target.shape)}")
-    b, s, v = target.shape[0], target.shape[1] - 1, target.shape[2]
-    _tensor(draft, "llvq_draft_verify: draft", (target.dtype,), nullable=True)
-    for t, name, dtype, shape in ((draft, "draft", target.dtype, (b, s, v)), (tokens, "tokens", torch.int32, (b, s)),
-                                  (uniforms, "uniforms", torch.float32, (b, s)), (noise, "noise", torch.float32, (b, v)),
-                                  (accepted, "accepted", torch.int32, (b,)), (out, "out", torch.int32, (b, s + 1)),
-                                  (counts, "counts", torch.int32, (b,))):
-        if t is None and name in ("draft", "counts"):
-            continue
-        _tensor(t, f"llvq_draft_verify: {name}", (dtype,))
-        if tuple(t.shape) != shape:
-            raise ValueError(f"llvq_draft_verify: {name} must be {list(shape)}, got {tuple(t.shape)}")
-    _tensor(workspace, "llvq_draft_verify: workspace", None, draft_workspace_bytes(b, v))
-    _tensor(err_count, "llvq_draft_verify: err_count", (torch.int32,), 4, nullable=True)
-    _check(load_library().llvq_draft_verify(_ptr(target), _ptr(draft), X_F32 if target.dtype == torch.float32 else X_BF16,
-                                            _ptr(tokens), _ptr(counts), _ptr(uniforms), _ptr(noise), b, s, v,
-                                            _ptr(accepted), _ptr(out), _ptr(workspace), _ptr(err_count),
-                                            _stream(stream)), "llvq_draft_verify")
+        raise ValueError(f"{call}: target must be [B][drafts + 1][vocab], got {tuple(target.shape)}")
+    b, s, v = target.shape
+    s -= 1
+
+    def of(t, name, kind, shape, nullable=False):
+        if t is None and nullable:
+            return None
+        p = _buffer(t, call, name, kind)
+        if t.shape != shape:
+            raise ValueError(f"{call}: {name} must be {list(shape)}, got {tuple(t.shape)}")
+        return p
+
+    i32, f32 = torch.int32, torch.float32
+    args = (of(tokens, "tokens", i32, (b, s)), of(counts, "counts", i32, (b,), True), of(uniforms, "uniforms", f32, (b, s)),
+            of(noise, "noise", f32, (b, v)))
+    draft_at = of(draft, "draft", dtype, (b, s, v), True)
+    outs = of(accepted, "accepted", i32, (b,)), of(out, "out", i32, (b, s + 1))
+    ws = _buffer(workspace, call, "workspace", None, draft_workspace_bytes(b, v))
+    err = _count(err_count, call)
+    _check(load_library().llvq_draft_verify(at, draft_at, X_F32 if dtype is f32 else X_BF16, *args, b, s, v, *outs, ws, err,
+                                            _raw_stream(stream, target.get_device())), call)

@@ -934,35 +934,73 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
     }
 }
 
-// Joins the splits of a row: one wave a row, four channels a lane, the splits in order.
-template <bool F32>
+// Joins the splits of a row under their common maximum.  A lane first takes the maximum and sum of two
+// splits, so that the weights of all are known after one round of loads; then 64 / LANES splits of a wave
+// are read side by side, four channels a lane, and what the waves of a row have is added in order through LDS.  WAVES
+// waves a row: one where rows are many and splits few, four where a long axis left few rows of many splits.
+constexpr int kMaxSplits = 128;
+
+template <bool F32, int LANES, int WAVES>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  constexpr int kSide = kWave / LANES;
   const Cache& c = a.c;
+  __shared__ __align__(16) float sums[4][kSide][LANES * 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int heads = c.heads * (int)a.share.by;
-  const int64_t rows = (int64_t)c.tokens * heads, row = (int64_t)blockIdx.x * 4 + wave;
-  if (row >= rows) return;
-  const int64_t t = row / heads, head = row - t * heads;
+  const int64_t rows = (int64_t)c.tokens * heads, row = ((int64_t)blockIdx.x * 4 + wave) / WAVES;
+  const bool in = row < rows;
+  const int64_t t = in ? row / heads : 0, head = in ? row - t * heads : 0;
   // rows that belong to no sequence are not written
   const int b = sequence_of(c, (int)t);
-  if (b >= c.batch) return;
-  const Seq s = sequence(c, b);
-  if (t < s.first || t >= s.first + s.n) return;
-  float top = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, a.stats[(i * rows + row) * 2]);
-  const int ch = lane * 4;
-  float l = 0.0f;
-  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = 0; i < a.splits; ++i) {
-    const int64_t at = i * rows + row;
-    const float m = a.stats[at * 2], li = a.stats[at * 2 + 1];
-    if (m == -INFINITY && li == 0.0f) continue;  // a split with nothing to see wrote no sums
-    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
-    l += li * f;
-    if (ch < c.dim) x += *reinterpret_cast<const f32x4*>(a.part + at * c.dim + ch) * f;
+  const Seq s = b < c.batch ? sequence(c, b) : Seq{0, 0, 0, true};
+  const bool live = in && t >= s.first && t < s.first + s.n;
+
+  float ms[2], ls[2], f[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int sp = i * kWave + lane;
+    const bool there = live && sp < a.splits;
+    ms[i] = there ? a.stats[(sp * rows + row) * 2] : -INFINITY;
+    ls[i] = there ? a.stats[(sp * rows + row) * 2 + 1] : 0.0f;
   }
-  if (ch >= c.dim) return;
+  float top = fmaxf(ms[0], ms[1]), l = 0.0f;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // a split that a row sees nothing of wrote no sums that count: weight zero, and it is not read
+    f[i] = ms[i] == -INFINITY ? (ls[i] == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(ms[i] - top);
+    if (ms[i] == -INFINITY && ls[i] == 0.0f) f[i] = -1.0f;
+    else l += ls[i] * f[i];
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) l += __shfl_xor(l, d);
+
+  const int side = lane / LANES, ch = (lane % LANES) * 4, part = wave % WAVES;
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i0 = part * kSide; i0 < a.splits; i0 += WAVES * kSide * 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * WAVES * kSide + side;
+      const float w = __shfl(i < kWave ? f[0] : f[1], i & 63);
+      if (i < a.splits && w >= 0.0f && ch < c.dim && live)
+        x += *reinterpret_cast<const f32x4*>(a.part + (i * rows + row) * c.dim + ch) * w;
+      else if (i < a.splits && w != w)
+        x += w;
+    }
+  }
+  if constexpr (kSide > 1 || WAVES > 1) {
+    *reinterpret_cast<f32x4*>(&sums[wave][side][ch]) = x;
+    __syncthreads();
+    if (part != 0 || side != 0) return;
+    x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
+#pragma unroll
+      for (int j = 0; j < kSide; ++j) x += *reinterpret_cast<const f32x4*>(&sums[wave + i][j][ch]);
+  }
+  if (!live || ch >= c.dim) return;
   x *= l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t at = t * a.out_token + head * a.out_head + ch;
   if constexpr (F32)
