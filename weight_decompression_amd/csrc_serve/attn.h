@@ -19,8 +19,8 @@
 // common part cancels.  For f32 queries both Q and P are split into three bf16 terms
 // (x = hi + mid + lo, what is left is below 2^-26 |x|), three matrix instructions in the place of one.
 //
-// A workgroup has four waves: WK of them share out the keys of a tile, 4 / WK the columns.  Few rows
-// (a decode step): WK = 4.  Many rows (a chunk): WK = 1.
+// Two kernels share this: k_attn_few for up to 64 rows of a (sequence, key head), where a workgroup's waves
+// share out the keys, and k_attn_many, where they share out the rows.
 #pragma once
 
 #include "kv_cache.h"
@@ -41,21 +41,8 @@ struct AttnArgs {
   int32_t* err;
 };
 
+constexpr int kManyRows = 128;        // rows of a workgroup of k_attn_many
 constexpr float kRescaleStep = 8.0f;  // log2: how far a maximum may be passed before the sums are rescaled
-
-// Byte offset of 16-byte chunk `ch` of key `row` in a staged tile.  Keys: 16 rows at one chunk (a
-// ds_read_b128 of 16 lanes) fall on 16 different slots of 256 bytes.  Values: the four rows that one
-// transposing load takes at 64 bytes of channels fall on four different 64-byte segments.
-template <int DP>
-__device__ __forceinline__ int k_at(int row, int ch) {
-  const int sw = DP == 64 ? (row >> 1) & 7 : row & 15;
-  return row * (DP * 2) + ((ch ^ sw) << 4);
-}
-template <int DP>
-__device__ __forceinline__ int v_at(int row, int ch) {
-  const int sw = DP == 64 ? (((row >> 1) & 1) << 2) | ((row >> 2) & 3) : ((row & 3) << 2) | ((row >> 2) & 3);
-  return row * (DP * 2) + ((ch ^ sw) << 4);
-}
 
 __device__ __forceinline__ float half_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -566,35 +553,40 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   }
 }
 
-// Many rows: the tiles are shared by the workgroup's four waves, each with 32 columns of its own.
-template <int KIND, int DP, int NT, int WK>
-struct AttnShape {
-  static constexpr int kWaveCols = 4 / WK;
-  static constexpr int kRows = 32 * kWaveCols;              // rows (columns of S^T) of a workgroup
-  static constexpr int kSub = WK == 1 ? 2 : 1;              // 32-key pieces of a wave in a tile
-  static constexpr int kKeys = 32 * kSub * WK;              // keys of a tile
-  static constexpr int kTile = kKeys * DP * 2;              // bytes of the staged keys, and of the values
-  static constexpr int kRawRow = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
-  static constexpr int kChunks = kKeys * kRawRow;
-  static constexpr int kPer = (kChunks + 255) / 256;        // chunks a thread stages
-  static constexpr int kJoin = WK > 1 ? 4 * 32 * DP * 4 : 0;  // the waves' sums, in the tiles' place
-  static constexpr int kLds = 2 * kTile > kJoin ? 2 * kTile : kJoin;
+// Many rows: 128 rows of a (sequence, key head), 32 columns a wave, tiles shared by the four waves.
+//
+// A chunk of a prompt reuses every key for many rows, so the matrix instructions bound it, next to exp and
+// what else the softmax costs on the vector units.  Two waves a SIMD (of two workgroups, or of what registers
+// allow) let one's softmax run under the other's products.  Tiles are double-buffered in LDS: after the one barrier
+// of a round the next tile, whose codes were loaded a round ago, is expanded into the other buffer, the loads of the one after it are issued,
+// and the round's products are taken.  32x32x16 instructions read an operand of 32 keys for 32 columns.
+template <int KIND, int DP, int NT>
+struct ManyShape {
+  static constexpr int kSub = NT == 1 && DP <= 128 ? 2 : 1;  // 32-key pieces of a tile
+  static constexpr int kKeys = 32 * kSub;
+  // rows padded so that 16 rows at one 16-byte chunk fall on 16 slots of 256 bytes (keys), and four rows
+  // at 64 bytes of channels on four segments (values)
+  static constexpr int kKeyRow = DP * 2 + 16, kValueRow = DP * 2 + 64;
+  static constexpr int kBuffer = kKeys * (kKeyRow + kValueRow);
+  static constexpr int kRaw = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
+  static constexpr int kChunks = kKeys * kRaw;
+  static constexpr int kPer = (kChunks + 255) / 256;      // chunks a thread stages
+  // registers: queries, outputs, scores, P, chunks in flight
+  static constexpr int kHeld = NT * DP / 4 + DP / 2 + 16 * kSub + 8 * NT * kSub + 14 * kPer + 30;
+  static constexpr int kWaves = kHeld <= 256 ? 2 : 1;
 };
 
-template <int KIND, int DP, int NT, int WK>
-__global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
-  using Sh = AttnShape<KIND, DP, NT, WK>;
-  constexpr int kKeys = Sh::kKeys, kSub = Sh::kSub, kSteps = DP / 16, kOut = DP / 32;
+template <int KIND, int DP, int NT>
+__global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn_many(AttnArgs a) {
+  using Sh = ManyShape<KIND, DP, NT>;
+  constexpr int kKeys = Sh::kKeys, kSub = Sh::kSub, kSteps = DP / 16, kOut = DP / 32, kPer = Sh::kPer, kRaw = Sh::kRaw;
+  constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
   const Cache& c = a.c;
-  __shared__ __align__(16) uint8_t lds[Sh::kLds];
-  uint8_t* lds_k = lds;
-  uint8_t* lds_v = lds + Sh::kTile;
-  __shared__ uint32_t bad_keys[2][4];
-  __shared__ __align__(16) float poison[DP];
+  __shared__ __align__(16) uint8_t lds[2 * Sh::kBuffer];
+  __shared__ uint32_t bad_keys[3][kSub];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wk = wave % WK, wq = wave / WK;
   const int half = lane >> 5, col = lane & 31;
 
   int id = blockIdx.x;
@@ -606,158 +598,135 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
   const int b = id / a.row_blocks;
   const Seq s = sequence(c, b);
   const int share = (int)a.share.by, rows = s.n * share;
-  if (a.err && tid == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * Sh::kRows))
-    atomicAdd(a.err, 1);
-  const int row0 = rb * Sh::kRows;
+  if (a.err && tid == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * kManyRows)) atomicAdd(a.err, 1);
+  const int row0 = rb * kManyRows;
   if (row0 >= rows) return;
+  const Span w = span_of(a, s, row0, kManyRows, kKeys, split);
 
-  // this lane's row, and the keys it sees: [lo, lo + seen)
-  const int row = row0 + wq * 32 + col;
+  const int row = row0 + wave * 32 + col;
   const bool live = row < rows;
   const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
   const int qhead = head * share + (live ? row - t * share : 0);
-  const int pos = s.len - s.n + t;
-  const int hi = a.causal ? min(max(pos + 1, 0), s.len) : s.len;
-  const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-  const int seen = live ? max(hi - lo, 0) : 0;
-
-  // the workgroup's keys: [first_key, last_key), and those that every row of it sees
-  const int t0 = (int)divide((uint32_t)row0, a.share);
-  const int t1 = (int)divide((uint32_t)(min(row0 + Sh::kRows, rows) - 1), a.share);
-  const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
-  const int last_key = a.causal ? min(max(p1 + 1, 0), s.len) : s.len;
-  const int first_key = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
-  const int all_hi = a.causal ? p0 + 1 : s.len;
-  const int all_lo = a.window > 0 ? max(p1 - a.window + 1, 0) : 0;
-  const int key0 = first_key / kKeys;
-  const int tiles = last_key > first_key ? (last_key + kKeys - 1) / kKeys - key0 : 0;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int tile_lo = min(split * per, tiles), tile_hi = min(tile_lo + per, tiles);
-
-  // the queries, as the second operand of S^T: 8 consecutive channels of the lane's column
+  int lo, seen;
+  seen_of(a, s, t, live, &lo, &seen);
   bf16x8 q[NT][kSteps];
-  {
-    const int64_t at = (int64_t)(s.first + t) * a.q_token + (int64_t)qhead * a.q_head;
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      const int ch = st * 16 + half * 8;
-      float x[8];
+  for (int st = 0; st < kSteps; ++st) {
+    bf16x8 terms[NT];
+    load_query<NT>(a, (int64_t)(s.first + t) * a.q_token + (int64_t)qhead * a.q_head, st * 16 + half * 8, live, terms);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-      if (live && ch < c.dim) {
-        if constexpr (NT == 1) {
-          if (a.q_vec)
-            load8<false, true>(a.q, at + ch, x);
-          else
-            load8<false, false>(a.q, at + ch, x);
-        } else {
-          if (a.q_vec)
-            load8<true, true>(a.q, at + ch, x);
-          else
-            load8<true, false>(a.q, at + ch, x);
-        }
-      }
-      bf16x8 terms[NT];
-      split_terms<NT>(x, terms);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) q[n][st] = terms[n];
-    }
+    for (int n = 0; n < NT; ++n) q[n][st] = terms[n];
   }
-
   f32x16 acc[kOut];
 #pragma unroll
   for (int i = 0; i < kOut; ++i) acc[i] = f32x16{0.0f};
   float m = -INFINITY, l = 0.0f;
 
-  u32x4 raw_k[Sh::kPer], raw_v[Sh::kPer];
-  uint32_t sc_k[Sh::kPer], sc_v[Sh::kPer];
+  const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
+  const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  // a thread's chunks of a tile: chunk i * 256 + tid is chunk `ch` of key `key0 + i * 256 / kRaw`
+  static_assert(256 % kRaw == 0, "a thread has one chunk place in all its rows");
+  const int ch = tid % kRaw, key0 = tid / kRaw;
+  const bool in_tile = Sh::kChunks >= 256 || tid < Sh::kChunks;  // (kPer is 1 where a tile has fewer)
+  const bool mine = in_tile && ch * 16 < c.row;
+  constexpr int32_t kNoKey = INT32_MIN;
+  int32_t ids[kPer];
+  u32x4 raw_k[kPer], raw_v[kPer];
+  uint32_t sc_k[kPer], sc_v[kPer];
+  bool there[kPer];
   bool lost = false;
+  auto page_of = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = tile * kKeys + key0 + i * (256 / kRaw);
+      ids[i] = mine && tile < w.tile_hi && j >= w.first_key && j < w.last_key ? table[divide((uint32_t)j, c.page)] : kNoKey;
+    }
+  };
   auto fetch = [&](int tile) {
 #pragma unroll
-    for (int i = 0; i < Sh::kPer; ++i) {
-      const int chunk = tid + i * 256;
-      const int key = chunk / Sh::kRawRow, ch = chunk % Sh::kRawRow;
-      const int j = (key0 + tile) * kKeys + key;
-      raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0};
-      sc_k[i] = sc_v[i] = 127;
-      if (chunk < Sh::kChunks && j >= first_key && j < last_key && ch * 16 < c.row) {
-        const uint32_t page = divide((uint32_t)j, c.page);
-        const int slot = j - (int)(page * c.page.by);
-        const int64_t base = block_of(c, b, page, head);
-        if (base >= 0) {
-          const uint8_t* blk = c.pool + base;
-          raw_k[i] = *reinterpret_cast<const u32x4*>(blk + slot * c.row + ch * 16);
-          raw_v[i] = *reinterpret_cast<const u32x4*>(blk + c.v_off + slot * c.row + ch * 16);
-          if constexpr (KIND != LLVQ_KV_BF16) {
-            const int g = KIND == LLVQ_KV_FP8 ? ch >> 1 : ch;
-            sc_k[i] = blk[c.ks_off + slot * c.groups + g];
-            sc_v[i] = blk[c.vs_off + slot * c.groups + g];
-          }
-        } else {
-          lost = true;
-        }
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t j = (uint32_t)(tile * kKeys + key0 + i * (256 / kRaw));
+      there[i] = ids[i] >= 0 && ids[i] < c.pages;
+      lost |= !there[i] && ids[i] != kNoKey;
+      // a place that is not there is read from the pool's start and left out when it is staged
+      const int slot = there[i] ? (int)(j - divide(j, c.page) * c.page.by) : 0, at = there[i] ? ch : 0;
+      const uint8_t* blk = c.pool + (there[i] ? (int64_t)ids[i] * page_bytes + head_off : 0);
+      raw_k[i] = *reinterpret_cast<const u32x4*>(blk + slot * c.row + at * 16);
+      raw_v[i] = *reinterpret_cast<const u32x4*>(blk + c.v_off + slot * c.row + at * 16);
+      if constexpr (KIND != LLVQ_KV_BF16) {
+        sc_k[i] = blk[c.ks_off + slot * c.groups + at * kOf / 4];
+        sc_v[i] = blk[c.vs_off + slot * c.groups + at * kOf / 4];
+      } else {
+        sc_k[i] = sc_v[i] = 127;
       }
     }
   };
-  auto stage = [&](int par) {
+  auto stage = [&](uint8_t* buffer, uint32_t* bad_bits) {
 #pragma unroll
-    for (int i = 0; i < Sh::kPer; ++i) {
-      const int chunk = tid + i * 256;
-      if (chunk < Sh::kChunks) {
-        const int key = chunk / Sh::kRawRow, ch = chunk % Sh::kRawRow;
-        constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
-        u32x4 o[kOf];
-        expand<KIND>(raw_k[i], sc_k[i], o);
+    for (int i = 0; i < kPer; ++i) {
+      if (!in_tile) break;
+      const int key = key0 + i * (256 / kRaw);
+      u32x4 rk = raw_k[i], rv = raw_v[i], o[kOf];
+      uint32_t sk = sc_k[i], sv = sc_v[i];
+      if (!there[i]) rk = rv = u32x4{0, 0, 0, 0}, sk = sv = 127;
+      expand<KIND>(rk, sk, o);
 #pragma unroll
-        for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(lds_k + k_at<DP>(key, ch * kOf + n)) = o[n];
-        // values that are not finite would spoil rows that do not see them (0 * NaN): they are left
-        // out here and added to the rows that do see them after the tile's products
-        bool bad;
-        if constexpr (KIND == LLVQ_KV_BF16) {
-          o[0] = raw_v[i];
-          bad = drop_nonfinite(&o[0]);
-        } else {
-          bad = sc_v[i] == 255;
-          expand<KIND>(bad ? u32x4{0, 0, 0, 0} : raw_v[i], bad ? 127 : sc_v[i], o);
-        }
-        if (bad) atomicOr(&bad_keys[par][key >> 5], 1u << (key & 31));
-#pragma unroll
-        for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(lds_v + v_at<DP>(key, ch * kOf + n)) = o[n];
+      for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(buffer + key * Sh::kKeyRow + (ch * kOf + n) * 16) = o[n];
+      // values that are not finite would spoil rows that do not see them (0 * NaN): they are left out
+      // here and added to the rows that do see them after the tile's products
+      bool bad;
+      if constexpr (KIND == LLVQ_KV_BF16) {
+        bad = drop_nonfinite(&rv);
+      } else {
+        bad = sv == 255;
+        if (bad) rv = u32x4{0, 0, 0, 0}, sv = 127;
       }
+      expand<KIND>(rv, sv, o);
+      if (bad) atomicOr(&bad_bits[key >> 5], 1u << (key & 31));
+#pragma unroll
+      for (int n = 0; n < kOf; ++n)
+        *reinterpret_cast<u32x4*>(buffer + kKeys * Sh::kKeyRow + key * Sh::kValueRow + (ch * kOf + n) * 16) = o[n];
     }
   };
 
-  if (tid < 8) bad_keys[tid >> 2][tid & 3] = 0;
-  if (tile_lo < tile_hi) fetch(tile_lo);
-  int par = 0;
-  for (int tile = tile_lo; tile < tile_hi; ++tile, par ^= 1) {
-    __syncthreads();  // the last tile has been read
-    stage(par);
-    __syncthreads();
-    if (tile + 1 < tile_hi) fetch(tile + 1);
-
-    const int key_base = (key0 + tile) * kKeys;
-    const bool whole = key_base >= all_lo && key_base + kKeys <= all_hi && key_base + kKeys <= s.len;
+  if (tid < 3 * kSub) bad_keys[tid / kSub][tid % kSub] = 0;
+  __syncthreads();
+  if (w.tile_lo < w.tile_hi) {
+    page_of(w.tile_lo);
+    fetch(w.tile_lo);
+    page_of(w.tile_lo + 1);
+    stage(lds, bad_keys[0]);
+    fetch(w.tile_lo + 1);
+    page_of(w.tile_lo + 2);
+  }
+  int third = 0;
+  for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
+    const int par = (tile - w.tile_lo) & 1, next = third == 2 ? 0 : third + 1, after = next == 2 ? 0 : next + 1;
+    const uint8_t* buffer = lds + par * Sh::kBuffer;
+    __syncthreads();  // this tile is staged, and the other buffer has been read
+    if (tid < kSub) bad_keys[after][tid] = 0;
+    if (tile + 1 < w.tile_hi) {
+      stage(lds + (par ^ 1) * Sh::kBuffer, bad_keys[next]);
+      fetch(tile + 2);
+      page_of(tile + 3);
+    }
+    const int key_base = tile * kKeys;
     f32x16 sc[kSub];
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
-      const int krow = (wk * kSub + u) * 32 + col;
       sc[u] = f32x16{0.0f};
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(lds_k + k_at<DP>(krow, st * 2 + half));
+        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(buffer + (u * 32 + col) * Sh::kKeyRow + (st * 2 + half) * 16);
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[n][st], sc[u], 0, 0, 0);
       }
     }
-    if (!whole) {
+    if (!(key_base >= w.all_lo && key_base + kKeys <= w.all_hi && key_base + kKeys <= s.len)) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = key_base + (wk * kSub + u) * 32 + 8 * (i / 4) + 4 * half + (i & 3);
-          sc[u][i] = (uint32_t)(j - lo) < (uint32_t)seen ? sc[u][i] : -INFINITY;
-        }
+        for (int i = 0; i < 16; ++i) sc[u][i] = masked(sc[u][i], key_base + u * 32 + 8 * (i / 4) + 4 * half + (i & 3), lo, seen);
     }
     float top = -INFINITY;
 #pragma unroll
@@ -768,14 +737,12 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
     // The maximum is raised only when it is passed by 2^8: p stays below 2^8 and its rounding is
     // relative, so the result is the same, and most tiles skip the rescaling of O.
     if (__any(top > m + kRescaleStep)) {
-      const float next = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-      m = next;
+      const float raised = fmaxf(m, top);
+      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - raised);
+      m = raised;
       l *= f;
 #pragma unroll
-      for (int i = 0; i < kOut; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+      for (int i = 0; i < kOut; ++i) acc[i] *= f;
     }
     const float ms = m == -INFINITY ? 0.0f : m;
     bf16x8 p[NT][kSub * 2];
@@ -785,153 +752,71 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
       for (int h2 = 0; h2 < 2; ++h2) {
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][h2 * 8 + e], a.scale_log2, -ms));
-          if constexpr (NT > 1) l += x[e];
-        }
+        for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][h2 * 8 + e], a.scale_log2, -ms));
         bf16x8 terms[NT];
         split_terms<NT>(x, terms);
-        // the sum takes the rounded values, two at a time: what all of a row's roundings have in common cancels
-        if constexpr (NT == 1) {
-          const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{terms[0][2 * e], terms[0][2 * e + 1]}, one, l, false);
-        }
+        l = sum_p<NT>(x, terms[0], l);
 #pragma unroll
         for (int n = 0; n < NT; ++n) p[n][u * 2 + h2] = terms[n];
       }
+    const uint8_t* values = buffer + kKeys * Sh::kKeyRow + (4 * half + ((lane & 15) >> 2)) * Sh::kValueRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
-    for (int d = 0; d < kOut; ++d)
+    for (int u = 0; u < kSub * 2; ++u)
 #pragma unroll
-      for (int u = 0; u < kSub * 2; ++u) {
-        const int vrow = wk * kSub * 32 + u * 16 + 4 * half + ((lane & 15) >> 2);
-        const int ch = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        const int in = (lane & 1) * 8;
+      for (int d = 0; d < kOut; ++d) {
+        const uint8_t* at = values + u * 16 * Sh::kValueRow + d * 64;
         union {
           s16x4 h[2];
           bf16x8 v;
         } vf;
-        vf.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_v + v_at<DP>(vrow, ch) + in));
-        vf.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_v + v_at<DP>(vrow + 8, ch) + in));
+        vf.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+        vf.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * Sh::kValueRow));
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.v, p[n][u], acc[d], 0, 0, 0);
       }
-    // values that are not finite, added to the rows that see them
-    for (int w = 0; w < kKeys / 32; ++w) {
-      uint32_t left = bad_keys[par][w];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      uint32_t left = __builtin_amdgcn_readfirstlane((int)bad_keys[third][u]);
       while (left) {
-        const int key = w * 32 + __builtin_ctz(left);
+        const int j = key_base + u * 32 + __builtin_ctz(left);
         left &= left - 1;
-        const int j = key_base + key;
-        __syncthreads();
         const uint32_t page = divide((uint32_t)j, c.page);
-        const int slot = j - (int)(page * c.page.by);
-        const int64_t base = block_of(c, b, page, head);
-        if (tid < DP) {
-          float x = 0.0f;
-          if (tid < c.dim && base >= 0) {
-            const uint8_t* blk = c.pool + base;
-            if constexpr (KIND == LLVQ_KV_BF16) {
-              x = bf16_f32(reinterpret_cast<const uint16_t*>(blk + c.v_off + slot * c.row)[tid]);
-              if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) x = 0.0f;
-            } else {
-              x = blk[c.vs_off + slot * c.groups + tid / kGroup] == 255 ? NAN : 0.0f;
-            }
+        const uint8_t* blk = c.pool + (int64_t)table[page] * page_bytes + head_off;
+        const bool sees = (uint32_t)(j - lo) < (uint32_t)seen;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const f32x4 x = nonfinite4<KIND>(c, blk, j - (int)(page * c.page.by), d * 32 + i4 * 8 + half * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (sees) acc[d][i4 * 4 + i] += x[i];
           }
-          poison[tid] = x;
-        }
-        __syncthreads();
-        if (key / (32 * kSub) == wk && (uint32_t)(j - lo) < (uint32_t)seen) {
-#pragma unroll
-          for (int d = 0; d < kOut; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[d][i] += poison[d * 32 + 8 * (i / 4) + 4 * half + (i & 3)];
-        }
       }
     }
-    if (tid < 4) bad_keys[par ^ 1][tid] = 0;
+    third = next;
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 
   l = half_sum(l);
-  if constexpr (WK > 1) {
-    // the waves that shared out the keys are joined through LDS: each brings its sums under the common
-    // maximum and the sums are added in the waves' order
-    __shared__ float wave_m[4][32], wave_l[4][32];
-    __syncthreads();
-    if (half == 0) wave_m[wave][col] = m;
-    __syncthreads();
-    float top = m;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) top = fmaxf(top, wave_m[wq * WK + w][col]);
-    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-    m = top;
-    if (half == 0) wave_l[wave][col] = l * f;
-    float* sums = reinterpret_cast<float*>(lds);  // [wave][32 columns][DP], quads of channels swizzled by the column
-#pragma unroll
-    for (int d = 0; d < kOut; ++d)
-#pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const int quad = (d * 8 + i4 * 2 + half) ^ (col & 7);
-        *reinterpret_cast<f32x4*>(sums + (wave * 32 + col) * DP + quad * 4) =
-            f32x4{acc[d][i4 * 4] * f, acc[d][i4 * 4 + 1] * f, acc[d][i4 * 4 + 2] * f, acc[d][i4 * 4 + 3] * f};
-      }
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) l += wave_l[wq * WK + w][col];
-    if (wk == 0) {
-#pragma unroll
-      for (int d = 0; d < kOut; ++d)
-#pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const int quad = (d * 8 + i4 * 2 + half) ^ (col & 7);
-          f32x4 x = *reinterpret_cast<const f32x4*>(sums + (wave * 32 + col) * DP + quad * 4);
-#pragma unroll
-          for (int w = 1; w < WK; ++w) x += *reinterpret_cast<const f32x4*>(sums + ((wave + w) * 32 + col) * DP + quad * 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[d][i4 * 4 + i] = x[i];
-        }
-    }
-    if (wk != 0) return;
-  }
   if (!live) return;
+  const int64_t at = (int64_t)(s.first + t) * c.heads * share + qhead;
   if (a.splits > 1) {
-    const int64_t at = (int64_t)split * c.tokens * c.heads * share + (int64_t)(s.first + t) * c.heads * share + qhead;
     if (half == 0) {
-      a.stats[at * 2] = m;
-      a.stats[at * 2 + 1] = l;
+      const int64_t all = (int64_t)c.tokens * c.heads * share;
+      a.stats[(split * all + at) * 2] = m;
+      a.stats[(split * all + at) * 2 + 1] = l;
     }
-    if (tile_lo >= tile_hi) return;
-#pragma unroll
-    for (int d = 0; d < kOut; ++d)
-#pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const int ch = d * 32 + i4 * 8 + half * 4;
-        if (ch < c.dim)
-          *reinterpret_cast<f32x4*>(a.part + at * c.dim + ch) =
-              f32x4{acc[d][i4 * 4], acc[d][i4 * 4 + 1], acc[d][i4 * 4 + 2], acc[d][i4 * 4 + 3]};
-      }
-    return;
+    if (w.tile_lo >= w.tile_hi) return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible key: the row is zero
-  const int64_t at = (int64_t)(s.first + t) * a.out_token + (int64_t)qhead * a.out_head;
+  const int64_t out_at = (int64_t)(s.first + t) * a.out_token + (int64_t)qhead * a.out_head;
 #pragma unroll
   for (int d = 0; d < kOut; ++d)
 #pragma unroll
-    for (int i4 = 0; i4 < 4; ++i4) {
-      const int ch = d * 32 + i4 * 8 + half * 4;
-      if (ch < c.dim) {
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = acc[d][i4 * 4 + i] * inv;
-        if constexpr (NT == 1)
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at + ch) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-        else
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + ch) = f32x4{x[0], x[1], x[2], x[3]};
-      }
-    }
+    for (int i4 = 0; i4 < 4; ++i4)
+      store_row4<NT>(a, at, out_at, split, d * 32 + i4 * 8 + half * 4,
+                     f32x4{acc[d][i4 * 4], acc[d][i4 * 4 + 1], acc[d][i4 * 4 + 2], acc[d][i4 * 4 + 3]}, inv);
 }
 
 // Joins the splits of a row under their common maximum.  A lane first takes the maximum and sum of two

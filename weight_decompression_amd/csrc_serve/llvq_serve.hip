@@ -119,7 +119,7 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, bool f32, Cut* cut) {
   const int64_t rows = (int64_t)max_chunk * share;
   cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1) ? 1 : 2;
-  const int64_t per = cut->cols ? 16 * cut->cols : 128;
+  const int64_t per = cut->cols ? 16 * cut->cols : kManyRows;
   const int64_t blocks = (rows + per - 1) / per;
   const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
   if (base > (1ll << 30)) return LLVQ_EINVAL;
@@ -145,7 +145,7 @@ int launch_attn(const AttnArgs& a, int cols, unsigned grid, hipStream_t s) {
   if (cols == 1)
     hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
   else if (cols == 0)
-    hipLaunchKernelGGL((k_attn<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attn_many<KIND, DP, NT>), dim3(grid), dim3(256), 0, s, a);
   else if constexpr (few_pairs(KIND, DP, NT))
     hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 2>), dim3(grid), dim3(256), 0, s, a);
   return launch_status();
