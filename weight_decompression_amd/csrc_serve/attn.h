@@ -576,6 +576,12 @@ struct ManyShape {
   static constexpr int kWaves = kHeld <= 256 ? 2 : 1;
 };
 
+// Where a key lies: its codes in the pool, from there its scales, and whether it is there at all.
+struct alignas(16) Place {
+  int64_t row;
+  int32_t scale, there;
+};
+
 template <int KIND, int DP, int NT>
 __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn_many(AttnArgs a) {
   using Sh = ManyShape<KIND, DP, NT>;
@@ -584,6 +590,8 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   const Cache& c = a.c;
   __shared__ __align__(16) uint8_t lds[2 * Sh::kBuffer];
   __shared__ uint32_t bad_keys[3][kSub];
+  __shared__ Place places[2][kKeys];
+  __shared__ uint32_t part[2];  // whether a tile has a place that is not there
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -628,34 +636,47 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   static_assert(256 % kRaw == 0, "a thread has one chunk place in all its rows");
   const int ch = tid % kRaw, key0 = tid / kRaw;
   const bool in_tile = Sh::kChunks >= 256 || tid < Sh::kChunks;  // (kPer is 1 where a tile has fewer)
-  const bool mine = in_tile && ch * 16 < c.row;
+  const bool narrow = c.dim < DP;                                // rows shorter than the tile's
+  const uint8_t* pool = c.pool + (ch * 16 < c.row ? ch * 16 : 0);
+  const int scale_ch = ch * 16 < c.row ? ch * kOf / 4 - ch * 16 : 0;
   constexpr int32_t kNoKey = INT32_MIN;
-  int32_t ids[kPer];
+  int32_t ids = kNoKey;
   u32x4 raw_k[kPer], raw_v[kPer];
   uint32_t sc_k[kPer], sc_v[kPer];
-  bool there[kPer];
-  bool lost = false;
-  auto page_of = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = tile * kKeys + key0 + i * (256 / kRaw);
-      ids[i] = mine && tile < w.tile_hi && j >= w.first_key && j < w.last_key ? table[divide((uint32_t)j, c.page)] : kNoKey;
-    }
+  int there[kPer];
+  bool lost = false, part_of = false;
+  // Where a tile's keys lie is worked out once a key, by the wave whose turn it is: its page numbers are loaded
+  // four rounds ahead, the places written three rounds ahead and the codes loaded two rounds ahead.
+  auto load_pages = [&](int tile) {
+    if (wave != (tile & 3)) return;
+    const int j = tile * kKeys + lane;
+    ids = lane < kKeys && tile < w.tile_hi && j >= w.first_key && j < w.last_key ? table[divide((uint32_t)j, c.page)] : kNoKey;
+  };
+  auto write_places = [&](int tile) {
+    if (wave != (tile & 3)) return;
+    const uint32_t j = (uint32_t)(tile * kKeys + lane);
+    const bool ok = ids >= 0 && ids < c.pages;
+    lost |= !ok && ids != kNoKey;
+    // a place that is not there is read from the pool's start and left out when it is staged
+    const int slot = ok ? (int)(j - divide(j, c.page) * c.page.by) : 0;
+    if (lane < kKeys)
+      places[tile & 1][lane] = Place{(ok ? (int64_t)ids * page_bytes + head_off : 0) + slot * c.row, c.ks_off + slot * (c.groups - c.row), ok};
+    if (lane == 0) part[tile & 1] = 0;
+    if (__any(lane < kKeys && !ok) && lane == 0) part[tile & 1] = 1;
   };
   auto fetch = [&](int tile) {
+    part_of = narrow || __builtin_amdgcn_readfirstlane((int)part[tile & 1]) != 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const uint32_t j = (uint32_t)(tile * kKeys + key0 + i * (256 / kRaw));
-      there[i] = ids[i] >= 0 && ids[i] < c.pages;
-      lost |= !there[i] && ids[i] != kNoKey;
-      // a place that is not there is read from the pool's start and left out when it is staged
-      const int slot = there[i] ? (int)(j - divide(j, c.page) * c.page.by) : 0, at = there[i] ? ch : 0;
-      const uint8_t* blk = c.pool + (there[i] ? (int64_t)ids[i] * page_bytes + head_off : 0);
-      raw_k[i] = *reinterpret_cast<const u32x4*>(blk + slot * c.row + at * 16);
-      raw_v[i] = *reinterpret_cast<const u32x4*>(blk + c.v_off + slot * c.row + at * 16);
+      const Place at = places[tile & 1][in_tile ? key0 + i * (256 / kRaw) : 0];
+      const uint8_t* k = pool + at.row;
+      there[i] = at.there;
+      raw_k[i] = *reinterpret_cast<const u32x4*>(k);
+      raw_v[i] = *reinterpret_cast<const u32x4*>(k + c.v_off);
       if constexpr (KIND != LLVQ_KV_BF16) {
-        sc_k[i] = blk[c.ks_off + slot * c.groups + at * kOf / 4];
-        sc_v[i] = blk[c.vs_off + slot * c.groups + at * kOf / 4];
+        const uint8_t* scale = k + (at.scale + scale_ch);
+        sc_k[i] = scale[0];
+        sc_v[i] = scale[c.vs_off - c.ks_off];
       } else {
         sc_k[i] = sc_v[i] = 127;
       }
@@ -668,7 +689,7 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
       const int key = key0 + i * (256 / kRaw);
       u32x4 rk = raw_k[i], rv = raw_v[i], o[kOf];
       uint32_t sk = sc_k[i], sv = sc_v[i];
-      if (!there[i]) rk = rv = u32x4{0, 0, 0, 0}, sk = sv = 127;
+      if (part_of && !(there[i] && ch * 16 < c.row)) rk = rv = u32x4{0, 0, 0, 0}, sk = sv = 127;
       expand<KIND>(rk, sk, o);
 #pragma unroll
       for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(buffer + key * Sh::kKeyRow + (ch * kOf + n) * 16) = o[n];
@@ -690,14 +711,19 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   };
 
   if (tid < 3 * kSub) bad_keys[tid / kSub][tid % kSub] = 0;
-  __syncthreads();
   if (w.tile_lo < w.tile_hi) {
-    page_of(w.tile_lo);
+    load_pages(w.tile_lo);
+    load_pages(w.tile_lo + 1);
+    load_pages(w.tile_lo + 2);
+    load_pages(w.tile_lo + 3);
+    write_places(w.tile_lo);
+    write_places(w.tile_lo + 1);
+    __syncthreads();
     fetch(w.tile_lo);
-    page_of(w.tile_lo + 1);
     stage(lds, bad_keys[0]);
     fetch(w.tile_lo + 1);
-    page_of(w.tile_lo + 2);
+    __syncthreads();
+    write_places(w.tile_lo + 2);
   }
   int third = 0;
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
@@ -708,18 +734,30 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
     if (tile + 1 < w.tile_hi) {
       stage(lds + (par ^ 1) * Sh::kBuffer, bad_keys[next]);
       fetch(tile + 2);
-      page_of(tile + 3);
+      write_places(tile + 3);
+      load_pages(tile + 4);
     }
     const int key_base = tile * kKeys;
+    // operands are read a few instructions ahead, in an order that is pinned: left to itself the compiler reads
+    // each right before its use and waits for it
+    constexpr int kAhead = 4;
     f32x16 sc[kSub];
+    {
+      const uint8_t* keys = buffer + col * Sh::kKeyRow + half * 16;
+      auto operand = [&](int k) { return *reinterpret_cast<const bf16x8*>(keys + (k % kSub) * 32 * Sh::kKeyRow + (k / kSub) * 32); };
+      bf16x8 kf[kAhead];
 #pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-      sc[u] = f32x16{0.0f};
+      for (int k = 0; k < kAhead; ++k) kf[k] = operand(k);
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(buffer + (u * 32 + col) * Sh::kKeyRow + (st * 2 + half) * 16);
+      for (int u = 0; u < kSub; ++u) sc[u] = f32x16{0.0f};
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = NT - 1; n >= 0; --n) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[n][st], sc[u], 0, 0, 0);
+      for (int k = 0; k < kSteps * kSub; ++k) {
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n)
+          sc[k % kSub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k % kAhead], q[n][k / kSub], sc[k % kSub], 0, 0, 0);
+        if (k + kAhead < kSteps * kSub) kf[k % kAhead] = operand(k + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (!(key_base >= w.all_lo && key_base + kKeys <= w.all_hi && key_base + kKeys <= s.len)) {
@@ -759,21 +797,31 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
 #pragma unroll
         for (int n = 0; n < NT; ++n) p[n][u * 2 + h2] = terms[n];
       }
-    const uint8_t* values = buffer + kKeys * Sh::kKeyRow + (4 * half + ((lane & 15) >> 2)) * Sh::kValueRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-#pragma unroll
-    for (int u = 0; u < kSub * 2; ++u)
-#pragma unroll
-      for (int d = 0; d < kOut; ++d) {
-        const uint8_t* at = values + u * 16 * Sh::kValueRow + d * 64;
+    {
+      const uint8_t* values = buffer + kKeys * Sh::kKeyRow + (4 * half + ((lane & 15) >> 2)) * Sh::kValueRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+      auto operand = [&](int k) {  // k = 16-key step * kOut + output tile
+        const uint8_t* at = values + (k / kOut) * 16 * Sh::kValueRow + (k % kOut) * 64;
         union {
           s16x4 h[2];
           bf16x8 v;
         } vf;
         vf.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
         vf.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * Sh::kValueRow));
+        return vf.v;
+      };
+      bf16x8 vf[kAhead];
 #pragma unroll
-        for (int n = NT - 1; n >= 0; --n) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.v, p[n][u], acc[d], 0, 0, 0);
+      for (int k = 0; k < kAhead; ++k) vf[k] = operand(k);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < 2 * kSub * kOut; ++k) {
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n)
+          acc[k % kOut] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k % kAhead], p[n][k / kOut], acc[k % kOut], 0, 0, 0);
+        if (k + kAhead < 2 * kSub * kOut) vf[k % kAhead] = operand(k + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
       uint32_t left = __builtin_amdgcn_readfirstlane((int)bad_keys[third][u]);
