@@ -576,10 +576,12 @@ struct ManyShape {
   static constexpr int kWaves = kHeld <= 256 ? 2 : 1;
 };
 
-// Where a key lies: its codes in the pool, from there its scales, and whether it is there at all.
+// Where a key lies, and its scale bytes.
+template <int KIND, int DP>
 struct alignas(16) Place {
-  int64_t row;
-  int32_t scale, there;
+  static constexpr int kWords = KIND == LLVQ_KV_BF16 ? 1 : DP <= 128 ? 1 : 2;  // of four scale bytes
+  int64_t row;                        // its key codes' offset in the pool
+  uint32_t scales[2][kWords];         // keys', values'
 };
 
 template <int KIND, int DP, int NT>
@@ -590,8 +592,11 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   const Cache& c = a.c;
   __shared__ __align__(16) uint8_t lds[2 * Sh::kBuffer];
   __shared__ uint32_t bad_keys[3][kSub];
-  __shared__ Place places[2][kKeys];
-  __shared__ uint32_t part[2];  // whether a tile has a place that is not there
+  using Where = Place<KIND, DP>;
+  __shared__ Where places[2][kKeys];
+  // of a tile: keys that are not there, and keys with a value that is not finite (in the quantised kinds, where the
+  // scales tell)
+  __shared__ uint64_t missing[2], spoilt[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -638,72 +643,122 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   const bool in_tile = Sh::kChunks >= 256 || tid < Sh::kChunks;  // (kPer is 1 where a tile has fewer)
   const bool narrow = c.dim < DP;                                // rows shorter than the tile's
   const uint8_t* pool = c.pool + (ch * 16 < c.row ? ch * 16 : 0);
-  const int scale_ch = ch * 16 < c.row ? ch * kOf / 4 - ch * 16 : 0;
+  const int scale_shift = KIND == LLVQ_KV_BF16 ? 0 : ch * kOf / 4 % 4 * 8;
+  const int scale_word = KIND == LLVQ_KV_BF16 ? 0 : ch * kOf / 16;
   constexpr int32_t kNoKey = INT32_MIN;
-  int32_t ids = kNoKey;
   u32x4 raw_k[kPer], raw_v[kPer];
   uint32_t sc_k[kPer], sc_v[kPer];
-  int there[kPer];
-  bool lost = false, part_of = false;
-  // Where a tile's keys lie is worked out once a key, by the wave whose turn it is: its page numbers are loaded
-  // four rounds ahead, the places written three rounds ahead and the codes loaded two rounds ahead.
+  uint64_t gone = 0, nonfinite = 0;  // of the loaded tile
+  bool lost = false;
+  // Where a tile's keys lie and how they are scaled is worked out once a key, by the wave whose turn it is: the
+  // page numbers are loaded five rounds ahead, the scales four, both written to LDS three and the codes loaded
+  // two rounds ahead.
+  int32_t ids = kNoKey;
+  Where found;
+  bool found_ok = false;
   auto load_pages = [&](int tile) {
     if (wave != (tile & 3)) return;
     const int j = tile * kKeys + lane;
     ids = lane < kKeys && tile < w.tile_hi && j >= w.first_key && j < w.last_key ? table[divide((uint32_t)j, c.page)] : kNoKey;
   };
-  auto write_places = [&](int tile) {
+  auto load_scales = [&](int tile) {
     if (wave != (tile & 3)) return;
     const uint32_t j = (uint32_t)(tile * kKeys + lane);
-    const bool ok = ids >= 0 && ids < c.pages;
-    lost |= !ok && ids != kNoKey;
+    found_ok = ids >= 0 && ids < c.pages;
+    lost |= !found_ok && ids != kNoKey;
     // a place that is not there is read from the pool's start and left out when it is staged
-    const int slot = ok ? (int)(j - divide(j, c.page) * c.page.by) : 0;
-    if (lane < kKeys)
-      places[tile & 1][lane] = Place{(ok ? (int64_t)ids * page_bytes + head_off : 0) + slot * c.row, c.ks_off + slot * (c.groups - c.row), ok};
-    if (lane == 0) part[tile & 1] = 0;
-    if (__any(lane < kKeys && !ok) && lane == 0) part[tile & 1] = 1;
-  };
-  auto fetch = [&](int tile) {
-    part_of = narrow || __builtin_amdgcn_readfirstlane((int)part[tile & 1]) != 0;
+    const int slot = found_ok ? (int)(j - divide(j, c.page) * c.page.by) : 0;
+    const int64_t blk = found_ok ? (int64_t)ids * page_bytes + head_off : 0;
+    found.row = blk + slot * c.row;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const Place at = places[tile & 1][in_tile ? key0 + i * (256 / kRaw) : 0];
-      const uint8_t* k = pool + at.row;
-      there[i] = at.there;
-      raw_k[i] = *reinterpret_cast<const u32x4*>(k);
-      raw_v[i] = *reinterpret_cast<const u32x4*>(k + c.v_off);
-      if constexpr (KIND != LLVQ_KV_BF16) {
-        const uint8_t* scale = k + (at.scale + scale_ch);
-        sc_k[i] = scale[0];
-        sc_v[i] = scale[c.vs_off - c.ks_off];
-      } else {
-        sc_k[i] = sc_v[i] = 127;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < Where::kWords; ++n) found.scales[i][n] = 0x7f7f7f7fu;
+    if constexpr (KIND != LLVQ_KV_BF16) {
+      if (found_ok) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* sp = c.pool + blk + (i ? c.vs_off : c.ks_off) + slot * c.groups;
+          if (c.groups % 4 == 0) {
+#pragma unroll
+            for (int n = 0; n < Where::kWords; ++n)
+              if (4 * n < c.groups) found.scales[i][n] = *reinterpret_cast<const uint32_t*>(sp + 4 * n);
+          } else {
+#pragma unroll
+            for (int n = 0; n < Where::kWords; ++n) {
+              uint32_t word = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) word |= (uint32_t)(4 * n + e < c.groups ? sp[4 * n + e] : 127) << (8 * e);
+              found.scales[i][n] = word;
+            }
+          }
+        }
       }
     }
   };
-  auto stage = [&](uint8_t* buffer, uint32_t* bad_bits) {
+  auto write_places = [&](int tile) {
+    if (wave != (tile & 3)) return;
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < Where::kWords; ++n) {
+      // a byte of 255 is the only one whose complement is zero
+      const uint32_t v = ~found.scales[1][n];
+      bad |= ((v - 0x01010101u) & ~v & 0x80808080u) != 0;
+    }
+    const uint64_t no = __ballot(!found_ok), spoils = __ballot(bad);
+    if (lane < kKeys) places[tile & 1][lane] = found;
+    if (lane == 0) {
+      missing[tile & 1] = no & (kKeys == 64 ? ~0ull : (1ull << (kKeys % 64)) - 1);
+      spoilt[tile & 1] = spoils & (kKeys == 64 ? ~0ull : (1ull << (kKeys % 64)) - 1);
+    }
+  };
+  auto uniform64 = [](uint64_t x) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+  };
+  auto fetch = [&](int tile) {
+    gone = uniform64(missing[tile & 1]);
+    nonfinite = uniform64(spoilt[tile & 1]);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if (!in_tile) break;
+      const Where at = places[tile & 1][in_tile ? key0 + i * (256 / kRaw) : 0];
+      const uint8_t* k = pool + at.row;
+      raw_k[i] = *reinterpret_cast<const u32x4*>(k);
+      raw_v[i] = *reinterpret_cast<const u32x4*>(k + c.v_off);
+      const int word = Where::kWords == 1 ? 0 : scale_word;
+      sc_k[i] = at.scales[0][word] >> scale_shift & 255;
+      sc_v[i] = at.scales[1][word] >> scale_shift & 255;
+    }
+  };
+  auto stage = [&](uint8_t* buffer, uint32_t* bad_bits) {
+    if (gone != 0 || narrow) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if ((gone >> (key0 + i * (256 / kRaw)) & 1) || ch * 16 >= c.row) raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0}, sc_k[i] = sc_v[i] = 127;
+    }
+    // values that are not finite would spoil rows that do not see them (0 * NaN): they are left out
+    // here and added to the rows that do see them after the tile's products
+    if constexpr (KIND == LLVQ_KV_BF16) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int key = key0 + i * (256 / kRaw);
+        if (drop_nonfinite(&raw_v[i])) atomicOr(&bad_bits[key >> 5], 1u << (key & 31));
+      }
+    } else if (nonfinite != 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (sc_v[i] == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sc_v[i] = 127;
+      if (tid < kSub) bad_bits[tid] = (uint32_t)(nonfinite >> (32 * tid));
+    }
+    if (!in_tile) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
       const int key = key0 + i * (256 / kRaw);
-      u32x4 rk = raw_k[i], rv = raw_v[i], o[kOf];
-      uint32_t sk = sc_k[i], sv = sc_v[i];
-      if (part_of && !(there[i] && ch * 16 < c.row)) rk = rv = u32x4{0, 0, 0, 0}, sk = sv = 127;
-      expand<KIND>(rk, sk, o);
+      u32x4 o[kOf];
+      expand<KIND>(raw_k[i], sc_k[i], o);
 #pragma unroll
       for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(buffer + key * Sh::kKeyRow + (ch * kOf + n) * 16) = o[n];
-      // values that are not finite would spoil rows that do not see them (0 * NaN): they are left out
-      // here and added to the rows that do see them after the tile's products
-      bool bad;
-      if constexpr (KIND == LLVQ_KV_BF16) {
-        bad = drop_nonfinite(&rv);
-      } else {
-        bad = sv == 255;
-        if (bad) rv = u32x4{0, 0, 0, 0}, sv = 127;
-      }
-      expand<KIND>(rv, sv, o);
-      if (bad) atomicOr(&bad_bits[key >> 5], 1u << (key & 31));
+      expand<KIND>(raw_v[i], sc_v[i], o);
 #pragma unroll
       for (int n = 0; n < kOf; ++n)
         *reinterpret_cast<u32x4*>(buffer + kKeys * Sh::kKeyRow + key * Sh::kValueRow + (ch * kOf + n) * 16) = o[n];
@@ -712,10 +767,9 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
 
   if (tid < 3 * kSub) bad_keys[tid / kSub][tid % kSub] = 0;
   if (w.tile_lo < w.tile_hi) {
-    load_pages(w.tile_lo);
-    load_pages(w.tile_lo + 1);
-    load_pages(w.tile_lo + 2);
-    load_pages(w.tile_lo + 3);
+    // (a wave has one tile of four at a time)
+    for (int i = 0; i < 4; ++i) load_pages(w.tile_lo + i);
+    for (int i = 0; i < 4; ++i) load_scales(w.tile_lo + i);
     write_places(w.tile_lo);
     write_places(w.tile_lo + 1);
     __syncthreads();
@@ -724,6 +778,7 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
     fetch(w.tile_lo + 1);
     __syncthreads();
     write_places(w.tile_lo + 2);
+    load_pages(w.tile_lo + 4);
   }
   int third = 0;
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
@@ -731,12 +786,6 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
     const uint8_t* buffer = lds + par * Sh::kBuffer;
     __syncthreads();  // this tile is staged, and the other buffer has been read
     if (tid < kSub) bad_keys[after][tid] = 0;
-    if (tile + 1 < w.tile_hi) {
-      stage(lds + (par ^ 1) * Sh::kBuffer, bad_keys[next]);
-      fetch(tile + 2);
-      write_places(tile + 3);
-      load_pages(tile + 4);
-    }
     const int key_base = tile * kKeys;
     // operands are read a few instructions ahead, in an order that is pinned: left to itself the compiler reads
     // each right before its use and waits for it
@@ -797,6 +846,13 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
 #pragma unroll
         for (int n = 0; n < NT; ++n) p[n][u * 2 + h2] = terms[n];
       }
+    if (tile + 1 < w.tile_hi) {
+      stage(lds + (par ^ 1) * Sh::kBuffer, bad_keys[next]);
+      fetch(tile + 2);
+      write_places(tile + 3);
+      load_scales(tile + 4);
+      load_pages(tile + 5);
+    }
     {
       const uint8_t* values = buffer + kKeys * Sh::kKeyRow + (4 * half + ((lane & 15) >> 2)) * Sh::kValueRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
       auto operand = [&](int k) {  // k = 16-key step * kOut + output tile
