@@ -553,27 +553,41 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   }
 }
 
-// Many rows: 128 rows of a (sequence, key head), 32 columns a wave, tiles shared by the four waves.
+// Many rows: 128 or 256 rows of a (sequence, key head), 32 columns a wave, tiles shared by the four or eight waves.
 //
 // A chunk of a prompt reuses every key for many rows, so the matrix instructions bound it, next to exp and
 // what else the softmax costs on the vector units.  Two waves a SIMD (of two workgroups, or of what registers
 // allow) let one's softmax run under the other's products.  Tiles are double-buffered in LDS: after the one barrier
 // of a round the next tile, whose codes were loaded a round ago, is expanded into the other buffer, the loads of the one after it are issued,
 // and the round's products are taken.  32x32x16 instructions read an operand of 32 keys for 32 columns.
-template <int KIND, int DP, int NT>
+template <int KIND, int DP, int NT, int WAVES>
 struct ManyShape {
+  static constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES;
+  static constexpr int kOutDim = DP < 128 ? DP : 128;        // channels of the output that a workgroup takes
+  static constexpr int kParts = DP / kOutDim;
   static constexpr int kSub = NT == 1 && DP <= 128 ? 2 : 1;  // 32-key pieces of a tile
   static constexpr int kKeys = 32 * kSub;
   // rows padded so that 16 rows at one 16-byte chunk fall on 16 slots of 256 bytes (keys), and four rows
   // at 64 bytes of channels on four segments (values)
-  static constexpr int kKeyRow = DP * 2 + 16, kValueRow = DP * 2 + 64;
+  static constexpr int kKeyRow = DP * 2 + 16, kValueRow = kOutDim * 2 + 64;
   static constexpr int kBuffer = kKeys * (kKeyRow + kValueRow);
-  static constexpr int kRaw = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
-  static constexpr int kChunks = kKeys * kRaw;
-  static constexpr int kPer = (kChunks + 255) / 256;      // chunks a thread stages
-  // registers: queries, outputs, scores, P, chunks in flight
-  static constexpr int kHeld = NT * DP / 4 + DP / 2 + 16 * kSub + 8 * NT * kSub + 14 * kPer + 30;
+  // registers: queries, outputs, scores, P, operands read ahead, chunks in flight
+  static constexpr int kHeld = NT * DP / 4 + kOutDim / 2 + 16 * kSub + 8 * NT * kSub + 16 + 30 +
+                               5 * (kKeys * code_bytes(KIND, DP + kOutDim) / 16 / kThreads);
   static constexpr int kWaves = kHeld <= 256 ? 2 : 1;
+};
+
+// The 16-byte chunks of codes that a thread stages of a tile: chunk `ch` of keys key0, key0 + step, ...
+template <int KIND, int DIM, int KEYS, int THREADS>
+struct Chunks {
+  static constexpr int kRaw = code_bytes(KIND, DIM) / 16, kAll = KEYS * kRaw;
+  static constexpr int kPer = (kAll + THREADS - 1) / THREADS, kStep = THREADS / kRaw;
+  static_assert(THREADS % kRaw == 0 && (kPer == 1 || kAll % THREADS == 0), "a thread has one chunk place in all its rows");
+  int ch, key0;
+  bool any;  // (kPer is 1 where a tile has fewer chunks than threads)
+  __device__ __forceinline__ explicit Chunks(int tid) : ch(tid % kRaw), key0(tid / kRaw), any(kAll >= THREADS || tid < kAll) {
+    if (!any) key0 = 0;
+  }
 };
 
 // Where a key lies, and its scale bytes.
@@ -584,11 +598,13 @@ struct alignas(16) Place {
   uint32_t scales[2][kWords];         // keys', values'
 };
 
-template <int KIND, int DP, int NT>
-__global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn_many(AttnArgs a) {
-  using Sh = ManyShape<KIND, DP, NT>;
-  constexpr int kKeys = Sh::kKeys, kSub = Sh::kSub, kSteps = DP / 16, kOut = DP / 32, kPer = Sh::kPer, kRaw = Sh::kRaw;
+template <int KIND, int DP, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves)) void k_attn_many(AttnArgs a) {
+  using Sh = ManyShape<KIND, DP, NT, WAVES>;
+  constexpr int kKeys = Sh::kKeys, kSub = Sh::kSub, kSteps = DP / 16, kOut = Sh::kOutDim / 32, kRows = Sh::kRows;
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
+  using KChunks = Chunks<KIND, DP, kKeys, Sh::kThreads>;
+  using VChunks = Chunks<KIND, Sh::kOutDim, kKeys, Sh::kThreads>;
   const Cache& c = a.c;
   __shared__ __align__(16) uint8_t lds[2 * Sh::kBuffer];
   __shared__ uint32_t bad_keys[3][kSub];
@@ -605,16 +621,18 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   int id = blockIdx.x;
   const int head = id % c.heads;
   id /= c.heads;
+  const int part = id % Sh::kParts, part_dim = part * Sh::kOutDim;
+  id /= Sh::kParts;
   const int split = id % a.splits;
   id /= a.splits;
   const int rb = a.row_blocks - 1 - id % a.row_blocks;  // the longest rows of a causal chunk first
   const int b = id / a.row_blocks;
   const Seq s = sequence(c, b);
   const int share = (int)a.share.by, rows = s.n * share;
-  if (a.err && tid == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * kManyRows)) atomicAdd(a.err, 1);
-  const int row0 = rb * kManyRows;
+  if (a.err && tid == 0 && head == 0 && split == 0 && part == 0 && rb == 0 && (s.bad || rows > a.row_blocks * kRows)) atomicAdd(a.err, 1);
+  const int row0 = rb * kRows;
   if (row0 >= rows) return;
-  const Span w = span_of(a, s, row0, kManyRows, kKeys, split);
+  const Span w = span_of(a, s, row0, kRows, kKeys, split);
 
   const int row = row0 + wave * 32 + col;
   const bool live = row < rows;
@@ -637,17 +655,18 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
 
   const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
-  // a thread's chunks of a tile: chunk i * 256 + tid is chunk `ch` of key `key0 + i * 256 / kRaw`
-  static_assert(256 % kRaw == 0, "a thread has one chunk place in all its rows");
-  const int ch = tid % kRaw, key0 = tid / kRaw;
-  const bool in_tile = Sh::kChunks >= 256 || tid < Sh::kChunks;  // (kPer is 1 where a tile has fewer)
-  const bool narrow = c.dim < DP;                                // rows shorter than the tile's
-  const uint8_t* pool = c.pool + (ch * 16 < c.row ? ch * 16 : 0);
-  const int scale_shift = KIND == LLVQ_KV_BF16 ? 0 : ch * kOf / 4 % 4 * 8;
-  const int scale_word = KIND == LLVQ_KV_BF16 ? 0 : ch * kOf / 16;
+  const KChunks kc(tid);
+  const VChunks vc(tid);
+  const bool k_in = kc.ch * 16 < c.row, v_in = code_bytes(KIND, part_dim) + vc.ch * 16 < c.row;
+  const bool narrow = c.dim < DP;  // rows shorter than the tile's
+  const uint8_t* k_pool = c.pool + (k_in ? kc.ch * 16 : 0);
+  const uint8_t* v_pool = c.pool + c.v_off + (v_in ? code_bytes(KIND, part_dim) + vc.ch * 16 : 0);
+  // the byte of a place's scales that belongs to the thread's chunks
+  const int k_shift = kc.ch * kOf / 4 % 4 * 8, v_shift = vc.ch * kOf / 4 % 4 * 8;
+  const int k_word = kc.ch * kOf / 16, v_word = part_dim / 128;
   constexpr int32_t kNoKey = INT32_MIN;
-  u32x4 raw_k[kPer], raw_v[kPer];
-  uint32_t sc_k[kPer], sc_v[kPer];
+  u32x4 raw_k[KChunks::kPer], raw_v[VChunks::kPer];
+  uint32_t sc_k[KChunks::kPer], sc_v[VChunks::kPer];
   uint64_t gone = 0, nonfinite = 0;  // of the loaded tile
   bool lost = false;
   // Where a tile's keys lie and how they are scaled is worked out once a key, by the wave whose turn it is: the
@@ -657,12 +676,12 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   Where found;
   bool found_ok = false;
   auto load_pages = [&](int tile) {
-    if (wave != (tile & 3)) return;
+    if (wave != (tile & (WAVES - 1))) return;
     const int j = tile * kKeys + lane;
     ids = lane < kKeys && tile < w.tile_hi && j >= w.first_key && j < w.last_key ? table[divide((uint32_t)j, c.page)] : kNoKey;
   };
   auto load_scales = [&](int tile) {
-    if (wave != (tile & 3)) return;
+    if (wave != (tile & (WAVES - 1))) return;
     const uint32_t j = (uint32_t)(tile * kKeys + lane);
     found_ok = ids >= 0 && ids < c.pages;
     lost |= !found_ok && ids != kNoKey;
@@ -697,7 +716,7 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
     }
   };
   auto write_places = [&](int tile) {
-    if (wave != (tile & 3)) return;
+    if (wave != (tile & (WAVES - 1))) return;
     bool bad = false;
 #pragma unroll
     for (int n = 0; n < Where::kWords; ++n) {
@@ -720,54 +739,66 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
     gone = uniform64(missing[tile & 1]);
     nonfinite = uniform64(spoilt[tile & 1]);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const Where at = places[tile & 1][in_tile ? key0 + i * (256 / kRaw) : 0];
-      const uint8_t* k = pool + at.row;
-      raw_k[i] = *reinterpret_cast<const u32x4*>(k);
-      raw_v[i] = *reinterpret_cast<const u32x4*>(k + c.v_off);
-      const int word = Where::kWords == 1 ? 0 : scale_word;
-      sc_k[i] = at.scales[0][word] >> scale_shift & 255;
-      sc_v[i] = at.scales[1][word] >> scale_shift & 255;
+    for (int i = 0; i < KChunks::kPer; ++i) {
+      const Where* at = &places[tile & 1][kc.key0 + i * KChunks::kStep];
+      raw_k[i] = *reinterpret_cast<const u32x4*>(k_pool + at->row);
+      sc_k[i] = at->scales[0][Where::kWords == 1 ? 0 : k_word] >> k_shift & 255;
+    }
+#pragma unroll
+    for (int i = 0; i < VChunks::kPer; ++i) {
+      const Where* at = &places[tile & 1][vc.key0 + i * VChunks::kStep];
+      raw_v[i] = *reinterpret_cast<const u32x4*>(v_pool + at->row);
+      sc_v[i] = at->scales[1][Where::kWords == 1 ? 0 : v_word] >> v_shift & 255;
     }
   };
   auto stage = [&](uint8_t* buffer, uint32_t* bad_bits) {
     if (gone != 0 || narrow) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if ((gone >> (key0 + i * (256 / kRaw)) & 1) || ch * 16 >= c.row) raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0}, sc_k[i] = sc_v[i] = 127;
+      for (int i = 0; i < KChunks::kPer; ++i)
+        if ((gone >> (kc.key0 + i * KChunks::kStep) & 1) || !k_in) raw_k[i] = u32x4{0, 0, 0, 0}, sc_k[i] = 127;
+#pragma unroll
+      for (int i = 0; i < VChunks::kPer; ++i)
+        if ((gone >> (vc.key0 + i * VChunks::kStep) & 1) || !v_in) raw_v[i] = u32x4{0, 0, 0, 0}, sc_v[i] = 127;
     }
     // values that are not finite would spoil rows that do not see them (0 * NaN): they are left out
     // here and added to the rows that do see them after the tile's products
     if constexpr (KIND == LLVQ_KV_BF16) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int key = key0 + i * (256 / kRaw);
+      for (int i = 0; i < VChunks::kPer; ++i) {
+        const int key = vc.key0 + i * VChunks::kStep;
         if (drop_nonfinite(&raw_v[i])) atomicOr(&bad_bits[key >> 5], 1u << (key & 31));
       }
     } else if (nonfinite != 0) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < VChunks::kPer; ++i)
         if (sc_v[i] == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sc_v[i] = 127;
       if (tid < kSub) bad_bits[tid] = (uint32_t)(nonfinite >> (32 * tid));
     }
-    if (!in_tile) return;
+    u32x4 o[kOf];
+    if (kc.any) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int key = key0 + i * (256 / kRaw);
-      u32x4 o[kOf];
-      expand<KIND>(raw_k[i], sc_k[i], o);
+      for (int i = 0; i < KChunks::kPer; ++i) {
+        expand<KIND>(raw_k[i], sc_k[i], o);
 #pragma unroll
-      for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(buffer + key * Sh::kKeyRow + (ch * kOf + n) * 16) = o[n];
-      expand<KIND>(raw_v[i], sc_v[i], o);
+        for (int n = 0; n < kOf; ++n)
+          *reinterpret_cast<u32x4*>(buffer + (kc.key0 + i * KChunks::kStep) * Sh::kKeyRow + (kc.ch * kOf + n) * 16) = o[n];
+      }
+    }
+    if (vc.any) {
 #pragma unroll
-      for (int n = 0; n < kOf; ++n)
-        *reinterpret_cast<u32x4*>(buffer + kKeys * Sh::kKeyRow + key * Sh::kValueRow + (ch * kOf + n) * 16) = o[n];
+      for (int i = 0; i < VChunks::kPer; ++i) {
+        expand<KIND>(raw_v[i], sc_v[i], o);
+#pragma unroll
+        for (int n = 0; n < kOf; ++n)
+          *reinterpret_cast<u32x4*>(buffer + kKeys * Sh::kKeyRow + (vc.key0 + i * VChunks::kStep) * Sh::kValueRow +
+                                    (vc.ch * kOf + n) * 16) = o[n];
+      }
     }
   };
 
   if (tid < 3 * kSub) bad_keys[tid / kSub][tid % kSub] = 0;
   if (w.tile_lo < w.tile_hi) {
-    // (a wave has one tile of four at a time)
+    // (a wave has one tile of WAVES at a time)
     for (int i = 0; i < 4; ++i) load_pages(w.tile_lo + i);
     for (int i = 0; i < 4; ++i) load_scales(w.tile_lo + i);
     write_places(w.tile_lo);
@@ -891,7 +922,7 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
         for (int d = 0; d < kOut; ++d)
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 x = nonfinite4<KIND>(c, blk, j - (int)(page * c.page.by), d * 32 + i4 * 8 + half * 4);
+            const f32x4 x = nonfinite4<KIND>(c, blk, j - (int)(page * c.page.by), part_dim + d * 32 + i4 * 8 + half * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (sees) acc[d][i4 * 4 + i] += x[i];
@@ -906,7 +937,7 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   if (!live) return;
   const int64_t at = (int64_t)(s.first + t) * c.heads * share + qhead;
   if (a.splits > 1) {
-    if (half == 0) {
+    if (half == 0 && part == 0) {
       const int64_t all = (int64_t)c.tokens * c.heads * share;
       a.stats[(split * all + at) * 2] = m;
       a.stats[(split * all + at) * 2 + 1] = l;
@@ -919,7 +950,7 @@ __global__ __launch_bounds__(256, (ManyShape<KIND, DP, NT>::kWaves)) void k_attn
   for (int d = 0; d < kOut; ++d)
 #pragma unroll
     for (int i4 = 0; i4 < 4; ++i4)
-      store_row4<NT>(a, at, out_at, split, d * 32 + i4 * 8 + half * 4,
+      store_row4<NT>(a, at, out_at, split, part_dim + d * 32 + i4 * 8 + half * 4,
                      f32x4{acc[d][i4 * 4], acc[d][i4 * 4 + 1], acc[d][i4 * 4 + 2], acc[d][i4 * 4 + 3]}, inv);
 }
 

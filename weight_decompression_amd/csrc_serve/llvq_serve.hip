@@ -108,10 +108,10 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
   }
 }
 
-// How a call is cut up: columns of 16 a workgroup of the kernel for few rows holds (0: the kernel for many
-// rows), row blocks and splits of the keys.
+// How a call is cut up: columns of 16 that a workgroup of the kernel for few rows holds, or waves of one of
+// the kernel for many rows (the other is 0), row blocks and splits of the keys.
 struct Cut {
-  int cols, row_blocks, splits;
+  int cols, waves, row_blocks, splits;
 };
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -119,16 +119,17 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, bool f32, Cut* cut) {
   const int64_t rows = (int64_t)max_chunk * share;
   cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1) ? 1 : 2;
-  const int64_t per = cut->cols ? 16 * cut->cols : kManyRows;
+  cut->waves = cut->cols ? 0 : rows <= 128 || f32 ? 4 : 8;
+  const int64_t per = cut->cols ? 16 * cut->cols : 32 * cut->waves;
   const int64_t blocks = (rows + per - 1) / per;
   const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
   if (base > (1ll << 30)) return LLVQ_EINVAL;
-  const int64_t want = ((cut->cols ? 2048 : 1024) + base - 1) / base;
+  const int64_t want = ((cut->cols ? 2048 : 4096 / cut->waves) + base - 1) / base;
   const int64_t most = ((int64_t)max_len + (cut->cols ? 127 : 511)) / (cut->cols ? 128 : 512);
   int64_t s = want < most ? want : most;
   cut->splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
   cut->row_blocks = (int)blocks;
-  return base * cut->splits > 0x7fffffff ? LLVQ_EINVAL : LLVQ_OK;
+  return base * cut->splits > (1 << 30) ? LLVQ_EINVAL : LLVQ_OK;  // (a kernel may take twice as many workgroups)
 }
 
 int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch, int32_t max_chunk, int32_t max_len) {
@@ -140,26 +141,37 @@ int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t bat
   return LLVQ_OK;
 }
 
+template <int KIND, int DP, int NT, int WAVES>
+int launch_many(const AttnArgs& a, unsigned grid, hipStream_t s) {
+  using Sh = ManyShape<KIND, DP, NT, WAVES>;
+  hipLaunchKernelGGL((k_attn_many<KIND, DP, NT, WAVES>), dim3(grid * Sh::kParts), dim3(Sh::kThreads), 0, s, a);
+  return launch_status();
+}
 template <int KIND, int DP, int NT>
-int launch_attn(const AttnArgs& a, int cols, unsigned grid, hipStream_t s) {
-  if (cols == 1)
-    hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
-  else if (cols == 0)
-    hipLaunchKernelGGL((k_attn_many<KIND, DP, NT>), dim3(grid), dim3(256), 0, s, a);
-  else if constexpr (few_pairs(KIND, DP, NT))
-    hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 2>), dim3(grid), dim3(256), 0, s, a);
+int launch_attn(const AttnArgs& a, const Cut& cut, unsigned grid, hipStream_t s) {
+  if (cut.waves == 4) return launch_many<KIND, DP, NT, 4>(a, grid, s);
+  if constexpr (NT == 1) {
+    if (cut.waves == 8) return launch_many<KIND, DP, NT, 8>(a, grid, s);
+  }
+  if constexpr (few_pairs(KIND, DP, NT)) {
+    if (cut.cols == 2) {
+      hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 2>), dim3(grid), dim3(256), 0, s, a);
+      return launch_status();
+    }
+  }
+  hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
   return launch_status();
 }
 template <int KIND, int DP>
-int launch_attn_nt(const AttnArgs& a, bool f32, int cols, unsigned grid, hipStream_t s) {
-  return f32 ? launch_attn<KIND, DP, 3>(a, cols, grid, s) : launch_attn<KIND, DP, 1>(a, cols, grid, s);
+int launch_attn_nt(const AttnArgs& a, bool f32, const Cut& cut, unsigned grid, hipStream_t s) {
+  return f32 ? launch_attn<KIND, DP, 3>(a, cut, grid, s) : launch_attn<KIND, DP, 1>(a, cut, grid, s);
 }
 template <int KIND>
-int launch_attn_dp(const AttnArgs& a, bool f32, int cols, unsigned grid, hipStream_t s) {
+int launch_attn_dp(const AttnArgs& a, bool f32, const Cut& cut, unsigned grid, hipStream_t s) {
   switch (padded_dim(a.c.dim)) {
-    case 64: return launch_attn_nt<KIND, 64>(a, f32, cols, grid, s);
-    case 128: return launch_attn_nt<KIND, 128>(a, f32, cols, grid, s);
-    default: return launch_attn_nt<KIND, 256>(a, f32, cols, grid, s);
+    case 64: return launch_attn_nt<KIND, 64>(a, f32, cut, grid, s);
+    case 128: return launch_attn_nt<KIND, 128>(a, f32, cut, grid, s);
+    default: return launch_attn_nt<KIND, 256>(a, f32, cut, grid, s);
   }
 }
 
@@ -265,9 +277,9 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const unsigned grid = (unsigned)((int64_t)c.batch * cut.row_blocks * cut.splits * c.heads);
   switch (d->kind) {
-    case LLVQ_KV_BF16: st = launch_attn_dp<LLVQ_KV_BF16>(a, f32, cut.cols, grid, s); break;
-    case LLVQ_KV_FP8: st = launch_attn_dp<LLVQ_KV_FP8>(a, f32, cut.cols, grid, s); break;
-    default: st = launch_attn_dp<LLVQ_KV_FP4>(a, f32, cut.cols, grid, s); break;
+    case LLVQ_KV_BF16: st = launch_attn_dp<LLVQ_KV_BF16>(a, f32, cut, grid, s); break;
+    case LLVQ_KV_FP8: st = launch_attn_dp<LLVQ_KV_FP8>(a, f32, cut, grid, s); break;
+    default: st = launch_attn_dp<LLVQ_KV_FP4>(a, f32, cut, grid, s); break;
   }
   if (st != LLVQ_OK || cut.splits == 1) return st;
   return f32 ? launch_join_dim<true>(a, s) : launch_join_dim<false>(a, s);
