@@ -110,19 +110,18 @@ __device__ __forceinline__ bool drop_nonfinite(u32x4* w) {
   return true;
 }
 
-// The sum of a lane's eight p.  bf16 queries: of the rounded values, two at a time, so that what all of a
-// row's roundings have in common cancels.
+// A lane's eight p, added to its four sums.  bf16 queries: the rounded values, two at a time, so that what all
+// of a row's roundings have in common cancels.
 template <int NT>
-__device__ __forceinline__ float sum_p(const float* x, const bf16x8& rounded, float l) {
+__device__ __forceinline__ void sum_p(const float* x, const bf16x8& rounded, float* l4) {
   if constexpr (NT == 1) {
     const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{rounded[2 * e], rounded[2 * e + 1]}, one, l, false);
+    for (int e = 0; e < 4; ++e) l4[e] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{rounded[2 * e], rounded[2 * e + 1]}, one, l4[e], false);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) l += x[e];
+    for (int e = 0; e < 8; ++e) l4[e & 3] += x[e];
   }
-  return l;
 }
 
 // Four channels of a cached value where they are not finite, zero where they are.
@@ -304,11 +303,12 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   }
 
   f32x4 acc[CT][kOut];
-  float m[CT], l[CT];
+  float m[CT], l4[CT][4];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     m[ct] = -INFINITY;
-    l[ct] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l4[ct][i] = 0.0f;
 #pragma unroll
     for (int d = 0; d < kOut; ++d) acc[ct][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -432,7 +432,8 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
         const float next = fmaxf(m[ct], top);
         const float f = m[ct] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[ct] - next);
         m[ct] = next;
-        l[ct] *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l4[ct][i] *= f;
 #pragma unroll
         for (int d = 0; d < kOut; ++d) acc[ct][d] *= f;
       }
@@ -442,7 +443,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
       for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(score[ct][i / 4][i & 3], a.scale_log2, -ms));
       bf16x8 terms[NT];
       split_terms<NT>(x, terms);
-      l[ct] = sum_p<NT>(x, terms[0], l[ct]);
+      sum_p<NT>(x, terms[0], l4[ct]);
 #pragma unroll
       for (int n = 0; n < NT; ++n) p[n][ct] = terms[n];
     }
@@ -513,15 +514,15 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   // the four waves' parts are joined through LDS under their common maximum and added in the waves' order
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    l[ct] = quad_sum(l[ct]);
+    const float l = quad_sum((l4[ct][0] + l4[ct][1]) + (l4[ct][2] + l4[ct][3]));
     __syncthreads();
     if (g == 0) wave_m[wave][col] = m[ct];
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = fmaxf(top, wave_m[i][col]);
-    const float f = m[ct] == -INFINITY ? (l[ct] == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(m[ct] - top);
-    if (g == 0) wave_l[wave][col] = l[ct] * f;
+    const float f = m[ct] == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(m[ct] - top);
+    if (g == 0) wave_l[wave][col] = l * f;
     float* sums = reinterpret_cast<float*>(lds);  // [wave][16 columns][DP], quads of channels swizzled by the column
 #pragma unroll
     for (int d = 0; d < kOut; ++d)
@@ -574,7 +575,10 @@ struct ManyShape {
   // registers: queries, outputs, scores, P, operands read ahead, chunks in flight
   static constexpr int kHeld = NT * DP / 4 + kOutDim / 2 + 16 * kSub + 8 * NT * kSub + 16 + 30 +
                                5 * (kKeys * code_bytes(KIND, DP + kOutDim) / 16 / kThreads);
-  static constexpr int kWaves = kHeld <= 256 ? 2 : 1;
+  // waves a SIMD; narrow heads spend their time on the softmax, not on products, and gain from a third (ragged chunks
+  // of 64-wide heads: 88 us instead of 105)
+  static constexpr int kWaves = DP == 64 && NT == 1 && WAVES == 4 ? 3 : kHeld <= 256 ? 2 : 1;
+  static constexpr int kAhead = DP == 64 ? 2 : 4;            // operands read ahead
 };
 
 // The 16-byte chunks of codes that a thread stages of a tile: chunk `ch` of keys key0, key0 + step, ...
@@ -651,12 +655,13 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   f32x16 acc[kOut];
 #pragma unroll
   for (int i = 0; i < kOut; ++i) acc[i] = f32x16{0.0f};
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (four sums: one chain of additions is slow)
 
   const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  // (where half of the threads have nothing of the keys, they take the values)
   const KChunks kc(tid);
-  const VChunks vc(tid);
+  const VChunks vc(KChunks::kAll <= Sh::kThreads / 2 && VChunks::kAll <= Sh::kThreads / 2 ? tid ^ (Sh::kThreads / 2) : tid);
   const bool k_in = kc.ch * 16 < c.row, v_in = code_bytes(KIND, part_dim) + vc.ch * 16 < c.row;
   const bool narrow = c.dim < DP;  // rows shorter than the tile's
   const uint8_t* k_pool = c.pool + (k_in ? kc.ch * 16 : 0);
@@ -820,7 +825,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     const int key_base = tile * kKeys;
     // operands are read a few instructions ahead, in an order that is pinned: left to itself the compiler reads
     // each right before its use and waits for it
-    constexpr int kAhead = 4;
+    constexpr int kAhead = Sh::kAhead;
     f32x16 sc[kSub];
     {
       const uint8_t* keys = buffer + col * Sh::kKeyRow + half * 16;
@@ -858,7 +863,8 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       const float raised = fmaxf(m, top);
       const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - raised);
       m = raised;
-      l *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l4[i] *= f;
 #pragma unroll
       for (int i = 0; i < kOut; ++i) acc[i] *= f;
     }
@@ -873,10 +879,12 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
         for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][h2 * 8 + e], a.scale_log2, -ms));
         bf16x8 terms[NT];
         split_terms<NT>(x, terms);
-        l = sum_p<NT>(x, terms[0], l);
+        sum_p<NT>(x, terms[0], l4);
 #pragma unroll
         for (int n = 0; n < NT; ++n) p[n][u * 2 + h2] = terms[n];
       }
+    // (the sums are taken here and not, as the compiler would have it, at the end of the round)
+    asm volatile("" : "+v"(l4[0]), "+v"(l4[1]), "+v"(l4[2]), "+v"(l4[3]));
     if (tile + 1 < w.tile_hi) {
       stage(lds + (par ^ 1) * Sh::kBuffer, bad_keys[next]);
       fetch(tile + 2);
@@ -933,7 +941,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 
-  l = half_sum(l);
+  const float l = half_sum((l4[0] + l4[1]) + (l4[2] + l4[3]));
   if (!live) return;
   const int64_t at = (int64_t)(s.first + t) * c.heads * share + qhead;
   if (a.splits > 1) {
