@@ -207,6 +207,26 @@ __device__ __forceinline__ float masked(float s, int j, int lo, int seen) {
   return (uint32_t)(j - lo) < (uint32_t)seen ? s : -INFINITY;
 }
 
+// Four scale bytes of a token (from byte 4 n on; 127, one, past the last), in loads as wide as their place allows.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* sp, int groups, int n) {
+  if (groups % 4 == 0) return 4 * n < groups ? *reinterpret_cast<const uint32_t*>(sp + 4 * n) : 0x7f7f7f7fu;
+  uint32_t word = 0;
+  if (groups % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      word |= (uint32_t)(4 * n + 2 * e < groups ? *reinterpret_cast<const uint16_t*>(sp + 4 * n + 2 * e) : 0x7f7f) << (16 * e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) word |= (uint32_t)(4 * n + e < groups ? sp[4 * n + e] : 127) << (8 * e);
+  }
+  return word;
+}
+// Whether one of four scale bytes is 255, the only one whose complement is zero.
+__device__ __forceinline__ bool has_255(uint32_t word) {
+  const uint32_t v = ~word;
+  return ((v - 0x01010101u) & word & 0x80808080u) != 0;
+}
+
 // Few rows: up to 64 rows of a (sequence, key head), in CT tiles of 16 columns.
 //
 // A decode step reads each cached byte for a handful of rows, so HBM bounds it and what counts is loads
@@ -282,6 +302,74 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   if (row0 >= rows) return;
   const Span w = span_of(a, s, row0, 16 * CT, 128, split);
 
+  const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
+  const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  const int ch = lane % kRaw;  // this lane's chunk of every row that it loads
+  const bool in_row = ch * 16 < c.row;
+  bool lost = false;
+  // the page number of this lane's key of a piece (lanes 32..63 as 0..31)
+  auto page_of = [&](int tile) -> int32_t {
+    const int j = (tile * 4 + wave) * 32 + (lane & 31);
+    if (tile >= w.tile_hi || j < w.first_key || j >= w.last_key) return kNoKey;
+    return table[divide((uint32_t)j, c.page)];
+  };
+  // A lane's key of a piece, lane % 32, tells where the piece's rows lie, and with lane / 32 whose scales it
+  // holds; a lane loads chunk `ch` of keys i * 64 / kRaw + lane / kRaw.
+  constexpr int kWords = KIND == LLVQ_KV_BF16 ? 1 : DP <= 128 ? 1 : 2;  // of four scale bytes
+  constexpr uint32_t kOnes = 0x7f7f7f7fu;
+  const uint8_t* pool = c.pool + (in_row ? ch * 16 : 0);
+  const int scale_shift = KIND == LLVQ_KV_BF16 ? 0 : ch * kOf / 4 % 4 * 8, word_at = KIND == LLVQ_KV_BF16 ? 0 : ch * kOf / 16;
+  const bool narrow = c.dim < DP;  // rows shorter than the tile's
+  int64_t rows_at[kLoads];
+  u32x4 raw_k[kLoads], raw_v[kLoads];
+  uint32_t scales[kWords], next_scales[kWords], gone = 0, next_gone = 0;  // of the piece that is staged, and of the next
+  auto locate = [&](int tile, int32_t ids) {
+    const uint32_t j = (uint32_t)((tile * 4 + wave) * 32 + (lane & 31));
+    const bool ok = ids >= 0 && ids < c.pages;
+    lost |= !ok && ids != kNoKey;
+    next_gone = (uint32_t)__ballot(!ok);
+    // a place that is not there is read from the pool's start and left out when it is staged
+    const int slot = ok ? (int)(j - divide(j, c.page) * c.page.by) : 0;
+    const int64_t blk = ok ? (int64_t)ids * page_bytes + head_off : 0, row = blk + slot * c.row;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int key = (i * kWave + lane) / kRaw;
+      rows_at[i] = (int64_t)(uint32_t)__shfl((int)(uint32_t)row, key) | (int64_t)__shfl((int)(row >> 32), key) << 32;
+    }
+#pragma unroll
+    for (int n = 0; n < kWords; ++n) {
+      next_scales[n] = kOnes;
+      if (KIND != LLVQ_KV_BF16 && ok)
+        next_scales[n] = scale_word(c.pool + blk + (lane < 32 ? c.ks_off : c.vs_off) + slot * c.groups, c.groups, n);
+    }
+  };
+  auto fetch_keys = [&]() {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) raw_k[i] = *reinterpret_cast<const u32x4*>(pool + rows_at[i]);
+  };
+  auto fetch_values = [&]() {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) raw_v[i] = *reinterpret_cast<const u32x4*>(pool + rows_at[i] + c.v_off);
+  };
+  // the scale byte of a chunk: of the keys (from lanes 0..31) or of the values
+  auto scale_of = [&](int key, int is_v) -> uint32_t {
+    if constexpr (KIND == LLVQ_KV_BF16) return 127;
+    uint32_t word = (uint32_t)__shfl((int)scales[0], key + 32 * is_v);
+    if constexpr (kWords == 2) {
+      const uint32_t second = (uint32_t)__shfl((int)scales[kWords - 1], key + 32 * is_v);
+      word = word_at ? second : word;
+    }
+    return word >> scale_shift & 255;
+  };
+
+  int32_t ids = page_of(w.tile_lo);
+  if (w.tile_lo < w.tile_hi) {
+    locate(w.tile_lo, ids);
+    fetch_keys();
+    fetch_values();
+    ids = page_of(w.tile_lo + 1);
+  }
+  // (the queries after the first piece's loads: they are a load away, the piece two)
   int lo[CT], seen[CT], t[CT], qhead[CT];
   bool live[CT];
   bf16x8 q[NT][CT][kSteps];
@@ -313,83 +401,24 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
     for (int d = 0; d < kOut; ++d) acc[ct][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
-  const int32_t* table = c.table + (int64_t)b * c.max_pages;
-  const int ch = lane % kRaw;  // this lane's chunk of every row that it loads
-  const bool in_row = ch * 16 < c.row;
-  bool lost = false;
-  // the page number of this lane's key of a piece (lanes 32..63 as 0..31)
-  auto page_of = [&](int tile) -> int32_t {
-    const int j = (tile * 4 + wave) * 32 + (lane & 31);
-    if (tile >= w.tile_hi || j < w.first_key || j >= w.last_key) return kNoKey;
-    return table[divide((uint32_t)j, c.page)];
-  };
-  // codes and scale bytes of a piece: row i of a lane is key (i * 64 + lane) / kRaw
-  int64_t base[kLoads];
-  int slot[kLoads];
-  bool ok[kLoads];
-  u32x4 raw[2][kLoads];
-  uint32_t sc[2][kLoads];
-  auto locate = [&](int tile, int32_t ids) {
-    lost |= ids >= c.pages || (ids < 0 && ids != kNoKey);
-    const uint32_t j = (uint32_t)((tile * 4 + wave) * 32 + (lane & 31));
-    const int my_slot = (int)(j - divide(j, c.page) * c.page.by);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int key = (i * kWave + lane) / kRaw;
-      const int32_t page = __shfl(ids, key);
-      slot[i] = __shfl(my_slot, key);
-      ok[i] = page >= 0 && page < c.pages && in_row;
-      // a place that is not there is read from the pool's start and left out when it is staged
-      if (!ok[i]) slot[i] = 0;
-      base[i] = ok[i] ? (int64_t)page * page_bytes + head_off : 0;
-    }
-  };
-  auto fetch = [&](int is_v) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint8_t* blk = c.pool + base[i];
-      raw[is_v][i] = *reinterpret_cast<const u32x4*>(blk + (is_v ? c.v_off : 0) + slot[i] * c.row + (ok[i] ? ch * 16 : 0));
-      if constexpr (KIND != LLVQ_KV_BF16)
-        sc[is_v][i] = blk[(is_v ? c.vs_off : c.ks_off) + slot[i] * c.groups + (ok[i] ? ch * kOf / 4 : 0)];
-      else
-        sc[is_v][i] = 127;
-    }
-  };
-  bool part_k = false, part_v = false;  // whether a place of the loaded piece is not there
-
-  int32_t ids = page_of(w.tile_lo);
-  bool there_k[kLoads], there_v[kLoads];
-  auto note = [&](bool* there, bool* part) {
-    bool all = true;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      there[i] = ok[i];
-      all &= ok[i];
-    }
-    *part = !__all(all);
-  };
-  if (w.tile_lo < w.tile_hi) {
-    locate(w.tile_lo, ids);
-    note(there_k, &part_k);
-    note(there_v, &part_v);
-    fetch(0);
-    fetch(1);
-    ids = page_of(w.tile_lo + 1);
-  }
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
     const int key_base = (tile * 4 + wave) * 32;
     const bool more = tile + 1 < w.tile_hi;
     // the keys
+    gone = next_gone;
+#pragma unroll
+    for (int n = 0; n < kWords; ++n) scales[n] = next_scales[n];
+    if (gone != 0 || narrow) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if ((gone >> ((i * kWave + lane) / kRaw) & 1) || !in_row) raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0};
+    }
     wave_order();
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int key = (i * kWave + lane) / kRaw;
-      u32x4 r = raw[0][i];
-      uint32_t sb = sc[0][i];
-      if (part_k && !there_k[i]) r = u32x4{0, 0, 0, 0}, sb = 127;
       u32x4 o[kOf];
-      expand<KIND>(r, sb, o);
+      expand<KIND>(raw_k[i], scale_of(key, 0), o);
 #pragma unroll
       for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(mine + key * Lds::kKeyRow + (ch * kOf + n) * 16) = o[n];
     }
@@ -397,8 +426,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
     if (more) {
       locate(tile + 1, ids);
       ids = page_of(tile + 2);
-      note(there_k, &part_k);
-      fetch(0);
+      fetch_keys();
     }
     f32x4 score[CT][2];
 #pragma unroll
@@ -447,33 +475,37 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
 #pragma unroll
       for (int n = 0; n < NT; ++n) p[n][ct] = terms[n];
     }
-    // the values, in the keys' place
-    uint32_t bad = 0;
+    // the values, in the keys' place.  Those that are not finite would spoil rows that do not see them
+    // (0 * NaN): they are left out here and added to the rows that do see them after the products
+    uint32_t bad = 0;  // keys that have one
+    if constexpr (KIND == LLVQ_KV_BF16) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (drop_nonfinite(&raw_v[i])) bad |= 1u << ((i * kWave + lane) / kRaw);
+      if (__any(bad != 0)) {
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) bad |= (uint32_t)__shfl_xor((int)bad, d);
+      }
+      bad = (uint32_t)__builtin_amdgcn_readfirstlane((int)bad);
+    } else {
+      bool spoilt = false;
+#pragma unroll
+      for (int n = 0; n < kWords; ++n) spoilt |= has_255(scales[n]);
+      bad = (uint32_t)(__ballot(spoilt) >> 32);
+    }
     wave_order();
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int key = (i * kWave + lane) / kRaw;
-      u32x4 r = raw[1][i];
-      uint32_t sb = sc[1][i];
-      if (part_v && !there_v[i]) r = u32x4{0, 0, 0, 0}, sb = 127;
+      uint32_t sb = scale_of(key, 1);
+      if (KIND != LLVQ_KV_BF16 && bad != 0 && sb == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sb = 127;
       u32x4 o[kOf];
-      bool spoilt;
-      if constexpr (KIND == LLVQ_KV_BF16) {
-        spoilt = drop_nonfinite(&r);
-      } else {
-        spoilt = sb == 255;
-        if (spoilt) r = u32x4{0, 0, 0, 0}, sb = 127;
-      }
-      if (spoilt) bad |= 1u << key;
-      expand<KIND>(r, sb, o);
+      expand<KIND>(raw_v[i], sb, o);
 #pragma unroll
       for (int n = 0; n < kOf; ++n) *reinterpret_cast<u32x4*>(mine + key * Lds::kValueRow + (ch * kOf + n) * 16) = o[n];
     }
     wave_order();
-    if (more) {
-      note(there_v, &part_v);
-      fetch(1);
-    }
+    if (more) fetch_values();
 #pragma unroll
     for (int d = 0; d < kOut; ++d) {
       const uint8_t* at = mine + (4 * g + ((lane & 15) >> 2)) * Lds::kValueRow + d * 32 + (lane & 3) * 8;
@@ -488,24 +520,18 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n) acc[ct][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf.v, p[n][ct], acc[ct][d], 0, 0, 0);
     }
-    // values that are not finite were left out (0 * NaN would spoil rows that do not see them) and are
-    // added to the rows that do
-    if (__any(bad != 0)) {
+    while (bad) {
+      const int key = __builtin_ctz(bad), j = key_base + key;
+      bad &= bad - 1;
+      const uint32_t page = divide((uint32_t)j, c.page);
+      const int slot = j - (int)(page * c.page.by);
+      const uint8_t* blk = c.pool + (int64_t)table[page] * page_bytes + head_off;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) bad |= (uint32_t)__shfl_xor((int)bad, d);
-      while (bad) {
-        const int key = __builtin_ctz(bad), j = key_base + key;
-        bad &= bad - 1;
-        const uint32_t page = divide((uint32_t)j, c.page);
-        const int at = j - (int)(page * c.page.by);
-        const uint8_t* blk = c.pool + (int64_t)table[page] * page_bytes + head_off;
+      for (int d = 0; d < kOut; ++d) {
+        const f32x4 x = nonfinite4<KIND>(c, blk, slot, d * 16 + 4 * g);
 #pragma unroll
-        for (int d = 0; d < kOut; ++d) {
-          const f32x4 x = nonfinite4<KIND>(c, blk, at, d * 16 + 4 * g);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            if ((uint32_t)(j - lo[ct]) < (uint32_t)seen[ct]) acc[ct][d] += x;
-        }
+        for (int ct = 0; ct < CT; ++ct)
+          if ((uint32_t)(j - lo[ct]) < (uint32_t)seen[ct]) acc[ct][d] += x;
       }
     }
   }
@@ -701,22 +727,10 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     if constexpr (KIND != LLVQ_KV_BF16) {
       if (found_ok) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* sp = c.pool + blk + (i ? c.vs_off : c.ks_off) + slot * c.groups;
-          if (c.groups % 4 == 0) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int n = 0; n < Where::kWords; ++n)
-              if (4 * n < c.groups) found.scales[i][n] = *reinterpret_cast<const uint32_t*>(sp + 4 * n);
-          } else {
-#pragma unroll
-            for (int n = 0; n < Where::kWords; ++n) {
-              uint32_t word = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) word |= (uint32_t)(4 * n + e < c.groups ? sp[4 * n + e] : 127) << (8 * e);
-              found.scales[i][n] = word;
-            }
-          }
-        }
+          for (int n = 0; n < Where::kWords; ++n)
+            found.scales[i][n] = scale_word(c.pool + blk + (i ? c.vs_off : c.ks_off) + slot * c.groups, c.groups, n);
       }
     }
   };
@@ -724,11 +738,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     if (wave != (tile & (WAVES - 1))) return;
     bool bad = false;
 #pragma unroll
-    for (int n = 0; n < Where::kWords; ++n) {
-      // a byte of 255 is the only one whose complement is zero
-      const uint32_t v = ~found.scales[1][n];
-      bad |= ((v - 0x01010101u) & ~v & 0x80808080u) != 0;
-    }
+    for (int n = 0; n < Where::kWords; ++n) bad |= has_255(found.scales[1][n]);
     const uint64_t no = __ballot(!found_ok), spoils = __ballot(bad);
     if (lane < kKeys) places[tile & 1][lane] = found;
     if (lane == 0) {
