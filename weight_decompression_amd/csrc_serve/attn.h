@@ -989,10 +989,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const int64_t rows = (int64_t)c.tokens * heads, row = ((int64_t)blockIdx.x * 4 + wave) / WAVES;
   const bool in = row < rows;
   const int64_t t = in ? row / heads : 0, head = in ? row - t * heads : 0;
-  // rows that belong to no sequence are not written
-  const int b = sequence_of(c, (int)t);
-  const Seq s = b < c.batch ? sequence(c, b) : Seq{0, 0, 0, true};
-  const bool live = in && t >= s.first && t < s.first + s.n;
+  // (rows that belong to no sequence are not written)
+  const bool live = in && t >= c.starts[0] && t < c.starts[c.batch];
 
   float ms[2], ls[2], f[2];
 #pragma unroll

@@ -24,7 +24,7 @@ struct DraftArgs {
   const int32_t* counts;    // [batch] or null
   const float* uniforms;    // [batch][drafts]
   const float* noise;       // [batch][vocab]
-  uint64_t* keys;           // [batch][parts][2]
+  uint64_t* keys;           // [batch][parts]
   int32_t* accepted;
   int32_t* out;             // [batch][drafts + 1]
   int32_t* err;
@@ -61,13 +61,27 @@ __device__ __forceinline__ int accepted_of(const DraftArgs& a, int b, bool* bad)
   return no ? __builtin_ctzll(no) : kWave;
 }
 
-__device__ __forceinline__ uint64_t score_key(float w, float e, int v) {
-  if (!(w > 0.0f) || !(e >= 0.0f)) return 0;
-  const float s = __fdiv_rn(w, e);
-  if (!(s >= 0.0f)) return 0;
+// A draw's best so far: its score and index.  Entries come in ascending order of the index.
+struct Best {
+  float score = 0.0f;
+  int at = -1;
+
+  // Whether w / e may pass the score: at most one entry in a few hundred does, so the division is only taken
+  // for those.  fl(w / e) > score needs w > score * e * (1 - 2^-24); the product's own rounding is 2^-24 (not where it is
+  // subnormal: the test is passed there), and the factor below leaves room for both.
+  __device__ __forceinline__ bool may(float w, float e) const {
+    const float t = score * e;
+    return w > 0.0f && e >= 0.0f && !(w < t * 0.999999f && t > 1e-30f);
+  }
+  __device__ __forceinline__ void take(float w, float e, int v) {
+    const float s = __fdiv_rn(w, e);
+    if (s > score || (at < 0 && s >= 0.0f)) score = s, at = v;
+  }
   // bit 31 (a score has no sign) marks the key as one of a candidate
-  return (uint64_t)(__float_as_uint(s) | 0x80000000u) << 32 | (0xffffffffu - (uint32_t)v);
-}
+  __device__ __forceinline__ uint64_t key() const {
+    return at < 0 ? 0 : (uint64_t)(__float_as_uint(score) | 0x80000000u) << 32 | (0xffffffffu - (uint32_t)at);
+  }
+};
 
 __device__ __forceinline__ uint64_t wave_max(uint64_t k) {
 #pragma unroll
@@ -89,49 +103,72 @@ __global__ __launch_bounds__(256) void k_draft_part(DraftArgs a) {
   const int64_t qrow = ((int64_t)b * a.drafts + done) * a.vocab;
   const int certain = !all && !a.draft ? a.tokens[(int64_t)b * a.drafts + done] : -1;
   const bool take = !all && a.draft;
+  const float* noise = a.noise + (int64_t)b * a.vocab;
   const int64_t from = (int64_t)part * a.per;
   const int64_t end = min(from + a.per, (int64_t)a.vocab);
-  uint64_t rest = 0, plain = 0;
-  for (int64_t v = from + tid; v < end; v += 256) {
-    const float p = prob<F32>(a.target, row + v);
-    const float e = a.noise[(int64_t)b * a.vocab + v];
-    float w = p;
-    if (take) w -= prob<F32>(a.draft, qrow + v);
-    if ((int)v == certain) w = 0.0f;
-    const uint64_t kr = score_key(w, e, (int)v), kp = score_key(p, e, (int)v);
-    rest = kr > rest ? kr : rest;
-    plain = kp > plain ? kp : plain;
+  constexpr int kAhead = 8;
+  Best rest;
+  for (int64_t v0 = from + tid; v0 < end; v0 += 256 * kAhead) {
+    float w[kAhead], e[kAhead], q[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t v = v0 + 256 * i;
+      const bool in = v < end;
+      w[i] = in ? prob<F32>(a.target, row + v) : 0.0f;
+      e[i] = in ? noise[v] : 1.0f;
+      q[i] = in && take ? prob<F32>(a.draft, qrow + v) : 0.0f;
+    }
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      w[i] = (int)(v0 + 256 * i) == certain ? 0.0f : w[i] - q[i];
+      any |= rest.may(w[i], e[i]);
+    }
+    if (any) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (rest.may(w[i], e[i])) rest.take(w[i], e[i], (int)(v0 + 256 * i));
+    }
   }
-  __shared__ uint64_t best[2][4];
-  rest = wave_max(rest);
-  plain = wave_max(plain);
-  if ((tid & 63) == 0) best[0][tid >> 6] = rest, best[1][tid >> 6] = plain;
+  __shared__ uint64_t best[4];
+  const uint64_t k = wave_max(rest.key());
+  if ((tid & 63) == 0) best[tid >> 6] = k;
   __syncthreads();
-  if (tid < 2) {
-    uint64_t k = 0;
-    for (int i = 0; i < 4; ++i) k = best[tid][i] > k ? best[tid][i] : k;
-    a.keys[((int64_t)b * a.parts + part) * 2 + tid] = k;
+  if (tid == 0) {
+    uint64_t top = best[0];
+    for (int i = 1; i < 4; ++i) top = best[i] > top ? best[i] : top;
+    a.keys[(int64_t)b * a.parts + part] = top;
   }
 }
 
 template <bool F32>
-__global__ __launch_bounds__(64) void k_draft_pick(DraftArgs a) {
-  const int b = blockIdx.x, lane = threadIdx.x;
+__global__ __launch_bounds__(256) void k_draft_pick(DraftArgs a) {
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   bool bad;
   const int done = accepted_of<F32>(a, b, &bad);
-  uint64_t rest = 0, plain = 0;
+  __shared__ uint64_t best[4];
+  uint64_t k = 0;
   for (int i = lane; i < a.parts; i += 64) {
-    const uint64_t* k = a.keys + ((int64_t)b * a.parts + i) * 2;
-    rest = k[0] > rest ? k[0] : rest;
-    plain = k[1] > plain ? k[1] : plain;
+    const uint64_t x = a.keys[(int64_t)b * a.parts + i];
+    k = x > k ? x : k;
   }
-  rest = wave_max(rest);
-  plain = wave_max(plain);
-  const uint64_t k = rest ? rest : plain;
+  k = wave_max(k);
+  if (k == 0) {  // the rest is empty: the target alone (the same in every wave)
+    const int64_t row = ((int64_t)b * (a.drafts + 1) + done) * a.vocab;
+    Best whole;
+    for (int64_t v = tid; v < a.vocab; v += 256) {
+      const float w = prob<F32>(a.target, row + v), e = a.noise[(int64_t)b * a.vocab + v];
+      if (whole.may(w, e)) whole.take(w, e, (int)v);
+    }
+    k = wave_max(whole.key());
+    if (lane == 0) best[tid >> 6] = k;
+    __syncthreads();
+    for (int i = 0; i < 4; ++i) k = best[i] > k ? best[i] : k;
+  }
   const int last = k ? (int)(0xffffffffu - (uint32_t)k) : -1;
-  for (int i = lane; i <= a.drafts; i += 64)
+  for (int i = tid; i <= a.drafts; i += 256)
     a.out[(int64_t)b * (a.drafts + 1) + i] = i < done ? a.tokens[(int64_t)b * a.drafts + i] : i == done ? last : -1;
-  if (lane == 0) {
+  if (tid == 0) {
     a.accepted[b] = done;
     if (a.err && (bad || !k)) atomicAdd(a.err, 1);
   }

@@ -86,39 +86,66 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float* x) {
   }
 }
 
-template <int KIND, bool F32, bool VEC>
-__global__ __launch_bounds__(256) void k_kv_write(Cache c, KvRows in, int per_wave, int items, int32_t* err) {
+// The places of a wave's PW tokens, and how many have none.
+template <int PW>
+struct Places {
+  int64_t base[PW];
+  int slot[PW];
+  bool there[PW];
+  int wrong = 0;
+  __device__ __forceinline__ Places(const Cache& c, int64_t first) {
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      base[i] = 0;
+      slot[i] = 0;
+      there[i] = false;
+      if (first + i < c.tokens) {
+        bool bad;
+        there[i] = place_of(c, (int)(first + i), &base[i], &slot[i], &bad);
+        wrong += bad;
+      }
+    }
+  }
+};
+
+// An item: 8 channels of one head's key or value.
+struct Item {
+  bool is_v;
+  int head, ch;
+};
+__device__ __forceinline__ Item item_of(const Cache& c, int it, const Divider& chunks) {
+  const int hv = (int)divide((uint32_t)it, chunks);
+  const bool is_v = hv >= c.heads;
+  return {is_v, is_v ? hv - c.heads : hv, it - hv * (int)chunks.by};
+}
+
+template <int KIND, bool F32, bool VEC, int PW>
+__global__ __launch_bounds__(256) void k_kv_write(Cache c, KvRows in, Divider chunks, int items, int32_t* err) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int chunks = c.dim / 8;
-  int wrong = 0;
-  for (int i = 0; i < per_wave; ++i) {
-    const int64_t tok = ((int64_t)blockIdx.x * 4 + wave) * per_wave + i;
-    if (tok >= c.tokens) break;
-    const int t = (int)tok;
-    int64_t base = 0;
-    int slot = 0;
-    bool bad = false;
-    const bool there = place_of(c, t, &base, &slot, &bad);
-    if (bad && blockIdx.y == 0) ++wrong;
-    if (!there) continue;
-    for (int it = (int)blockIdx.y * kWave + lane; it < items; it += (int)gridDim.y * kWave) {
-      const int hv = it / chunks, ch = it - hv * chunks;
-      const bool is_v = hv >= c.heads;
-      const int head = is_v ? hv - c.heads : hv;
-      float x[8];
-      load8<F32, VEC>(is_v ? in.v : in.k,
-                      (int64_t)t * (is_v ? in.v_token : in.k_token) + (int64_t)head * (is_v ? in.v_head : in.k_head) + ch * 8, x);
-      uint8_t* blk = c.pool + base + (int64_t)head * c.block;
-      uint8_t* dst = blk + (is_v ? c.v_off : 0) + slot * c.row;
+  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * PW;
+  const Places<PW> at(c, first);
+  if (err && at.wrong && blockIdx.y == 0 && lane == 0) atomicAdd(err, at.wrong);
+  for (int it = (int)blockIdx.y * kWave + lane; it < items; it += (int)gridDim.y * kWave) {
+    const Item m = item_of(c, it, chunks);
+    const int64_t from = (int64_t)m.head * (m.is_v ? in.v_head : in.k_head) + m.ch * 8;
+    float x[PW][8];
+#pragma unroll
+    for (int i = 0; i < PW; ++i)
+      if (at.there[i]) load8<F32, VEC>(m.is_v ? in.v : in.k, (first + i) * (m.is_v ? in.v_token : in.k_token) + from, x[i]);
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      if (!at.there[i]) continue;
+      uint8_t* blk = c.pool + at.base[i] + (int64_t)m.head * c.block;
+      uint8_t* dst = blk + (m.is_v ? c.v_off : 0) + at.slot[i] * c.row;
       if constexpr (KIND == LLVQ_KV_BF16) {
-        store8<false, true>(dst, ch * 8, x);
+        store8<false, true>(dst, m.ch * 8, x[i]);
       } else {
         // the group's largest magnitude over its four lanes, as bits: a NaN's and an infinity's are the
         // largest of all
         uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
         top = max(top, (uint32_t)__shfl_xor((int)top, 1));
         top = max(top, (uint32_t)__shfl_xor((int)top, 2));
         const bool nonfinite = top >= 0x7f800000u;
@@ -130,94 +157,98 @@ __global__ __launch_bounds__(256) void k_kv_write(Cache c, KvRows in, int per_wa
         int e = (int)(top >> 23) - 127 - kExp + ((top & 0x7fffffu) > kMant ? 1 : 0);
         e = min(max(e, -100), kHigh);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = nonfinite ? 0.0f : fminf(fmaxf(x[j] * inv, -kTop), kTop);
+        for (int j = 0; j < 8; ++j) y[j] = nonfinite ? 0.0f : fminf(fmaxf(x[i][j] * inv, -kTop), kTop);
         if constexpr (KIND == LLVQ_KV_FP8) {
-          int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
-          lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
-          int hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
-          hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
-          *reinterpret_cast<u32x2*>(dst + ch * 8) = u32x2{(uint32_t)lo, (uint32_t)hi};
+          int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+          lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+          int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+          hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+          *reinterpret_cast<u32x2*>(dst + m.ch * 8) = u32x2{(uint32_t)lo, (uint32_t)hi};
         } else {
           uint32_t w = 0;
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], 1.0f, 0);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], 1.0f, 1);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], 1.0f, 2);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], 1.0f, 3);
-          *reinterpret_cast<uint32_t*>(dst + ch * 4) = w;
+          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[0], y[1], 1.0f, 0);
+          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 1.0f, 1);
+          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], 1.0f, 2);
+          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], 1.0f, 3);
+          *reinterpret_cast<uint32_t*>(dst + m.ch * 4) = w;
         }
-        if ((ch & 3) == 0) {
-          blk[(is_v ? c.vs_off : c.ks_off) + slot * c.groups + (ch >> 2)] = (uint8_t)(nonfinite ? 255 : e + 127);
+        if ((m.ch & 3) == 0) {
+          blk[(m.is_v ? c.vs_off : c.ks_off) + at.slot[i] * c.groups + (m.ch >> 2)] = (uint8_t)(nonfinite ? 255 : e + 127);
           if (nonfinite && err) atomicAdd(err, 1);
         }
       }
     }
   }
-  if (wrong && err && lane == 0) atomicAdd(err, wrong);
 }
 
-// 8 values of one token from its codes and scale byte.
+// 8 values from their codes and scale byte.
 template <int KIND>
-__device__ __forceinline__ void values8(const uint8_t* codes, uint32_t scale_byte, float* x) {
+__device__ __forceinline__ void values8(const u32x4 codes, uint32_t scale_byte, float* x) {
+  // a byte of 255 is an infinite f32, which the conversions turn into NaN for every code
+  const float scale = __uint_as_float(scale_byte << 23);
+  uint32_t u[4];
   if constexpr (KIND == LLVQ_KV_BF16) {
-    load8<false, true>(codes, 0, x);
-  } else {
-    // a byte of 255 is an infinite f32, which the conversions turn into NaN for every code
-    const float scale = __uint_as_float(scale_byte << 23);
-    bf16x2 p[4];
-    if constexpr (KIND == LLVQ_KV_FP8) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(codes);
-      p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, false);
-      p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, true);
-      p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], scale, false);
-      p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], scale, true);
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes);
-      p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
-      p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
-      p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
-      p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, p[i]);
-      x[2 * i] = __uint_as_float(u << 16);
-      x[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) u[i] = codes[i];
+  } else if constexpr (KIND == LLVQ_KV_FP8) {
+    u[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[0], scale, false));
+    u[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[0], scale, true));
+    u[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[1], scale, false));
+    u[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[1], scale, true));
+  } else {
+    u[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[0], scale, 0));
+    u[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[0], scale, 1));
+    u[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[0], scale, 2));
+    u[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[0], scale, 3));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
 
-template <int KIND, bool F32, bool VEC>
-__global__ __launch_bounds__(256) void k_kv_read(Cache c, KvRows out, int per_wave, int items, int32_t* err) {
+template <int KIND, bool F32, bool VEC, int PW>
+__global__ __launch_bounds__(256) void k_kv_read(Cache c, KvRows out, Divider chunks, int items, int32_t* err) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int chunks = c.dim / 8;
-  int wrong = 0;
-  for (int i = 0; i < per_wave; ++i) {
-    const int64_t tok = ((int64_t)blockIdx.x * 4 + wave) * per_wave + i;
-    if (tok >= c.tokens) break;
-    const int t = (int)tok;
-    int64_t base = 0;
-    int slot = 0;
-    bool bad = false;
-    const bool there = place_of(c, t, &base, &slot, &bad);
-    if (bad && blockIdx.y == 0) ++wrong;
-    for (int it = (int)blockIdx.y * kWave + lane; it < items; it += (int)gridDim.y * kWave) {
-      const int hv = it / chunks, ch = it - hv * chunks;
-      const bool is_v = hv >= c.heads;
-      const int head = is_v ? hv - c.heads : hv;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (there) {
-        const uint8_t* blk = c.pool + base + (int64_t)head * c.block;
-        uint32_t s = 0;
-        if constexpr (KIND != LLVQ_KV_BF16) s = blk[(is_v ? c.vs_off : c.ks_off) + slot * c.groups + (ch >> 2)];
-        values8<KIND>(blk + (is_v ? c.v_off : 0) + slot * c.row + code_bytes(KIND, ch * 8), s, x);
+  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * PW;
+  const Places<PW> at(c, first);
+  if (err && at.wrong && blockIdx.y == 0 && lane == 0) atomicAdd(err, at.wrong);
+  for (int it = (int)blockIdx.y * kWave + lane; it < items; it += (int)gridDim.y * kWave) {
+    const Item m = item_of(c, it, chunks);
+    const int64_t to = (int64_t)m.head * (m.is_v ? out.v_head : out.k_head) + m.ch * 8;
+    u32x4 codes[PW];
+    uint32_t scale[PW];
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      codes[i] = u32x4{0, 0, 0, 0};  // what has no place reads as zeros
+      scale[i] = 127;
+      if (!at.there[i]) continue;
+      const uint8_t* blk = c.pool + at.base[i] + (int64_t)m.head * c.block;
+      const uint8_t* src = blk + (m.is_v ? c.v_off : 0) + at.slot[i] * c.row + code_bytes(KIND, m.ch * 8);
+      if constexpr (KIND == LLVQ_KV_BF16) {
+        codes[i] = *reinterpret_cast<const u32x4*>(src);
+      } else {
+        if constexpr (KIND == LLVQ_KV_FP8) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(src);
+          codes[i][0] = w[0], codes[i][1] = w[1];
+        } else {
+          codes[i][0] = *reinterpret_cast<const uint32_t*>(src);
+        }
+        scale[i] = blk[(m.is_v ? c.vs_off : c.ks_off) + at.slot[i] * c.groups + (m.ch >> 2)];
       }
-      store8<F32, VEC>(const_cast<void*>(is_v ? out.v : out.k),
-                       (int64_t)t * (is_v ? out.v_token : out.k_token) + (int64_t)head * (is_v ? out.v_head : out.k_head) + ch * 8, x);
+    }
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      if (first + i >= c.tokens) break;
+      float x[8];
+      values8<KIND>(codes[i], scale[i], x);
+      store8<F32, VEC>(const_cast<void*>(m.is_v ? out.v : out.k), (first + i) * (m.is_v ? out.v_token : out.k_token) + to, x);
     }
   }
-  if (wrong && err && lane == 0) atomicAdd(err, wrong);
 }
 
 }  // namespace serve

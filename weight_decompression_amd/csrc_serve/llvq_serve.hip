@@ -64,21 +64,21 @@ bool wide(const void* p, int64_t token, int64_t head, int bytes) {
   return aligned(p, 16) && (token * bytes) % 16 == 0 && (head * bytes) % 16 == 0;
 }
 
-template <int KIND, bool WRITE>
+template <int KIND, bool WRITE, int PW>
 int launch_kv(const Cache& c, const KvRows& r, bool f32, bool vec, int32_t* err, hipStream_t s) {
   const int items = 2 * c.heads * (c.dim / 8);
-  // One token a wave while that leaves compute units idle, four after that
-  const int per_wave = c.tokens >= 16384 ? 4 : 1;
-  const unsigned gx = (unsigned)((c.tokens + 4ll * per_wave - 1) / (4ll * per_wave));
+  const Divider chunks = make_divider((uint32_t)(c.dim / 8));
+  const unsigned gx = (unsigned)((c.tokens + 4ll * PW - 1) / (4ll * PW));
   const unsigned parts = (unsigned)((items + kWave - 1) / kWave);
-  const unsigned gy = c.tokens >= 4096 ? (parts + 3) / 4 : parts;
+  // a wave has one item of each token while that leaves it few workgroups, up to four after that
+  const unsigned gy = (uint64_t)gx * parts >= 16384 ? (parts + 3) / 4 : parts;
   const dim3 grid(gx, gy > 65535 ? 65535 : gy);
-#define LLVQ_KV_CASE(F32, VEC)                                                                              \
-  if (f32 == F32 && vec == VEC) {                                                                           \
-    if constexpr (WRITE)                                                                                    \
-      hipLaunchKernelGGL((k_kv_write<KIND, F32, VEC>), grid, dim3(256), 0, s, c, r, per_wave, items, err);  \
-    else                                                                                                    \
-      hipLaunchKernelGGL((k_kv_read<KIND, F32, VEC>), grid, dim3(256), 0, s, c, r, per_wave, items, err);   \
+#define LLVQ_KV_CASE(F32, VEC)                                                                                \
+  if (f32 == F32 && vec == VEC) {                                                                             \
+    if constexpr (WRITE)                                                                                      \
+      hipLaunchKernelGGL((k_kv_write<KIND, F32, VEC, PW>), grid, dim3(256), 0, s, c, r, chunks, items, err);  \
+    else                                                                                                      \
+      hipLaunchKernelGGL((k_kv_read<KIND, F32, VEC, PW>), grid, dim3(256), 0, s, c, r, chunks, items, err);   \
   }
   LLVQ_KV_CASE(false, false) LLVQ_KV_CASE(false, true) LLVQ_KV_CASE(true, false) LLVQ_KV_CASE(true, true)
 #undef LLVQ_KV_CASE
@@ -101,11 +101,15 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
   const bool vec = wide(k, k_token, k_head, size) && wide(v, v_token, v_head, size);
   const KvRows r = {k, v, k_token, k_head, v_token, v_head};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  // Four tokens a wave once that fills the chip: four loads in flight, and neighbours of a page written together
+  const bool four = (int64_t)c.tokens * c.heads * c.dim >= 1 << 22;
+#define LLVQ_KV_KIND(KIND) four ? launch_kv<KIND, WRITE, 4>(c, r, f32, vec, err, s) : launch_kv<KIND, WRITE, 1>(c, r, f32, vec, err, s)
   switch (d->kind) {
-    case LLVQ_KV_BF16: return launch_kv<LLVQ_KV_BF16, WRITE>(c, r, f32, vec, err, s);
-    case LLVQ_KV_FP8: return launch_kv<LLVQ_KV_FP8, WRITE>(c, r, f32, vec, err, s);
-    default: return launch_kv<LLVQ_KV_FP4, WRITE>(c, r, f32, vec, err, s);
+    case LLVQ_KV_BF16: return LLVQ_KV_KIND(LLVQ_KV_BF16);
+    case LLVQ_KV_FP8: return LLVQ_KV_KIND(LLVQ_KV_FP8);
+    default: return LLVQ_KV_KIND(LLVQ_KV_FP4);
   }
+#undef LLVQ_KV_KIND
 }
 
 // How a call is cut up: columns of 16 that a workgroup of the kernel for few rows holds, or waves of one of
@@ -127,7 +131,14 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
   if (base > (1ll << 30)) return LLVQ_EINVAL;
   const int64_t made = cut->cols || d->head_dim <= 128 ? base : 2 * base;  // (wide heads in halves)
-  const int64_t want = ((cut->cols ? 2048 : 4096 / cut->waves) + made - 1) / made;
+  int64_t want = ((cut->cols ? 2048 : 4096 / cut->waves) + made - 1) / made;
+  if (cut->cols) {
+    // one round of resident workgroups where a sequence is cut into many parts (three sequences of 131000 keys in e2m1:
+    // 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all lengths (64 of up to
+    // 16384 in e4m3: 268 us at 2048, 295 at 1024)
+    const int64_t resident = 256 * few_waves(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1, cut->cols);
+    if (base <= resident / 2) want = resident / base;
+  }
   const int64_t most = ((int64_t)max_len + (cut->cols ? 127 : 511)) / (cut->cols ? 128 : 512);
   int64_t s = want < most ? want : most;
   cut->splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
@@ -290,7 +301,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
 
 LLVQ_API int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab) {
   if (batch < 0 || batch > LLVQ_MAX_SEQS || vocab < 1) return LLVQ_EINVAL;
-  return (int64_t)batch * draft_parts(batch, vocab) * 16;
+  return (int64_t)batch * draft_parts(batch, vocab) * 8;
 }
 
 LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
@@ -325,10 +336,10 @@ LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dt
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dtype == LLVQ_X_F32) {
     hipLaunchKernelGGL((k_draft_part<true>), dim3(a.parts, batch), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_draft_pick<true>), dim3(batch), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((k_draft_pick<true>), dim3(batch), dim3(256), 0, s, a);
   } else {
     hipLaunchKernelGGL((k_draft_part<false>), dim3(a.parts, batch), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_draft_pick<false>), dim3(batch), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((k_draft_pick<false>), dim3(batch), dim3(256), 0, s, a);
   }
   return launch_status();
 }
