@@ -38,12 +38,15 @@ __device__ __forceinline__ bool place_of(const Cache& c, int t, int64_t* base, i
   return true;
 }
 
-template <bool F32, bool VEC>
+// STREAM: what is read once does not displace the cache's own lines (a prompt of 14.6 k tokens of 32 heads in e2m1: 69 us
+// instead of 82).
+template <bool F32, bool VEC, bool STREAM = false>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float* x) {
   if constexpr (F32) {
     const float* f = static_cast<const float*>(p) + at;
     if constexpr (VEC) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(f), b = *reinterpret_cast<const f32x4*>(f + 4);
+      const f32x4* w = reinterpret_cast<const f32x4*>(f);
+      const f32x4 a = STREAM ? __builtin_nontemporal_load(w) : w[0], b = STREAM ? __builtin_nontemporal_load(w + 1) : w[1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
     } else {
@@ -53,7 +56,8 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float* x) {
   } else {
     const uint16_t* h = static_cast<const uint16_t*>(p) + at;
     if constexpr (VEC) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(h);
+      const u32x4* w = reinterpret_cast<const u32x4*>(h);
+      const u32x4 a = STREAM ? __builtin_nontemporal_load(w) : w[0];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(a[i] << 16), x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
     } else {
@@ -132,7 +136,8 @@ __global__ __launch_bounds__(256) void k_kv_write(Cache c, KvRows in, Divider ch
     float x[PW][8];
 #pragma unroll
     for (int i = 0; i < PW; ++i)
-      if (at.there[i]) load8<F32, VEC>(m.is_v ? in.v : in.k, (first + i) * (m.is_v ? in.v_token : in.k_token) + from, x[i]);
+      if (at.there[i])
+        load8<F32, VEC, true>(m.is_v ? in.v : in.k, (first + i) * (m.is_v ? in.v_token : in.k_token) + from, x[i]);
 #pragma unroll
     for (int i = 0; i < PW; ++i) {
       if (!at.there[i]) continue;

@@ -71,7 +71,7 @@ int launch_kv(const Cache& c, const KvRows& r, bool f32, bool vec, int32_t* err,
   const unsigned gx = (unsigned)((c.tokens + 4ll * PW - 1) / (4ll * PW));
   const unsigned parts = (unsigned)((items + kWave - 1) / kWave);
   // a wave has one item of each token while that leaves it few workgroups, up to four after that
-  const unsigned gy = (uint64_t)gx * parts >= 16384 ? (parts + 3) / 4 : parts;
+  const unsigned gy = (uint64_t)gx * parts >= 1024 ? (parts + 3) / 4 : parts;
   const dim3 grid(gx, gy > 65535 ? 65535 : gy);
 #define LLVQ_KV_CASE(F32, VEC)                                                                                \
   if (f32 == F32 && vec == VEC) {                                                                             \
