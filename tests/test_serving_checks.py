@@ -115,7 +115,7 @@ def test_draft_refusals(lib):
         assert draft(lib, **bad) == -1, bad
     assert draft(lib, b=0, target=None, noise=None, acc=None, out=None, ws=None) == 0
     assert lib.llvq_draft_workspace_bytes(-1, 10) == -1 and lib.llvq_draft_workspace_bytes(1, 0) == -1
-    assert wd.draft_workspace_bytes(3, 2048) == 24 and wd.draft_workspace_bytes(3, 2049) == 48
+    assert wd.draft_workspace_bytes(3, 8192) == 24 and wd.draft_workspace_bytes(3, 8193) == 5 * 24
 
 
 def test_serving_host_code_is_clean_under_sanitizers(tmp_path):

@@ -230,8 +230,8 @@ __device__ __forceinline__ bool has_255(uint32_t word) {
 // Few rows: up to 64 rows of a (sequence, key head), in CT tiles of 16 columns.
 //
 // A decode step reads each cached byte for a handful of rows, so HBM bounds it and what counts is loads
-// in flight.  Every wave therefore runs by itself: it takes every fourth 32-key piece of the workgroup's
-// share, stages it in its own 64 * DP bytes of LDS (the keys, then the values in the same place) and waits for
+// in flight.  Every wave therefore runs by itself: it takes every fourth (or eighth) 32-key piece of the
+// workgroup's share, stages it in its own 64 * DP bytes of LDS (the keys, then the values in the same place) and waits for
 // nothing but its own loads, which are issued a piece ahead (page numbers two pieces ahead).  With 16x16x32
 // instructions a lane holds 8 scores of a piece, and a tile of outputs takes DP / 4 registers of a lane.
 // In S^T's layout a lane (column lane % 16, g = lane / 16) holds keys 4 g + i and 16 + 4 g + i, which are
@@ -271,8 +271,8 @@ constexpr int few_waves(int kind, int dp, int nt, int ct) {
 // Two column tiles share a staged piece where two waves a SIMD still fit.
 constexpr bool few_pairs(int kind, int dp, int nt) { return few_waves(kind, dp, nt, 2) >= 2; }
 
-template <int KIND, int DP, int NT, int CT>
-__global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
+template <int KIND, int DP, int NT, int CT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
   constexpr int kRaw = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
   constexpr int kLoads = 32 * kRaw / kWave;        // chunks a lane loads of a piece
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
@@ -280,8 +280,8 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   constexpr int32_t kNoKey = INT32_MIN;
   const Cache& c = a.c;
   using Lds = FewLds<DP>;
-  __shared__ __align__(16) uint8_t lds[4 * Lds::kWaveBytes];
-  __shared__ float wave_m[4][16], wave_l[4][16];
+  __shared__ __align__(16) uint8_t lds[WAVES * Lds::kWaveBytes];
+  __shared__ float wave_m[WAVES][16], wave_l[WAVES][16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   if (a.err && tid == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * 16 * CT)) atomicAdd(a.err, 1);
   const int row0 = rb * 16 * CT;
   if (row0 >= rows) return;
-  const Span w = span_of(a, s, row0, 16 * CT, 128, split);
+  const Span w = span_of(a, s, row0, 16 * CT, 32 * WAVES, split);
 
   const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   bool lost = false;
   // the page number of this lane's key of a piece (lanes 32..63 as 0..31)
   auto page_of = [&](int tile) -> int32_t {
-    const int j = (tile * 4 + wave) * 32 + (lane & 31);
+    const int j = (tile * WAVES + wave) * 32 + (lane & 31);
     if (tile >= w.tile_hi || j < w.first_key || j >= w.last_key) return kNoKey;
     return table[divide((uint32_t)j, c.page)];
   };
@@ -324,7 +324,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   u32x4 raw_k[kLoads], raw_v[kLoads];
   uint32_t scales[kWords], next_scales[kWords], gone = 0, next_gone = 0;  // of the piece that is staged, and of the next
   auto locate = [&](int tile, int32_t ids) {
-    const uint32_t j = (uint32_t)((tile * 4 + wave) * 32 + (lane & 31));
+    const uint32_t j = (uint32_t)((tile * WAVES + wave) * 32 + (lane & 31));
     const bool ok = ids >= 0 && ids < c.pages;
     lost |= !ok && ids != kNoKey;
     next_gone = (uint32_t)__ballot(!ok);
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   }
 
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
-    const int key_base = (tile * 4 + wave) * 32;
+    const int key_base = (tile * WAVES + wave) * 32;
     const bool more = tile + 1 < w.tile_hi;
     // the keys
     gone = next_gone;
@@ -537,7 +537,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 
-  // the four waves' parts are joined through LDS under their common maximum and added in the waves' order
+  // the waves' parts are joined through LDS under their common maximum and added in the waves' order
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     const float l = quad_sum((l4[ct][0] + l4[ct][1]) + (l4[ct][2] + l4[ct][3]));
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, wave_m[i][col]);
+    for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_m[i][col]);
     const float f = m[ct] == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(m[ct] - top);
     if (g == 0) wave_l[wave][col] = l * f;
     float* sums = reinterpret_cast<float*>(lds);  // [wave][16 columns][DP], quads of channels swizzled by the column
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
     __syncthreads();
     float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) total += wave_l[i][col];
+    for (int i = 0; i < WAVES; ++i) total += wave_l[i][col];
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // no visible key: the row is zero
     if (live[ct]) {
       const int64_t row = (int64_t)(s.first + t[ct]) * c.heads * share + qhead[ct];
@@ -567,12 +567,10 @@ __global__ __launch_bounds__(256, few_waves(KIND, DP, NT, CT)) void k_attn_few(A
         a.stats[(split * all + row) * 2 + 1] = total;
       }
       if (a.splits == 1 || w.tile_lo < w.tile_hi) {
-#pragma unroll
-        for (int d4 = 0; d4 < kOut / 4; ++d4) {
-          const int d = d4 * 4 + wave;  // each wave writes a quarter of the channels
+        for (int d = wave; d < kOut; d += WAVES) {  // the waves share out the channels
           f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x += *reinterpret_cast<const f32x4*>(sums + (i * 16 + col) * DP + (((d * 4 + g) ^ (col & 7)) << 2));
+          for (int i = 0; i < WAVES; ++i) x += *reinterpret_cast<const f32x4*>(sums + (i * 16 + col) * DP + (((d * 4 + g) ^ (col & 7)) << 2));
           store_row4<NT>(a, row, out_at, split, d * 16 + g * 4, x, inv);
         }
       }

@@ -92,27 +92,25 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t k) {
   return k;
 }
 
-template <bool F32>
-__global__ __launch_bounds__(256) void k_draft_part(DraftArgs a) {
-  const int b = blockIdx.y, part = blockIdx.x, tid = threadIdx.x;
-  bool bad;
-  const int done = accepted_of<F32>(a, b, &bad);
+// A workgroup's best of entries [from, end) of the row that sequence b draws from, in every thread.
+template <bool F32, int THREADS>
+__device__ __forceinline__ uint64_t best_of(const DraftArgs& a, int b, int done, bool with_draft, int64_t from, int64_t end) {
+  constexpr int kAhead = THREADS == 1024 ? 16 : 8;  // entries in flight a thread: one workgroup alone waits for each round of loads
+  __shared__ uint64_t best[THREADS / 64];
+  const int tid = threadIdx.x;
   const int n = a.counts ? min(max(a.counts[b], 0), a.drafts) : a.drafts;
-  const bool all = done >= n;
+  const bool less = with_draft && done < n;
   const int64_t row = ((int64_t)b * (a.drafts + 1) + done) * a.vocab;
   const int64_t qrow = ((int64_t)b * a.drafts + done) * a.vocab;
-  const int certain = !all && !a.draft ? a.tokens[(int64_t)b * a.drafts + done] : -1;
-  const bool take = !all && a.draft;
+  const int certain = less && !a.draft ? a.tokens[(int64_t)b * a.drafts + done] : -1;
+  const bool take = less && a.draft;
   const float* noise = a.noise + (int64_t)b * a.vocab;
-  const int64_t from = (int64_t)part * a.per;
-  const int64_t end = min(from + a.per, (int64_t)a.vocab);
-  constexpr int kAhead = 8;
-  Best rest;
-  for (int64_t v0 = from + tid; v0 < end; v0 += 256 * kAhead) {
+  Best mine;
+  for (int64_t v0 = from + tid; v0 < end; v0 += THREADS * kAhead) {
     float w[kAhead], e[kAhead], q[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int64_t v = v0 + 256 * i;
+      const int64_t v = v0 + THREADS * i;
       const bool in = v < end;
       w[i] = in ? prob<F32>(a.target, row + v) : 0.0f;
       e[i] = in ? noise[v] : 1.0f;
@@ -121,57 +119,67 @@ __global__ __launch_bounds__(256) void k_draft_part(DraftArgs a) {
     bool any = false;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      w[i] = (int)(v0 + 256 * i) == certain ? 0.0f : w[i] - q[i];
-      any |= rest.may(w[i], e[i]);
+      w[i] = (int)(v0 + THREADS * i) == certain ? 0.0f : w[i] - q[i];
+      any |= mine.may(w[i], e[i]);
     }
     if (any) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (rest.may(w[i], e[i])) rest.take(w[i], e[i], (int)(v0 + 256 * i));
+        if (mine.may(w[i], e[i])) mine.take(w[i], e[i], (int)(v0 + THREADS * i));
     }
   }
-  __shared__ uint64_t best[4];
-  const uint64_t k = wave_max(rest.key());
+  const uint64_t k = wave_max(mine.key());
+  __syncthreads();  // (an earlier call's keys have been read)
   if ((tid & 63) == 0) best[tid >> 6] = k;
   __syncthreads();
-  if (tid == 0) {
-    uint64_t top = best[0];
-    for (int i = 1; i < 4; ++i) top = best[i] > top ? best[i] : top;
-    a.keys[(int64_t)b * a.parts + part] = top;
-  }
+  uint64_t top = best[0];
+  for (int i = 1; i < THREADS / 64; ++i) top = best[i] > top ? best[i] : top;
+  return top;
 }
 
-template <bool F32>
-__global__ __launch_bounds__(256) void k_draft_pick(DraftArgs a) {
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  bool bad;
-  const int done = accepted_of<F32>(a, b, &bad);
-  __shared__ uint64_t best[4];
-  uint64_t k = 0;
-  for (int i = lane; i < a.parts; i += 64) {
-    const uint64_t x = a.keys[(int64_t)b * a.parts + i];
-    k = x > k ? x : k;
-  }
-  k = wave_max(k);
-  if (k == 0) {  // the rest is empty: the target alone (the same in every wave)
-    const int64_t row = ((int64_t)b * (a.drafts + 1) + done) * a.vocab;
-    Best whole;
-    for (int64_t v = tid; v < a.vocab; v += 256) {
-      const float w = prob<F32>(a.target, row + v), e = a.noise[(int64_t)b * a.vocab + v];
-      if (whole.may(w, e)) whole.take(w, e, (int)v);
-    }
-    k = wave_max(whole.key());
-    if (lane == 0) best[tid >> 6] = k;
-    __syncthreads();
-    for (int i = 0; i < 4; ++i) k = best[i] > k ? best[i] : k;
-  }
+// The answer of sequence b, from the rest's best; where the rest was empty, from the target alone.
+template <bool F32, int THREADS>
+__device__ __forceinline__ void answer(const DraftArgs& a, int b, int done, bool bad, uint64_t k) {
+  const int tid = threadIdx.x;
+  if (k == 0) k = best_of<F32, THREADS>(a, b, done, false, 0, a.vocab);
   const int last = k ? (int)(0xffffffffu - (uint32_t)k) : -1;
-  for (int i = tid; i <= a.drafts; i += 256)
+  for (int i = tid; i <= a.drafts; i += THREADS)
     a.out[(int64_t)b * (a.drafts + 1) + i] = i < done ? a.tokens[(int64_t)b * a.drafts + i] : i == done ? last : -1;
   if (tid == 0) {
     a.accepted[b] = done;
     if (a.err && (bad || !k)) atomicAdd(a.err, 1);
   }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(1024) void k_draft_one(DraftArgs a) {
+  const int b = blockIdx.x;
+  bool bad;
+  const int done = accepted_of<F32>(a, b, &bad);
+  answer<F32, 1024>(a, b, done, bad, best_of<F32, 1024>(a, b, done, true, 0, a.vocab));
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void k_draft_part(DraftArgs a) {
+  const int b = blockIdx.y;
+  bool bad;
+  const int done = accepted_of<F32>(a, b, &bad);
+  const int64_t from = (int64_t)blockIdx.x * a.per;
+  const uint64_t k = best_of<F32, 256>(a, b, done, true, from, min(from + a.per, (int64_t)a.vocab));
+  if (threadIdx.x == 0) a.keys[(int64_t)b * a.parts + blockIdx.x] = k;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void k_draft_pick(DraftArgs a) {
+  const int b = blockIdx.x;
+  bool bad;
+  const int done = accepted_of<F32>(a, b, &bad);
+  uint64_t k = 0;
+  for (int i = threadIdx.x & 63; i < a.parts; i += 64) {
+    const uint64_t x = a.keys[(int64_t)b * a.parts + i];
+    k = x > k ? x : k;
+  }
+  answer<F32, 256>(a, b, done, bad, wave_max(k));  // (the same in every wave)
 }
 
 }  // namespace serve

@@ -112,8 +112,8 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
 #undef LLVQ_KV_KIND
 }
 
-// How a call is cut up: columns of 16 that a workgroup of the kernel for few rows holds, or waves of one of
-// the kernel for many rows (the other is 0), row blocks and splits of the keys.
+// How a call is cut up: columns of 16 that a workgroup of the kernel for few rows holds (0: the kernel for many
+// rows), waves of a workgroup, row blocks and splits of the keys.
 struct Cut {
   int cols, waves, row_blocks, splits;
 };
@@ -125,7 +125,7 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1) ? 1 : 2;
   // Eight waves stage a tile for 256 rows: 539 us instead of 594 at chunks of 2 x 2048 rows of 128-wide heads over 8192 keys, 220 instead
   // of 391 at 256-wide heads; 64-wide heads run better with three workgroups of four a compute unit
-  cut->waves = cut->cols ? 0 : rows <= 128 || f32 || d->head_dim <= 64 ? 4 : 8;
+  cut->waves = cut->cols ? 4 : rows <= 128 || f32 || d->head_dim <= 64 ? 4 : 8;
   const int64_t per = cut->cols ? 16 * cut->cols : 32 * cut->waves;
   const int64_t blocks = (rows + per - 1) / per;
   const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
@@ -141,6 +141,9 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   }
   const int64_t most = ((int64_t)max_len + (cut->cols ? 127 : 511)) / (cut->cols ? 128 : 512);
   int64_t s = want < most ? want : most;
+  // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to three pieces (at
+  // 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups 7.4 us and the join 4.6 after it)
+  if (cut->cols == 1 && padded_dim(d->head_dim) <= 128 && base <= 256 && max_len <= 768) cut->waves = 8, s = 1;
   cut->splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
   cut->row_blocks = (int)blocks;
   return base * cut->splits > (1 << 30) ? LLVQ_EINVAL : LLVQ_OK;  // (a kernel may take twice as many workgroups)
@@ -161,20 +164,24 @@ int launch_many(const AttnArgs& a, unsigned grid, hipStream_t s) {
   hipLaunchKernelGGL((k_attn_many<KIND, DP, NT, WAVES>), dim3(grid * Sh::kParts), dim3(Sh::kThreads), 0, s, a);
   return launch_status();
 }
+template <int KIND, int DP, int NT, int CT, int WAVES>
+int launch_few(const AttnArgs& a, unsigned grid, hipStream_t s) {
+  hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, CT, WAVES>), dim3(grid), dim3(64 * WAVES), 0, s, a);
+  return launch_status();
+}
 template <int KIND, int DP, int NT>
 int launch_attn(const AttnArgs& a, const Cut& cut, unsigned grid, hipStream_t s) {
-  if (cut.waves == 4) return launch_many<KIND, DP, NT, 4>(a, grid, s);
   if constexpr (NT == 1 && DP > 64) {
-    if (cut.waves == 8) return launch_many<KIND, DP, NT, 8>(a, grid, s);
+    if (cut.cols == 0 && cut.waves == 8) return launch_many<KIND, DP, NT, 8>(a, grid, s);
   }
+  if (cut.cols == 0) return launch_many<KIND, DP, NT, 4>(a, grid, s);
   if constexpr (few_pairs(KIND, DP, NT)) {
-    if (cut.cols == 2) {
-      hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 2>), dim3(grid), dim3(256), 0, s, a);
-      return launch_status();
-    }
+    if (cut.cols == 2) return launch_few<KIND, DP, NT, 2, 4>(a, grid, s);
   }
-  hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, 1>), dim3(grid), dim3(256), 0, s, a);
-  return launch_status();
+  if constexpr (DP <= 128) {
+    if (cut.waves == 8) return launch_few<KIND, DP, NT, 1, 8>(a, grid, s);
+  }
+  return launch_few<KIND, DP, NT, 1, 4>(a, grid, s);
 }
 template <int KIND, int DP>
 int launch_attn_nt(const AttnArgs& a, bool f32, const Cut& cut, unsigned grid, hipStream_t s) {
@@ -208,10 +215,24 @@ int launch_join_dim(const AttnArgs& a, hipStream_t s) {
   }
 }
 
+// Workgroups that share out a row; 1: one of 1024 threads does it all in one launch (one compute unit alone draws no more
+// than 40 GB/s: a row of 32000 takes it 14 us, 16 workgroups 5 us and the second launch 2).
 int draft_parts(int32_t batch, int32_t vocab) {
+  if (vocab <= 8192 || batch >= 512) return 1;
   // about 1024 workgroups in all, each of at least 2048 entries
   const int64_t most = ((int64_t)vocab + 2047) / 2048, want = (1024 + (batch > 0 ? batch : 1) - 1) / (batch > 0 ? batch : 1);
   return (int)(want < most ? want : most);
+}
+
+template <bool F32>
+int launch_draft(const DraftArgs& a, hipStream_t s) {
+  if (a.parts == 1) {
+    hipLaunchKernelGGL((k_draft_one<F32>), dim3(a.batch), dim3(1024), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_draft_part<F32>), dim3(a.parts, a.batch), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_draft_pick<F32>), dim3(a.batch), dim3(256), 0, s, a);
+  }
+  return launch_status();
 }
 
 }  // namespace
@@ -334,12 +355,5 @@ LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dt
   a.parts = draft_parts(batch, vocab);
   a.per = (vocab + a.parts - 1) / a.parts;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == LLVQ_X_F32) {
-    hipLaunchKernelGGL((k_draft_part<true>), dim3(a.parts, batch), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_draft_pick<true>), dim3(batch), dim3(256), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((k_draft_part<false>), dim3(a.parts, batch), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_draft_pick<false>), dim3(batch), dim3(256), 0, s, a);
-  }
-  return launch_status();
+  return dtype == LLVQ_X_F32 ? launch_draft<true>(a, s) : launch_draft<false>(a, s);
 }
