@@ -697,6 +697,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   u32x4 raw_k[KChunks::kPer], raw_v[VChunks::kPer];
   uint32_t sc_k[KChunks::kPer], sc_v[VChunks::kPer];
   uint64_t gone = 0, nonfinite = 0;  // of the loaded tile
+  uint64_t spoilt_now = 0, spoilt_next = 0;  // of the tile that is multiplied, and of the staged one after it
   bool lost = false;
   // Where a tile's keys lie and how they are scaled is worked out once a key, by the wave whose turn it is: the
   // page numbers are loaded five rounds ahead, the scales four, both written to LDS three and the codes loaded
@@ -785,8 +786,8 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
 #pragma unroll
       for (int i = 0; i < VChunks::kPer; ++i)
         if (sc_v[i] == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sc_v[i] = 127;
-      if (tid < kSub) bad_bits[tid] = (uint32_t)(nonfinite >> (32 * tid));
     }
+    spoilt_next = nonfinite;
     u32x4 o[kOf];
     if (kc.any) {
 #pragma unroll
@@ -819,6 +820,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     __syncthreads();
     fetch(w.tile_lo);
     stage(lds, bad_keys[0]);
+    spoilt_now = spoilt_next;
     fetch(w.tile_lo + 1);
     __syncthreads();
     write_places(w.tile_lo + 2);
@@ -853,6 +855,17 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    const uint8_t* values = buffer + kKeys * Sh::kKeyRow + (4 * half + ((lane & 15) >> 2)) * Sh::kValueRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    auto value_operand = [&](int k) {  // k = 16-key step * kOut + output tile
+      const uint8_t* at = values + (k / kOut) * 16 * Sh::kValueRow + (k % kOut) * 64;
+      union {
+        s16x4 h[2];
+        bf16x8 v;
+      } vf;
+      vf.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+      vf.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * Sh::kValueRow));
+      return vf.v;
+    };
     if (!(key_base >= w.all_lo && key_base + kKeys <= w.all_hi && key_base + kKeys <= s.len)) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
@@ -901,33 +914,22 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       load_pages(tile + 5);
     }
     {
-      const uint8_t* values = buffer + kKeys * Sh::kKeyRow + (4 * half + ((lane & 15) >> 2)) * Sh::kValueRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-      auto operand = [&](int k) {  // k = 16-key step * kOut + output tile
-        const uint8_t* at = values + (k / kOut) * 16 * Sh::kValueRow + (k % kOut) * 64;
-        union {
-          s16x4 h[2];
-          bf16x8 v;
-        } vf;
-        vf.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
-        vf.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * Sh::kValueRow));
-        return vf.v;
-      };
       bf16x8 vf[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) vf[k] = operand(k);
+      for (int k = 0; k < kAhead; ++k) vf[k] = value_operand(k);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int k = 0; k < 2 * kSub * kOut; ++k) {
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n)
           acc[k % kOut] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k % kAhead], p[n][k / kOut], acc[k % kOut], 0, 0, 0);
-        if (k + kAhead < 2 * kSub * kOut) vf[k % kAhead] = operand(k + kAhead);
+        if (k + kAhead < 2 * kSub * kOut) vf[k % kAhead] = value_operand(k + kAhead);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
-      uint32_t left = __builtin_amdgcn_readfirstlane((int)bad_keys[third][u]);
+      uint32_t left = KIND == LLVQ_KV_BF16 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)bad_keys[third][u]) : (uint32_t)(spoilt_now >> (32 * u));
       while (left) {
         const int j = key_base + u * 32 + __builtin_ctz(left);
         left &= left - 1;
@@ -946,6 +948,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       }
     }
     third = next;
+    spoilt_now = spoilt_next;
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 
