@@ -407,8 +407,8 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  *   max_len : at least 1; about the longest length: it decides only how the keys are split, not
  *            what is computed.
  *   scale  : > 0 and finite.   window : 0 (none) .. 2^30.
- *   workspace : llvq_attn_workspace_bytes(...) bytes for the same arguments, 16-byte aligned
- *            (may be NULL if that is 0), contents not kept.
+ *   workspace : at least llvq_attn_workspace_bytes(...) bytes for the same arguments, 16-byte aligned
+ *            (may be NULL if that is 0), contents not kept; workspace_bytes: what it holds.
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (its tokens'
  *            keys and values are then taken as zeros), starts or lengths had to be cut, or a sequence has more rows than max_chunk.
  * Sums, maxima and outputs are f32; bf16 queries take P in bf16, f32 queries take Q and P in three
@@ -416,7 +416,7 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
 int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
               int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
               int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,
-              int32_t* err_count, void* stream);
+              int64_t workspace_bytes, int32_t* err_count, void* stream);
 
 /* Bytes of llvq_attn's workspace, or LLVQ_EINVAL.  Host only. */
 int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch,
@@ -435,12 +435,13 @@ int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads, int64_t 
  *   noise  : [batch][vocab], exponential, >= 0 (a NaN or negative one is never drawn).
  *   accepted : [batch]: a.   out : [batch][drafts + 1]: the accepted tokens, the drawn one (-1 if
  *            no weight is positive: counted), then -1.
- *   drafts : 0..LLVQ_MAX_DRAFTS.   workspace : llvq_draft_workspace_bytes(batch, vocab) bytes, 8-byte aligned.
+ *   drafts : 0..LLVQ_MAX_DRAFTS.   workspace : at least llvq_draft_workspace_bytes(batch, vocab) bytes, 8-byte
+ *            aligned, contents not kept; workspace_bytes: what it holds.
  * All arrays contiguous.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
                       const int32_t* counts, const float* uniforms, const float* noise, int32_t batch,
                       int32_t drafts, int32_t vocab, int32_t* accepted, int32_t* out, void* workspace,
-                      int32_t* err_count, void* stream);
+                      int64_t workspace_bytes, int32_t* err_count, void* stream);
 
 /* Bytes of llvq_draft_verify's workspace, or LLVQ_EINVAL.  Host only. */
 int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab);

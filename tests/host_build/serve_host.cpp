@@ -49,15 +49,15 @@ int main() {
       CHECK(st == (x == 0 && y >= 0 ? LLVQ_OK : LLVQ_EINVAL));
     }
     const llvq_batch b = {ip, ip, ip, 2, 2, 3};
-    CHECK(llvq_attn(&d, p, p, 1024, 128, nullptr, 1024, 128, LLVQ_X_BF16, 8, &b, x, x, 0.1f, 1, x, p, nullptr, nullptr) == LLVQ_EINVAL);
-    CHECK(llvq_draft_verify(p, p, LLVQ_X_F32, ip, ip, (float*)p, (float*)p, 1, x, x, nullptr, (int32_t*)p, p, nullptr, nullptr) ==
+    CHECK(llvq_attn(&d, p, p, 1024, 128, nullptr, 1024, 128, LLVQ_X_BF16, 8, &b, x, x, 0.1f, 1, x, p, 256, nullptr, nullptr) == LLVQ_EINVAL);
+    CHECK(llvq_draft_verify(p, p, LLVQ_X_F32, ip, ip, (float*)p, (float*)p, 1, x, x, nullptr, (int32_t*)p, p, 256, nullptr, nullptr) ==
           LLVQ_EINVAL);
   }
-  CHECK(llvq_attn(&d, p, p, 1024, 128, p, 1024, 128, LLVQ_X_BF16, 8, nullptr, 1, 1, 0.1f, 1, 0, p, nullptr, nullptr) == LLVQ_EINVAL);
+  CHECK(llvq_attn(&d, p, p, 1024, 128, p, 1024, 128, LLVQ_X_BF16, 8, nullptr, 1, 1, 0.1f, 1, 0, p, 256, nullptr, nullptr) == LLVQ_EINVAL);
   const llvq_batch nothing = {nullptr, nullptr, nullptr, 0, 0, 0};
-  CHECK(llvq_attn(&d, nullptr, nullptr, 0, 0, nullptr, 0, 0, LLVQ_X_F32, 8, &nothing, 1, 1, 0.1f, 1, 0, nullptr, nullptr, nullptr) ==
+  CHECK(llvq_attn(&d, nullptr, nullptr, 0, 0, nullptr, 0, 0, LLVQ_X_F32, 8, &nothing, 1, 1, 0.1f, 1, 0, nullptr, 0, nullptr, nullptr) ==
         LLVQ_OK);
-  CHECK(llvq_attn(&d, p, p, 1, 1, p, 4, 4, LLVQ_X_F32, 8, &nothing, 1, 1, NAN, 1, 0, p, nullptr, nullptr) == LLVQ_EINVAL);
+  CHECK(llvq_attn(&d, p, p, 1, 1, p, 4, 4, LLVQ_X_F32, 8, &nothing, 1, 1, NAN, 1, 0, p, 256, nullptr, nullptr) == LLVQ_EINVAL);
   printf("ok %d\n", g_checks);
   return 0;
 }

@@ -76,10 +76,10 @@ def test_kv_refusals(lib, name):
 
 
 def attn(lib, d=None, pool=P, q=P, qs=(512, 64), out=P, os_=(512, 64), dtype=1, heads=8, n=None, max_chunk=2, max_len=4000,
-         scale=0.1, causal=1, window=0, ws=P, err=None):
+         scale=0.1, causal=1, window=0, ws=P, size=1 << 30, err=None):
     d, n = desc() if d is None else d, batch() if n is None else n
     return lib.llvq_attn(ctypes.byref(d), pool, q, *qs, out, *os_, dtype, heads, ctypes.byref(n), max_chunk, max_len, scale, causal,
-                         window, ws, err, None)
+                         window, ws, size, err, None)
 
 
 def test_attn_refusals(lib):
@@ -91,7 +91,8 @@ def test_attn_refusals(lib):
                 dict(dtype=0, out=ctypes.c_void_p(0x10008)), dict(dtype=2), dict(heads=0), dict(heads=7), dict(heads=1),
                 dict(qs=(-1, 64)), dict(os_=(510, 64)), dict(os_=(512, 62)), dict(os_=(-4, 64)), dict(max_chunk=0), dict(max_len=0),
                 dict(max_len=(1 << 30) + 1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")),
-                dict(window=-1), dict(window=(1 << 30) + 1), dict(ws=None), dict(ws=ODD), dict(err=ctypes.c_void_p(0x10002))):
+                dict(window=-1), dict(window=(1 << 30) + 1), dict(ws=None), dict(ws=ODD), dict(size=0), dict(size=wd.attn_workspace_bytes(desc(), 8, 3, 2, 2, 4000) - 1),
+                dict(err=ctypes.c_void_p(0x10002))):
         assert attn(lib, **bad) == -1, bad
     assert attn(lib, q=None, out=None, ws=None, n=batch(tokens=0)) == 0
     for args in ((7, 10, 2, 2, 100), (8, -1, 2, 2, 100), (8, 10, -1, 2, 100), (8, 10, 2, 0, 100), (8, 10, 2, 2, 0),
@@ -102,8 +103,8 @@ def test_attn_refusals(lib):
     assert many > 0 and many % (10 * 8 * (64 + 2) * 4) == 0
 
 
-def draft(lib, target=P, q=P, dtype=0, tokens=P, counts=P, uni=P, noise=P, b=2, s=3, vocab=100, acc=P, out=P, ws=P, err=None):
-    return lib.llvq_draft_verify(target, q, dtype, tokens, counts, uni, noise, b, s, vocab, acc, out, ws, err, None)
+def draft(lib, target=P, q=P, dtype=0, tokens=P, counts=P, uni=P, noise=P, b=2, s=3, vocab=100, acc=P, out=P, ws=P, size=1 << 20, err=None):
+    return lib.llvq_draft_verify(target, q, dtype, tokens, counts, uni, noise, b, s, vocab, acc, out, ws, size, err, None)
 
 
 def test_draft_refusals(lib):
@@ -111,7 +112,7 @@ def test_draft_refusals(lib):
     for bad in (dict(target=None), dict(target=two), dict(q=two), dict(dtype=2), dict(tokens=None), dict(tokens=two), dict(counts=two),
                 dict(uni=None), dict(uni=two), dict(noise=None), dict(noise=two), dict(b=-1), dict(b=32769), dict(s=-1), dict(s=64),
                 dict(vocab=0), dict(acc=None), dict(acc=two), dict(out=None), dict(out=two), dict(ws=None), dict(ws=ODD),
-                dict(err=two), dict(dtype=1, target=ctypes.c_void_p(0x10001))):
+                dict(size=15), dict(err=two), dict(dtype=1, target=ctypes.c_void_p(0x10001))):
         assert draft(lib, **bad) == -1, bad
     assert draft(lib, b=0, target=None, noise=None, acc=None, out=None, ws=None) == 0
     assert lib.llvq_draft_workspace_bytes(-1, 10) == -1 and lib.llvq_draft_workspace_bytes(1, 0) == -1
@@ -162,8 +163,6 @@ def no_library(monkeypatch):
     def sentinel(*a, **k):
         raise _Reached()
     monkeypatch.setattr(wd, "load_library", sentinel)
-    monkeypatch.setattr(wd, "attn_workspace_bytes", lambda *a: 64)
-    monkeypatch.setattr(wd, "draft_workspace_bytes", lambda *a: 64)
 
 
 def i32(*shape):
@@ -217,8 +216,8 @@ def test_attn_binding(no_library):
         wd.attn(**attn_args())
     for bad in (dict(q=g(torch.zeros(5, 5, 64))), dict(q=g(torch.zeros(5, 6, 32))), dict(q=g(torch.zeros(5, 384))), dict(q=None),
                 dict(out=g(torch.zeros(5, 6, 64).bfloat16())), dict(out=g(torch.zeros(4, 6, 64))), dict(out=torch.zeros(5, 6, 64)),
-                dict(out=g(torch.zeros(1, 6, 64)).expand(5, 6, 64)), dict(workspace=g(torch.zeros(63, dtype=torch.uint8))),
-                dict(workspace=None), dict(pool=None), dict(table=i32(2, 2))):
+                dict(out=g(torch.zeros(1, 6, 64)).expand(5, 6, 64)), dict(workspace=torch.zeros(64, dtype=torch.uint8)),
+                dict(workspace=7), dict(starts=None), dict(pool=None), dict(table=i32(2, 2))):
         with pytest.raises((ValueError, TypeError)):
             wd.attn(**attn_args(**bad))
 
@@ -237,7 +236,7 @@ def test_draft_binding(no_library):
     for bad in (dict(target=g(torch.zeros(2, 10))), dict(target=g(torch.zeros(2, 4, 10).half())), dict(draft=g(torch.zeros(2, 4, 10))),
                 dict(draft=g(torch.zeros(2, 3, 10).bfloat16())), dict(tokens=g(torch.zeros(2, 3, dtype=torch.int64))), dict(tokens=i32(3, 2)),
                 dict(uniforms=g(torch.zeros(2, 4))), dict(noise=g(torch.zeros(10))), dict(accepted=i32(3)), dict(out=i32(2, 3)),
-                dict(counts=i32(3)), dict(workspace=g(torch.zeros(8, dtype=torch.uint8))), dict(target=torch.zeros(2, 4, 10)),
+                dict(counts=i32(3)), dict(workspace=torch.zeros(64, dtype=torch.uint8)), dict(workspace=None), dict(target=torch.zeros(2, 4, 10)),
                 dict(noise=g(torch.zeros(10, 2)).t())):
         with pytest.raises((ValueError, TypeError)):
             wd.draft_verify(**draft_args(**bad))

@@ -139,11 +139,11 @@ def load_library(path=LIB_PATH):
     for name in ("llvq_kv_write", "llvq_kv_read"):
         getattr(lib, name).argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, bp, vp, vp]
         getattr(lib, name).restype = ctypes.c_int
-    lib.llvq_attn.argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, i32, bp, i32, i32, f32, i32, i32, vp, vp, vp]
+    lib.llvq_attn.argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, i32, bp, i32, i32, f32, i32, i32, vp, i64, vp, vp]
     lib.llvq_attn.restype = ctypes.c_int
     lib.llvq_attn_workspace_bytes.argtypes = [kp, i32, i64, i32, i32, i32]
     lib.llvq_attn_workspace_bytes.restype = i64
-    lib.llvq_draft_verify.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.llvq_draft_verify.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, i64, vp, vp]
     lib.llvq_draft_verify.restype = ctypes.c_int
     lib.llvq_draft_workspace_bytes.argtypes = [i32, i32]
     lib.llvq_draft_workspace_bytes.restype = i64
@@ -404,9 +404,11 @@ def _pool_nbytes(desc):
     return pages * heads * ((2 * page * token + 15) // 16 * 16)
 
 
+# These calls run many times a token, and a call's checks cost as much as its launch (3 us): the ordinary case
+# is one expression over all of a call's tensors, and only where it fails is each looked at for the message.
+
 def _buffer(t, call, name, dtype=None, nbytes=0):
-    """Checks a contiguous device buffer (dtype None: any); returns its address.  The checks of _tensor;
-    messages are only made when one fails, since these calls run many times a token."""
+    """Checks a contiguous device buffer (dtype None: any); returns its address."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{call}: {name} must be a torch tensor, got {type(t).__name__}")
@@ -422,22 +424,8 @@ def _buffer(t, call, name, dtype=None, nbytes=0):
 
 
 def _count(err_count, call):
-    if err_count is None:
-        return None
     import torch
     return _buffer(err_count, call, "err_count", torch.int32, 4)
-
-
-def _batch(starts, lens, table, tokens, call):
-    """llvq_batch from starts [B + 1], lens [B] and table [B][max_pages] (int32)."""
-    import torch
-    i32 = torch.int32
-    at = _buffer(starts, call, "starts", i32), _buffer(lens, call, "lens", i32), _buffer(table, call, "table", i32)
-    n, shape = lens.shape, table.shape
-    if len(n) != 1 or len(shape) != 2 or shape[0] != n[0] or starts.shape != (n[0] + 1,):
-        raise ValueError(f"{call}: starts, lens and table must be [B + 1], [B] and [B][max_pages], got "
-                         f"{tuple(starts.shape)}, {tuple(n)} and {tuple(shape)}")
-    return Batch(*at, n[0], shape[1], tokens)
 
 
 def _rows(t, call, name, heads, dim):
@@ -469,21 +457,57 @@ def _apart(t, call, name):
         raise ValueError(f"{call}: {name} has rows that overlap (strides {t.stride()})")
 
 
-def _kv_call(call, desc, pool, k, v, starts, lens, table, err_count, stream):
+def _paged(desc, pool, starts, lens, table, tokens, call):
+    """The pool's address and llvq_batch from starts [B + 1], lens [B] and table [B][max_pages] (int32)."""
     import torch
-    ks = _rows(k, call, "k", desc.kv_heads, desc.head_dim)
-    vs = _rows(v, call, "v", desc.kv_heads, desc.head_dim)
-    if k.shape != v.shape or k.dtype is not v.dtype:
-        raise ValueError(f"{call}: k and v must have one shape and dtype, got {tuple(k.shape)} {k.dtype} and "
-                         f"{tuple(v.shape)} {v.dtype}")
+    i32 = torch.int32
+    need = _pool_nbytes(desc)
+    try:
+        good = (pool.is_cuda and starts.is_cuda and lens.is_cuda and table.is_cuda and pool.dtype is torch.uint8 and
+                starts.dtype is i32 and lens.dtype is i32 and table.dtype is i32 and pool.is_contiguous() and
+                starts.is_contiguous() and lens.is_contiguous() and table.is_contiguous() and pool.numel() >= need)
+    except AttributeError:
+        good = False
+    if not good:
+        _buffer(pool, call, "pool", torch.uint8, need)
+        for t, name in ((starts, "starts"), (lens, "lens"), (table, "table")):
+            _buffer(t, call, name, i32)
+    n, shape = lens.shape, table.shape
+    if len(n) != 1 or len(shape) != 2 or shape[0] != n[0] or starts.shape != (n[0] + 1,):
+        raise ValueError(f"{call}: starts, lens and table must be [B + 1], [B] and [B][max_pages], got "
+                         f"{tuple(starts.shape)}, {tuple(n)} and {tuple(shape)}")
+    return pool.data_ptr(), Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), n[0], shape[1], tokens)
+
+
+def _pair(call, a, b, names, heads, dim):
+    """Checks two tensors of rows of one shape and dtype; (address, strides) of each and the dtype code."""
+    import torch
+    try:
+        shape, sa, sb, dtype = a.shape, a.stride(), b.stride(), a.dtype
+        good = (a.is_cuda and b.is_cuda and (dtype is torch.bfloat16 or dtype is torch.float32) and b.dtype is dtype and
+                b.shape == shape and len(shape) == 3 and shape[1] == heads and shape[2] == dim and sa[2] == 1 and sb[2] == 1)
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _rows(a, call, names[0], heads, dim)
+        _rows(b, call, names[1], heads, dim)
+        if a.shape != b.shape or a.dtype is not b.dtype:
+            raise ValueError(f"{call}: {names[0]} and {names[1]} must have one shape and dtype, got {tuple(a.shape)} {a.dtype} and "
+                             f"{tuple(b.shape)} {b.dtype}")
+        sa, sb, dtype = a.stride(), b.stride(), a.dtype
+    return a.data_ptr(), sa[0], sa[1], b.data_ptr(), sb[0], sb[1], X_F32 if dtype is torch.float32 else X_BF16
+
+
+def _kv_call(call, desc, pool, k, v, starts, lens, table, err_count, stream):
+    rows = _pair(call, k, v, "kv", desc.kv_heads, desc.head_dim)
     if call == "llvq_kv_read":
         _apart(k, call, "k")
         _apart(v, call, "v")
-    at = _buffer(pool, call, "pool", torch.uint8, _pool_nbytes(desc))
-    err = _count(err_count, call)
-    batch = _batch(starts, lens, table, k.shape[0], call)
-    _check(getattr(load_library(), call)(desc, at, *ks, *vs, X_F32 if k.dtype is torch.float32 else X_BF16, batch, err,
-                                         _raw_stream(stream, k.get_device())), call)
+    at, batch = _paged(desc, pool, starts, lens, table, k.shape[0], call)
+    err = None if err_count is None else _count(err_count, call)
+    code = getattr(load_library(), call)(desc, at, *rows, batch, err, _raw_stream(stream, k.get_device()))
+    if code:
+        raise LlvqError(code, call)
 
 
 def kv_write(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
@@ -516,22 +540,19 @@ def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len,
     heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
     if heads < 1 or desc.kv_heads < 1 or heads % desc.kv_heads:
         raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
-    qs = _rows(q, call, "q", heads, desc.head_dim)
-    os_ = _rows(out, call, "out", heads, desc.head_dim)
-    if q.shape != out.shape or q.dtype is not out.dtype:
-        raise ValueError(f"{call}: q and out must have one shape and dtype, got {tuple(q.shape)} {q.dtype} and "
-                         f"{tuple(out.shape)} {out.dtype}")
+    *rows, dtype = _pair(call, q, out, ("q", "out"), heads, desc.head_dim)
     _apart(out, call, "out")
-    at = _buffer(pool, call, "pool", torch.uint8, _pool_nbytes(desc))
-    err = _count(err_count, call)
-    batch = _batch(starts, lens, table, q.shape[0], call)
-    need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
-    ws = None if workspace is None and need == 0 else _buffer(workspace, call, "workspace", None, need)
-    if scale is None:
-        scale = desc.head_dim ** -0.5
-    _check(load_library().llvq_attn(desc, at, *qs, *os_, X_F32 if q.dtype is torch.float32 else X_BF16, heads, batch, max_chunk,
-                                    max_len, scale, 1 if causal else 0, window, ws, err, _raw_stream(stream, q.get_device())),
-           call)
+    at, batch = _paged(desc, pool, starts, lens, table, q.shape[0], call)
+    ws, size = (None, 0) if workspace is None else (_buffer(workspace, call, "workspace"), workspace.numel() * workspace.element_size())
+    err = None if err_count is None else _count(err_count, call)
+    code = load_library().llvq_attn(desc, at, *rows, dtype, heads, batch, max_chunk, max_len,
+                                    desc.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, size,
+                                    err, _raw_stream(stream, q.get_device()))
+    if code:
+        need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
+        if size < need:
+            raise ValueError(f"{call}: workspace holds {size} bytes; the call needs at least {need}")
+        raise LlvqError(code, call)
 
 
 def draft_workspace_bytes(batch, vocab) -> int:
@@ -548,29 +569,33 @@ def draft_verify(target, draft, tokens, uniforms, noise, accepted, out, workspac
     (accepted tokens, one drawn token, then -1), int32."""
     import torch
     call = "llvq_draft_verify"
+    i32, f32 = torch.int32, torch.float32
     dtype = target.dtype if isinstance(target, torch.Tensor) else None
     at = _buffer(target, call, "target")
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+    if dtype is not f32 and dtype is not torch.bfloat16:
         raise TypeError(f"{call}: target must have dtype torch.float32 or torch.bfloat16, got {dtype}")
     if target.dim() != 3 or target.shape[1] < 1:
         raise ValueError(f"{call}: target must be [B][drafts + 1][vocab], got {tuple(target.shape)}")
     b, s, v = target.shape
     s -= 1
-
-    def of(t, name, kind, shape, nullable=False):
-        if t is None and nullable:
-            return None
-        p = _buffer(t, call, name, kind)
-        if t.shape != shape:
+    each = ((tokens, "tokens", i32, (b, s)), (uniforms, "uniforms", f32, (b, s)), (noise, "noise", f32, (b, v)),
+            (accepted, "accepted", i32, (b,)), (out, "out", i32, (b, s + 1)))
+    if draft is not None:
+        each += ((draft, "draft", dtype, (b, s, v)),)
+    if counts is not None:
+        each += ((counts, "counts", i32, (b,)),)
+    for t, name, kind, shape in each:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is kind and t.shape == shape and t.is_contiguous()):
+            _buffer(t, call, name, kind)
             raise ValueError(f"{call}: {name} must be {list(shape)}, got {tuple(t.shape)}")
-        return p
-
-    i32, f32 = torch.int32, torch.float32
-    args = (of(tokens, "tokens", i32, (b, s)), of(counts, "counts", i32, (b,), True), of(uniforms, "uniforms", f32, (b, s)),
-            of(noise, "noise", f32, (b, v)))
-    draft_at = of(draft, "draft", dtype, (b, s, v), True)
-    outs = of(accepted, "accepted", i32, (b,)), of(out, "out", i32, (b, s + 1))
-    ws = _buffer(workspace, call, "workspace", None, draft_workspace_bytes(b, v))
-    err = _count(err_count, call)
-    _check(load_library().llvq_draft_verify(at, draft_at, X_F32 if dtype is f32 else X_BF16, *args, b, s, v, *outs, ws, err,
-                                            _raw_stream(stream, target.get_device())), call)
+    ws, size = _buffer(workspace, call, "workspace"), workspace.numel() * workspace.element_size()
+    err = None if err_count is None else _count(err_count, call)
+    code = load_library().llvq_draft_verify(at, None if draft is None else draft.data_ptr(), X_F32 if dtype is f32 else X_BF16,
+                                            tokens.data_ptr(), None if counts is None else counts.data_ptr(), uniforms.data_ptr(),
+                                            noise.data_ptr(), b, s, v, accepted.data_ptr(), out.data_ptr(), ws, size,
+                                            err, _raw_stream(stream, target.get_device()))
+    if code:
+        need = draft_workspace_bytes(b, v)
+        if size < need:
+            raise ValueError(f"{call}: workspace holds {size} bytes; the call needs at least {need}")
+        raise LlvqError(code, call)

@@ -149,6 +149,11 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   return base * cut->splits > (1 << 30) ? LLVQ_EINVAL : LLVQ_OK;  // (a kernel may take twice as many workgroups)
 }
 
+// The splits' sums, maxima and sums of p.
+int64_t workspace_of(const Cut& cut, const llvq_kv_desc* d, int32_t heads, int64_t tokens) {
+  return (int64_t)cut.splits * tokens * heads * (d->head_dim + 2) * 4;
+}
+
 int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch, int32_t max_chunk, int32_t max_len) {
   const int st = check_desc(d);
   if (st != LLVQ_OK) return st;
@@ -258,20 +263,21 @@ LLVQ_API int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads,
                                            int32_t max_chunk, int32_t max_len) {
   int st = check_attn(d, heads, tokens, batch, max_chunk, max_len);
   if (st != LLVQ_OK) return st;
-  int splits = 1;
+  int64_t most = 0;
   for (const bool f32 : {false, true}) {  // either type of query
     Cut cut;
     st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, f32, &cut);
     if (st != LLVQ_OK) return st;
-    if (cut.splits > splits) splits = cut.splits;
+    const int64_t n = cut.splits > 1 ? workspace_of(cut, d, heads, tokens) : 0;
+    if (n > most) most = n;
   }
-  return splits == 1 ? 0 : (int64_t)splits * tokens * heads * (d->head_dim + 2) * 4;
+  return most;
 }
 
 LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
                        int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
                        int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,
-                       int32_t* err_count, void* stream) {
+                       int64_t workspace_bytes, int32_t* err_count, void* stream) {
   Cache c;
   int st = make_cache(d, pool, batch, &c);
   if (st != LLVQ_OK) return st;
@@ -288,7 +294,8 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   Cut cut;
   st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, f32, &cut);
   if (st != LLVQ_OK) return st;
-  if (cut.splits > 1 && (!workspace || !aligned(workspace, 16))) return LLVQ_EINVAL;
+  const int64_t need = cut.splits > 1 ? workspace_of(cut, d, heads, c.tokens) : 0;
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LLVQ_EINVAL;
   AttnArgs a = {};
   a.c = c;
   a.q = q;
@@ -328,7 +335,7 @@ LLVQ_API int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab) {
 LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
                                const int32_t* counts, const float* uniforms, const float* noise, int32_t batch,
                                int32_t drafts, int32_t vocab, int32_t* accepted, int32_t* out, void* workspace,
-                               int32_t* err_count, void* stream) {
+                               int64_t workspace_bytes, int32_t* err_count, void* stream) {
   if (batch < 0 || batch > LLVQ_MAX_SEQS || drafts < 0 || drafts >= kMaxDrafts || vocab < 1) return LLVQ_EINVAL;
   if (dtype != LLVQ_X_F32 && dtype != LLVQ_X_BF16) return LLVQ_EINVAL;
   if (err_count && !aligned(err_count, 4)) return LLVQ_EINVAL;
@@ -338,6 +345,7 @@ LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dt
   if (!aligned(target, size) || !aligned(draft, size) || !aligned(tokens, 4) || !aligned(counts, 4) || !aligned(uniforms, 4) ||
       !aligned(noise, 4) || !aligned(accepted, 4) || !aligned(out, 4) || !aligned(workspace, 8))
     return LLVQ_EINVAL;
+  if (workspace_bytes < llvq_draft_workspace_bytes(batch, vocab)) return LLVQ_EINVAL;
   DraftArgs a = {};
   a.target = target;
   a.draft = draft;
