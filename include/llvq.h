@@ -345,6 +345,7 @@ enum { LLVQ_KV_BF16 = 0, LLVQ_KV_FP8 = 1, LLVQ_KV_FP4 = 2 };
 #define LLVQ_MAX_HEAD_DIM 256
 #define LLVQ_MAX_PAGE 4096
 #define LLVQ_MAX_SEQS 32768
+#define LLVQ_MAX_TOKENS (1 << 27)
 #define LLVQ_MAX_DRAFTS 63
 
 typedef struct {
@@ -368,7 +369,7 @@ typedef struct {
   const int32_t* table;  /* [batch][max_pages]; entries past a sequence's pages are not read */
   int32_t batch;         /* 0..LLVQ_MAX_SEQS (0: nothing to do)                           */
   int32_t max_pages;     /* >= 0                                                          */
-  int32_t tokens;        /* rows of new tokens, >= 0 (0: nothing to do)                   */
+  int32_t tokens;        /* rows of new tokens, 0..LLVQ_MAX_TOKENS (0: nothing to do)     */
 } llvq_batch;
 
 /* Bytes of a pool, or LLVQ_EINVAL.  Host only. */
@@ -403,7 +404,8 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  *   q, out : [tokens][heads][head_dim], LLVQ_X_F32 or LLVQ_X_BF16 (`dtype`, both), channels contiguous; strides in
  *            elements, >= 0; out aligned to 4 elements, its strides multiples of 4.
  *   heads  : a multiple of kv_heads.
- *   max_chunk : at least the new tokens of any sequence (rows of a sequence past it may be left unwritten: counted).
+ *   max_chunk : at least the new tokens of any sequence, and batch * max_chunk >= tokens (rows of a sequence past it
+ *            may be left unwritten: counted).
  *   max_len : at least 1; about the longest length: it decides only how the keys are split, not
  *            what is computed.
  *   scale  : > 0 and finite.   window : 0 (none) .. 2^30.

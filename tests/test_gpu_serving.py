@@ -198,6 +198,8 @@ def check_attn(su, caches, q, out, dtype, window=0, causal=True, scale=None):
     ("fp4", 1, 1, 64, 48, [130], [400], 100),
     ("bf16", 2, 1, 96, 16, [5, 1], [70, 90], 1),                           # each row sees itself alone
     ("fp8", 1, 4, 128, 16, [1, 2], [0, 1], 0),                             # lens shorter than the chunk: empty rows
+    ("fp8", 32, 1, 32, 4, [1] * 70, list(range(70)), 0),                   # workgroups enough without a split
+    ("fp4", 1, 70, 64, 16, [1, 1], [65, 1000], 0),                         # more than 64 rows of one token
 ])
 def test_attention(kind, kv_heads, share, dim, page, new, lens, window, dtype):
     su = Setup(kind, kv_heads, dim, page, new, lens, seed=dim + len(new), max_pages=max(1, -(-max(lens) // page)) + 2)
@@ -328,7 +330,7 @@ def test_arrays_that_do_not_fit_are_bounded_and_counted():
         err.zero_()
         run_attn(su, q, torch.bfloat16, plan=su.plan(starts, lens), err=err)
         assert err.item() > 0, (starts, lens)
-    for page in (-1, su.pages, 1 << 30):
+    for page in (-1, su.pages, 1 << 30, -2 ** 31):
         table = su.table.copy()
         table[1, 1] = page
         err.zero_()
@@ -336,7 +338,7 @@ def test_arrays_that_do_not_fit_are_bounded_and_counted():
         assert err.item() > 0 and torch.equal(out[:2], fine[:2]) and torch.isfinite(out).all()
     err.zero_()
     run_attn(su, dev(su.rng.randn(100, 2, 64).astype(np.float32), torch.bfloat16), torch.bfloat16,
-             plan=su.plan([0, 50, 100], [40, 90]), max_chunk=2, err=err)      # more rows than max_chunk
+             plan=su.plan([0, 90, 100], [40, 90]), max_chunk=50, err=err)     # more rows than max_chunk
     assert err.item() > 0
 
 
@@ -422,7 +424,7 @@ def check_draft(case, counts=None, errors=0):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("b,s,vocab", [(1, 0, 1), (1, 4, 7), (3, 1, 2049), (5, 7, 32000), (40, 3, 1001), (2, 63, 300),
-                                       (1, 2, 100003)])
+                                       (1, 2, 100003), (600, 2, 50), (3, 2, 8193)])
 @pytest.mark.parametrize("certain", [False, True])
 def test_draft_verify(b, s, vocab, dtype, certain):
     case = draft_case(b, s, vocab, dtype, seed=b + s, certain=certain)

@@ -40,7 +40,7 @@ def batch(**over):
 BAD_DESCS = [dict(kind=3), dict(kind=-1), dict(kv_heads=0), dict(kv_heads=1025), dict(head_dim=48), dict(head_dim=0),
              dict(head_dim=288), dict(page_tokens=0), dict(page_tokens=4097), dict(pages=0), dict(pages=-1)]
 BAD_BATCHES = [dict(starts=None), dict(lens=None), dict(table=None), dict(starts=0x10002), dict(lens=0x10001), dict(table=0x10003),
-               dict(batch=-1), dict(batch=32769), dict(max_pages=-1), dict(tokens=-1)]
+               dict(batch=-1), dict(batch=32769), dict(max_pages=-1), dict(tokens=-1), dict(tokens=(1 << 27) + 1)]
 
 
 def kv(lib, name, d=None, pool=P, k=P, ks=(128, 64), v=P, vs=(128, 64), dtype=0, n=None, err=None):
@@ -88,7 +88,7 @@ def test_attn_refusals(lib):
     for bad in BAD_BATCHES:
         assert attn(lib, n=batch(**bad)) == -1, bad
     for bad in (dict(pool=None), dict(pool=ODD), dict(q=None), dict(out=None), dict(q=ctypes.c_void_p(0x10001)), dict(out=ODD),
-                dict(dtype=0, out=ctypes.c_void_p(0x10008)), dict(dtype=2), dict(heads=0), dict(heads=7), dict(heads=1),
+                dict(dtype=0, out=ctypes.c_void_p(0x10008)), dict(dtype=2), dict(heads=0), dict(heads=7), dict(heads=1), dict(max_chunk=1),
                 dict(qs=(-1, 64)), dict(os_=(510, 64)), dict(os_=(512, 62)), dict(os_=(-4, 64)), dict(max_chunk=0), dict(max_len=0),
                 dict(max_len=(1 << 30) + 1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")),
                 dict(window=-1), dict(window=(1 << 30) + 1), dict(ws=None), dict(ws=ODD), dict(size=0), dict(size=wd.attn_workspace_bytes(desc(), 8, 3, 2, 2, 4000) - 1),
@@ -96,11 +96,11 @@ def test_attn_refusals(lib):
         assert attn(lib, **bad) == -1, bad
     assert attn(lib, q=None, out=None, ws=None, n=batch(tokens=0)) == 0
     for args in ((7, 10, 2, 2, 100), (8, -1, 2, 2, 100), (8, 10, -1, 2, 100), (8, 10, 2, 0, 100), (8, 10, 2, 2, 0),
-                 (8, 1 << 31, 2, 2, 100), (8, 10, 32769, 2, 100)):
+                 (8, 1 << 31, 2, 2, 100), (8, 10, 32769, 2, 100), (8, 5, 2, 2, 100), (8, 4, 32768, 1 << 20, 100)):
         assert lib.llvq_attn_workspace_bytes(ctypes.byref(desc()), *args) == -1, args
-    assert wd.attn_workspace_bytes(desc(), 8, 10, 2, 2, 100) == 0               # a short axis is not split
-    many = wd.attn_workspace_bytes(desc(), 8, 10, 2, 2, 100000)
-    assert many > 0 and many % (10 * 8 * (64 + 2) * 4) == 0
+    assert wd.attn_workspace_bytes(desc(), 8, 4, 2, 2, 100) == 0               # a short axis is not split
+    many = wd.attn_workspace_bytes(desc(), 8, 4, 2, 2, 100000)
+    assert many > 0 and many % (4 * 8 * (64 + 2) * 4) == 0
 
 
 def draft(lib, target=P, q=P, dtype=0, tokens=P, counts=P, uni=P, noise=P, b=2, s=3, vocab=100, acc=P, out=P, ws=P, size=1 << 20, err=None):
@@ -149,6 +149,9 @@ class _OnGpu(torch.Tensor):
     def is_cuda(self):
         return True
 
+    def get_device(self):
+        return 0
+
 
 def g(t):
     return torch.Tensor._make_subclass(_OnGpu, t)
@@ -163,6 +166,28 @@ def no_library(monkeypatch):
     def sentinel(*a, **k):
         raise _Reached()
     monkeypatch.setattr(wd, "load_library", sentinel)
+
+
+class _OnOther(_OnGpu):
+    def get_device(self):
+        return 1
+
+
+def other(t):
+    return torch.Tensor._make_subclass(_OnOther, t)
+
+
+def test_tensors_on_several_devices_are_refused(no_library):
+    for over in (dict(v=other(torch.zeros(5, 2, 64))), dict(pool=other(torch.zeros(1 << 16, dtype=torch.uint8))),
+                 dict(table=other(torch.zeros(3, 2, dtype=torch.int32))), dict(err_count=other(torch.zeros(1, dtype=torch.int32)))):
+        with pytest.raises(ValueError, match="devices"):
+            wd.kv_write(**kv_args(**over))
+    for over in (dict(out=other(torch.zeros(5, 6, 64))), dict(workspace=other(torch.zeros(64, dtype=torch.uint8)))):
+        with pytest.raises(ValueError, match="devices"):
+            wd.attn(**attn_args(**over))
+    for over in (dict(noise=other(torch.zeros(2, 10))), dict(workspace=other(torch.zeros(64, dtype=torch.uint8)))):
+        with pytest.raises(ValueError, match="devices"):
+            wd.draft_verify(**draft_args(**over))
 
 
 def i32(*shape):

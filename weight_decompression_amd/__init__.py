@@ -167,13 +167,15 @@ def _stream(stream):
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _raw_stream(stream, device):
-    """The handle of `stream`, or of torch's current stream on a device, without a Stream object
-    (which costs 3 us, as much as a launch)."""
-    if stream is not None:
-        return stream
+def _launch(function, device, stream, *args):
+    """Calls a C entry (its last argument the stream) with a device current: on `stream`, or on torch's
+    current stream of that device, whose handle is taken without a Stream object (which costs 3 us, as much
+    as a launch)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device)
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _launch(function, device, stream, *args)
+    return function(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
 
 
 # ---------------------------------------------------------------------------
@@ -423,9 +425,18 @@ def _buffer(t, call, name, dtype=None, nbytes=0):
     return t.data_ptr()
 
 
-def _count(err_count, call):
+def _count(err_count, device, call):
     import torch
-    return _buffer(err_count, call, "err_count", torch.int32, 4)
+    at = _buffer(err_count, call, "err_count", torch.int32, 4)
+    _one_device(call, device, err_count)
+    return at
+
+
+def _space(workspace, device, call):
+    """A workspace's address and bytes."""
+    at = _buffer(workspace, call, "workspace")
+    _one_device(call, device, workspace)
+    return at, workspace.numel() * workspace.element_size()
 
 
 def _rows(t, call, name, heads, dim):
@@ -457,13 +468,19 @@ def _apart(t, call, name):
         raise ValueError(f"{call}: {name} has rows that overlap (strides {t.stride()})")
 
 
-def _paged(desc, pool, starts, lens, table, tokens, call):
+def _one_device(call, device, *tensors):
+    if any(t.get_device() != device for t in tensors):
+        raise ValueError(f"{call}: tensors on several devices")
+
+
+def _paged(desc, pool, starts, lens, table, tokens, device, call):
     """The pool's address and llvq_batch from starts [B + 1], lens [B] and table [B][max_pages] (int32)."""
     import torch
     i32 = torch.int32
     need = _pool_nbytes(desc)
     try:
-        good = (pool.is_cuda and starts.is_cuda and lens.is_cuda and table.is_cuda and pool.dtype is torch.uint8 and
+        good = (pool.get_device() == starts.get_device() == lens.get_device() == table.get_device() == device and
+                pool.dtype is torch.uint8 and
                 starts.dtype is i32 and lens.dtype is i32 and table.dtype is i32 and pool.is_contiguous() and
                 starts.is_contiguous() and lens.is_contiguous() and table.is_contiguous() and pool.numel() >= need)
     except AttributeError:
@@ -472,6 +489,7 @@ def _paged(desc, pool, starts, lens, table, tokens, call):
         _buffer(pool, call, "pool", torch.uint8, need)
         for t, name in ((starts, "starts"), (lens, "lens"), (table, "table")):
             _buffer(t, call, name, i32)
+        _one_device(call, device, pool, starts, lens, table)
     n, shape = lens.shape, table.shape
     if len(n) != 1 or len(shape) != 2 or shape[0] != n[0] or starts.shape != (n[0] + 1,):
         raise ValueError(f"{call}: starts, lens and table must be [B + 1], [B] and [B][max_pages], got "
@@ -484,7 +502,7 @@ def _pair(call, a, b, names, heads, dim):
     import torch
     try:
         shape, sa, sb, dtype = a.shape, a.stride(), b.stride(), a.dtype
-        good = (a.is_cuda and b.is_cuda and (dtype is torch.bfloat16 or dtype is torch.float32) and b.dtype is dtype and
+        good = (0 <= a.get_device() == b.get_device() and (dtype is torch.bfloat16 or dtype is torch.float32) and b.dtype is dtype and
                 b.shape == shape and len(shape) == 3 and shape[1] == heads and shape[2] == dim and sa[2] == 1 and sb[2] == 1)
     except (AttributeError, IndexError):
         good = False
@@ -494,6 +512,7 @@ def _pair(call, a, b, names, heads, dim):
         if a.shape != b.shape or a.dtype is not b.dtype:
             raise ValueError(f"{call}: {names[0]} and {names[1]} must have one shape and dtype, got {tuple(a.shape)} {a.dtype} and "
                              f"{tuple(b.shape)} {b.dtype}")
+        _one_device(call, a.get_device(), b)
         sa, sb, dtype = a.stride(), b.stride(), a.dtype
     return a.data_ptr(), sa[0], sa[1], b.data_ptr(), sb[0], sb[1], X_F32 if dtype is torch.float32 else X_BF16
 
@@ -503,9 +522,10 @@ def _kv_call(call, desc, pool, k, v, starts, lens, table, err_count, stream):
     if call == "llvq_kv_read":
         _apart(k, call, "k")
         _apart(v, call, "v")
-    at, batch = _paged(desc, pool, starts, lens, table, k.shape[0], call)
-    err = None if err_count is None else _count(err_count, call)
-    code = getattr(load_library(), call)(desc, at, *rows, batch, err, _raw_stream(stream, k.get_device()))
+    device = k.get_device()
+    at, batch = _paged(desc, pool, starts, lens, table, k.shape[0], device, call)
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(getattr(load_library(), call), device, stream, desc, at, *rows, batch, err)
     if code:
         raise LlvqError(code, call)
 
@@ -542,12 +562,12 @@ def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len,
         raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
     *rows, dtype = _pair(call, q, out, ("q", "out"), heads, desc.head_dim)
     _apart(out, call, "out")
-    at, batch = _paged(desc, pool, starts, lens, table, q.shape[0], call)
-    ws, size = (None, 0) if workspace is None else (_buffer(workspace, call, "workspace"), workspace.numel() * workspace.element_size())
-    err = None if err_count is None else _count(err_count, call)
-    code = load_library().llvq_attn(desc, at, *rows, dtype, heads, batch, max_chunk, max_len,
-                                    desc.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, size,
-                                    err, _raw_stream(stream, q.get_device()))
+    device = q.get_device()
+    at, batch = _paged(desc, pool, starts, lens, table, q.shape[0], device, call)
+    ws, size = (None, 0) if workspace is None else _space(workspace, device, call)
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(load_library().llvq_attn, device, stream, desc, at, *rows, dtype, heads, batch, max_chunk, max_len,
+                   desc.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, size, err)
     if code:
         need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
         if size < need:
@@ -584,16 +604,17 @@ def draft_verify(target, draft, tokens, uniforms, noise, accepted, out, workspac
         each += ((draft, "draft", dtype, (b, s, v)),)
     if counts is not None:
         each += ((counts, "counts", i32, (b,)),)
+    device = target.get_device()
     for t, name, kind, shape in each:
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is kind and t.shape == shape and t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is kind and t.shape == shape and t.is_contiguous()):
             _buffer(t, call, name, kind)
+            _one_device(call, device, t)
             raise ValueError(f"{call}: {name} must be {list(shape)}, got {tuple(t.shape)}")
-    ws, size = _buffer(workspace, call, "workspace"), workspace.numel() * workspace.element_size()
-    err = None if err_count is None else _count(err_count, call)
-    code = load_library().llvq_draft_verify(at, None if draft is None else draft.data_ptr(), X_F32 if dtype is f32 else X_BF16,
-                                            tokens.data_ptr(), None if counts is None else counts.data_ptr(), uniforms.data_ptr(),
-                                            noise.data_ptr(), b, s, v, accepted.data_ptr(), out.data_ptr(), ws, size,
-                                            err, _raw_stream(stream, target.get_device()))
+    ws, size = _space(workspace, device, call)
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(load_library().llvq_draft_verify, device, stream, at, None if draft is None else draft.data_ptr(),
+                   X_F32 if dtype is f32 else X_BF16, tokens.data_ptr(), None if counts is None else counts.data_ptr(),
+                   uniforms.data_ptr(), noise.data_ptr(), b, s, v, accepted.data_ptr(), out.data_ptr(), ws, size, err)
     if code:
         need = draft_workspace_bytes(b, v)
         if size < need:

@@ -277,7 +277,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   constexpr int kLoads = 32 * kRaw / kWave;        // chunks a lane loads of a piece
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
   constexpr int kSteps = DP / 32, kOut = DP / 16;
-  constexpr int32_t kNoKey = INT32_MIN;
   const Cache& c = a.c;
   using Lds = FewLds<DP>;
   __shared__ __align__(16) uint8_t lds[WAVES * Lds::kWaveBytes];
@@ -308,10 +307,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   const bool in_row = ch * 16 < c.row;
   bool lost = false;
   // the page number of this lane's key of a piece (lanes 32..63 as 0..31)
+  auto is_key = [&](int tile, int j) { return tile < w.tile_hi && j >= w.first_key && j < w.last_key; };
   auto page_of = [&](int tile) -> int32_t {
     const int j = (tile * WAVES + wave) * 32 + (lane & 31);
-    if (tile >= w.tile_hi || j < w.first_key || j >= w.last_key) return kNoKey;
-    return table[divide((uint32_t)j, c.page)];
+    return is_key(tile, j) ? table[divide((uint32_t)j, c.page)] : 0;
   };
   // A lane's key of a piece, lane % 32, tells where the piece's rows lie, and with lane / 32 whose scales it
   // holds; a lane loads chunk `ch` of keys i * 64 / kRaw + lane / kRaw.
@@ -325,8 +324,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   uint32_t scales[kWords], next_scales[kWords], gone = 0, next_gone = 0;  // of the piece that is staged, and of the next
   auto locate = [&](int tile, int32_t ids) {
     const uint32_t j = (uint32_t)((tile * WAVES + wave) * 32 + (lane & 31));
-    const bool ok = ids >= 0 && ids < c.pages;
-    lost |= !ok && ids != kNoKey;
+    const bool key = is_key(tile, (int)j), ok = key && ids >= 0 && ids < c.pages;
+    lost |= key && !ok;
     next_gone = (uint32_t)__ballot(!ok);
     // a place that is not there is read from the pool's start and left out when it is staged
     const int slot = ok ? (int)(j - divide(j, c.page) * c.page.by) : 0;
@@ -693,7 +692,6 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   // the byte of a place's scales that belongs to the thread's chunks
   const int k_shift = kc.ch * kOf / 4 % 4 * 8, v_shift = vc.ch * kOf / 4 % 4 * 8;
   const int k_word = kc.ch * kOf / 16, v_word = part_dim / 128;
-  constexpr int32_t kNoKey = INT32_MIN;
   u32x4 raw_k[KChunks::kPer], raw_v[VChunks::kPer];
   uint32_t sc_k[KChunks::kPer], sc_v[VChunks::kPer];
   uint64_t gone = 0, nonfinite = 0;  // of the loaded tile
@@ -702,19 +700,21 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   // Where a tile's keys lie and how they are scaled is worked out once a key, by the wave whose turn it is: the
   // page numbers are loaded five rounds ahead, the scales four, both written to LDS three and the codes loaded
   // two rounds ahead.
-  int32_t ids = kNoKey;
+  int32_t ids = 0;
   Where found;
   bool found_ok = false;
+  auto is_key = [&](int tile, int j) { return lane < kKeys && tile < w.tile_hi && j >= w.first_key && j < w.last_key; };
   auto load_pages = [&](int tile) {
     if (wave != (tile & (WAVES - 1))) return;
     const int j = tile * kKeys + lane;
-    ids = lane < kKeys && tile < w.tile_hi && j >= w.first_key && j < w.last_key ? table[divide((uint32_t)j, c.page)] : kNoKey;
+    ids = is_key(tile, j) ? table[divide((uint32_t)j, c.page)] : 0;
   };
   auto load_scales = [&](int tile) {
     if (wave != (tile & (WAVES - 1))) return;
     const uint32_t j = (uint32_t)(tile * kKeys + lane);
-    found_ok = ids >= 0 && ids < c.pages;
-    lost |= !found_ok && ids != kNoKey;
+    const bool key = is_key(tile, (int)j);
+    found_ok = key && ids >= 0 && ids < c.pages;
+    lost |= key && !found_ok;
     // a place that is not there is read from the pool's start and left out when it is staged
     const int slot = found_ok ? (int)(j - divide(j, c.page) * c.page.by) : 0;
     const int64_t blk = found_ok ? (int64_t)ids * page_bytes + head_off : 0;

@@ -33,7 +33,7 @@ int check_desc(const llvq_kv_desc* d) {
 int make_cache(const llvq_kv_desc* d, const void* pool, const llvq_batch* n, Cache* c) {
   const int st = check_desc(d);
   if (st != LLVQ_OK) return st;
-  if (!n || n->batch < 0 || n->batch > LLVQ_MAX_SEQS || n->tokens < 0 || n->max_pages < 0) return LLVQ_EINVAL;
+  if (!n || n->batch < 0 || n->batch > LLVQ_MAX_SEQS || n->tokens < 0 || n->tokens > LLVQ_MAX_TOKENS || n->max_pages < 0) return LLVQ_EINVAL;
   if (n->batch > 0 && n->tokens > 0) {
     if (!pool || !n->starts || !n->lens || (n->max_pages > 0 && !n->table)) return LLVQ_EINVAL;
     if (!aligned(pool, 16) || !aligned(n->starts, 4) || !aligned(n->lens, 4) || !aligned(n->table, 4)) return LLVQ_EINVAL;
@@ -120,33 +120,50 @@ struct Cut {
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, bool f32, Cut* cut) {
-  const int64_t rows = (int64_t)max_chunk * share;
-  cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1) ? 1 : 2;
-  // Eight waves stage a tile for 256 rows: 539 us instead of 594 at chunks of 2 x 2048 rows of 128-wide heads over 8192 keys, 220 instead
-  // of 391 at 256-wide heads; 64-wide heads run better with three workgroups of four a compute unit
-  cut->waves = cut->cols ? 4 : rows <= 128 || f32 || d->head_dim <= 64 ? 4 : 8;
+// The rules go by sizes that the host knows; times are of whole calls on one MI355X.
+// A window only makes the splits fewer.
+int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chunk, int32_t max_len, int32_t window, bool f32,
+           Cut* cut) {
+  if (window > 0 && max_len - max_chunk > window) max_len = window + max_chunk;
+  const int64_t rows = (int64_t)max_chunk * share, seqs = (int64_t)d->kv_heads * (batch > 0 ? batch : 1);
+  const int dim = padded_dim(d->head_dim), parts = dim > 128 ? 2 : 1, terms = f32 ? 3 : 1;
+  if (rows * seqs > (1ll << 33)) return LLVQ_EINVAL;
+  cut->waves = 4;
+  cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, dim, terms) ? 1 : 2;
+  // Eight waves stage a tile for 256 rows: 539 us instead of 594 at chunks of 2 x 2048 rows of 128-wide heads over 8192
+  // keys, 220 instead of 391 at 256-wide heads.  64-wide heads run better with three workgroups of four a compute unit,
+  // and where 256 rows a workgroup leave compute units idle, 128 do better (369 rows of 32 heads: 17 us instead of 19)
+  if (!cut->cols && !f32 && dim > 64 && rows > 128 && (rows + 255) / 256 * seqs * parts >= 256) cut->waves = 8;
   const int64_t per = cut->cols ? 16 * cut->cols : 32 * cut->waves;
-  const int64_t blocks = (rows + per - 1) / per;
-  const int64_t base = blocks * d->kv_heads * (batch > 0 ? batch : 1);
-  if (base > (1ll << 30)) return LLVQ_EINVAL;
-  const int64_t made = cut->cols || d->head_dim <= 128 ? base : 2 * base;  // (wide heads in halves)
-  int64_t want = ((cut->cols ? 2048 : 4096 / cut->waves) + made - 1) / made;
+  const int64_t blocks = (rows + per - 1) / per, base = blocks * seqs;
+  if (base > (1ll << 29)) return LLVQ_EINVAL;
+  int64_t s;
   if (cut->cols) {
-    // one round of resident workgroups where a sequence is cut into many parts (three sequences of 131000 keys in e2m1:
-    // 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all lengths (64 of up to
-    // 16384 in e4m3: 268 us at 2048, 295 at 1024)
-    const int64_t resident = 256 * few_waves(d->kind, padded_dim(d->head_dim), f32 ? 3 : 1, cut->cols);
-    if (base <= resident / 2) want = resident / base;
+    // One round of resident workgroups where a sequence is cut into many parts (three sequences of 131000 keys in e2m1:
+    // 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all lengths (64 of up to 16384 in
+    // e4m3: 268 us at 2048, 295 at 1024), no split where they fill the chip twice (57 x 32 of up to 176 keys: 54 us, 72 split)
+    const int64_t resident = 256 * few_waves(d->kind, dim, terms, cut->cols);
+    s = base >= 2 * resident ? 1 : base > resident / 2 ? (2048 + base - 1) / base : resident / base;
+    const int64_t most = ((int64_t)max_len + 127) / 128;
+    if (s > most) s = most;
+    // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to three pieces (at
+    // 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups 7.4 us and the join 4.6 after it)
+    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= 768) cut->waves = 8, s = 1;
+  } else {
+    // A split shortens a workgroup's way (about 1 us a tile of 64 keys; f32 and wide heads more) and costs its sums' way
+    // out and back (8 bytes a channel of every row at 5 TB/s): the least of tiles / s + cost * s, up to two rounds of
+    // workgroups (3 x 295 rows of 12 heads in a window of 1932 keys: 37 us at 6 splits, 56 at 12)
+    const int64_t slots = 256 * (cut->waves == 8 ? 1 : dim == 64 && !f32 ? 3 : 2);
+    const double tiles = max_len / 64.0 * (f32 ? 2.5 : 1.0) * parts, cost = (double)rows * seqs * d->head_dim * 8.0 / 5e6;
+    s = (2 * slots + base * parts / 2) / (base * parts);
+    const int64_t best = (int64_t)sqrt(tiles / cost), most = ((int64_t)max_len + 127) / 128;
+    if (s > best) s = best;
+    if (s > most) s = most;
   }
-  const int64_t most = ((int64_t)max_len + (cut->cols ? 127 : 511)) / (cut->cols ? 128 : 512);
-  int64_t s = want < most ? want : most;
-  // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to three pieces (at
-  // 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups 7.4 us and the join 4.6 after it)
-  if (cut->cols == 1 && padded_dim(d->head_dim) <= 128 && base <= 256 && max_len <= 768) cut->waves = 8, s = 1;
   cut->splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
   cut->row_blocks = (int)blocks;
-  return base * cut->splits > (1 << 30) ? LLVQ_EINVAL : LLVQ_OK;  // (a kernel may take twice as many workgroups)
+  // (a launch has fewer than 2^32 threads)
+  return base * cut->splits * parts * 64 * cut->waves >= (1ll << 32) ? LLVQ_EINVAL : LLVQ_OK;
 }
 
 // The splits' sums, maxima and sums of p.
@@ -159,6 +176,7 @@ int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t bat
   if (st != LLVQ_OK) return st;
   if (heads < d->kv_heads || heads % d->kv_heads || heads > 65536) return LLVQ_EINVAL;
   if (tokens < 0 || tokens * heads > 0x7fffffff || batch < 0 || batch > LLVQ_MAX_SEQS) return LLVQ_EINVAL;
+  if (tokens > (int64_t)batch * max_chunk) return LLVQ_EINVAL;
   if (max_chunk < 1 || max_len < 1 || max_len > kMaxLen || (int64_t)max_chunk * heads > 0x7fffffff) return LLVQ_EINVAL;
   return LLVQ_OK;
 }
@@ -266,7 +284,7 @@ LLVQ_API int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads,
   int64_t most = 0;
   for (const bool f32 : {false, true}) {  // either type of query
     Cut cut;
-    st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, f32, &cut);
+    st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, 0, f32, &cut);
     if (st != LLVQ_OK) return st;
     const int64_t n = cut.splits > 1 ? workspace_of(cut, d, heads, tokens) : 0;
     if (n > most) most = n;
@@ -292,7 +310,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   if (!q || !out || !aligned(q, size) || !aligned(out, 4 * size)) return LLVQ_EINVAL;
   if (q_token < 0 || q_head < 0 || out_token < 0 || out_head < 0 || out_token % 4 || out_head % 4) return LLVQ_EINVAL;
   Cut cut;
-  st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, f32, &cut);
+  st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, window, f32, &cut);
   if (st != LLVQ_OK) return st;
   const int64_t need = cut.splits > 1 ? workspace_of(cut, d, heads, c.tokens) : 0;
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LLVQ_EINVAL;
