@@ -82,20 +82,34 @@ def build(verbose=True, device_checks=False):
         "-O3",
         "-std=c++17",
         "-fPIC",
-        "-shared",
         "-fvisibility=hidden",
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall",
         "-I", INCLUDE,
         "-I", CSRC,
         "-I", BUILD_DIR,
-        "-o", tmp,
-        os.path.join(CSRC, "llvq.hip"),
-        os.path.join(CSRC_SERVE, "llvq_serve.hip"),
     ]
     if device_checks:
         cmd.insert(1, "-DLLVQ_DEVICE_CHECKS")
-    _run(cmd, verbose)
+    # the two units are compiled side by side, into names private to this process
+    units = [os.path.join(CSRC, "llvq.hip"), os.path.join(CSRC_SERVE, "llvq_serve.hip")]
+    objects = [os.path.join(BUILD_DIR, f"{os.path.basename(out)}.{i}.{os.getpid()}.tmp.o") for i in range(len(units))]
+    try:
+        runs = []
+        for unit, obj in zip(units, objects):
+            one = cmd + ["-c", "-o", obj, unit]
+            if verbose:
+                print("+ " + " ".join(one), flush=True)
+            runs.append((one, subprocess.Popen(one)))
+        codes = [(one, run.wait()) for one, run in runs]
+        for one, code in codes:
+            if code:
+                raise subprocess.CalledProcessError(code, one)
+        _run([hipcc_path(), f"--offload-arch={OFFLOAD_ARCH}", "-fPIC", "-shared", "-o", tmp, *objects], verbose)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, out)
     return out
 

@@ -2,22 +2,23 @@
 //
 //   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i),
 //
-// over the keys j of the sequence that row i may see, in one pass over the keys: m_i is a running
-// maximum, and what was summed under an older maximum is multiplied by exp(old - new).
+// over the keys j of the sequence that row i may see, in one pass over the keys: m_i is a running maximum,
+// and what was summed under an older maximum is multiplied by exp(old - new).
 //
-// The queries that share a key head are the columns of one product: row r = t * G + g of a (sequence,
-// key head) is token t's g-th query head.  Both products are taken transposed, S^T = K Q^T and
-// O^T = V^T P^T, on 32x32x16 bf16 matrix instructions.  In the result layout a lane holds one column
-// (lane % 32), so a row's maximum, sum and rescaling are the lane's own (and its partner's, lane ^ 32),
-// and S^T's registers are, after exp and packing, P^T's operand without any exchange: a lane holds keys
-// 8 * (i / 4) + 4 * (lane / 32) + i % 4, so the second product simply takes its keys in that order, and
-// reads V from LDS through the transposing 64-bit load, four keys of one channel at a time.
+// The queries that share a key head are the columns of one product: row r = t * G + g of a (sequence, key
+// head) is token t's g-th query head.  Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T,
+// on bf16 matrix instructions (32x32x16 for many rows, 16x16x32 for few).  In the result layout of the
+// first a lane holds one column (lane % 32), so a row's maximum, sum and rescaling are the lane's own (and
+// its partner's, lane ^ 32), and S^T's registers are, after exp and packing, P^T's operand without any
+// exchange: a lane holds keys 8 * (i / 4) + 4 * (lane / 32) + i % 4, so the second product simply takes its
+// keys in that order, and reads V from LDS through the transposing 64-bit load, four keys of one channel at
+// a time.
 //
-// Codes become bf16 exactly (at most 4 significant bits times a power of two), so staging a tile as bf16 in LDS
-// loses nothing.  Scores, maxima, sums and outputs are f32.  P is rounded to bf16 (relative 2^-8 at most, the
-// same as the rounding of a bf16 output), and the sum of P is that of the rounded values, so that their
-// common part cancels.  For f32 queries both Q and P are split into three bf16 terms
-// (x = hi + mid + lo, what is left is below 2^-26 |x|), three matrix instructions in the place of one.
+// Codes become bf16 exactly (at most 4 significant bits times a power of two), so staging a tile as bf16 in
+// LDS loses nothing.  Scores, maxima, sums and outputs are f32.  P is rounded to bf16 (relative 2^-8 at
+// most, the same as the rounding of a bf16 output), and the sum of P is that of the rounded values, so that
+// their common part cancels.  For f32 queries both Q and P are split into three bf16 terms (x = hi + mid +
+// lo, what is left is below 2^-26 |x|), three matrix instructions in the place of one.
 //
 // Two kernels share this: k_attn_few for up to 64 rows of a (sequence, key head), where a workgroup's waves
 // share out the keys, and k_attn_many, where they share out the rows.
@@ -41,7 +42,6 @@ struct AttnArgs {
   int32_t* err;
 };
 
-constexpr int kManyRows = 128;        // rows of a workgroup of k_attn_many
 constexpr float kRescaleStep = 8.0f;  // log2: how far a maximum may be passed before the sums are rescaled
 
 __device__ __forceinline__ float half_max(float x) {
@@ -207,7 +207,8 @@ __device__ __forceinline__ float masked(float s, int j, int lo, int seen) {
   return (uint32_t)(j - lo) < (uint32_t)seen ? s : -INFINITY;
 }
 
-// Four scale bytes of a token (from byte 4 n on; 127, one, past the last), in loads as wide as their place allows.
+// Four scale bytes of a token (from byte 4 n on; 127, one, past the last), in loads as wide as their place
+// allows.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* sp, int groups, int n) {
   if (groups % 4 == 0) return 4 * n < groups ? *reinterpret_cast<const uint32_t*>(sp + 4 * n) : 0x7f7f7f7fu;
   uint32_t word = 0;
@@ -229,17 +230,22 @@ __device__ __forceinline__ bool has_255(uint32_t word) {
 
 // Few rows: up to 64 rows of a (sequence, key head), in CT tiles of 16 columns.
 //
-// A decode step reads each cached byte for a handful of rows, so HBM bounds it and what counts is loads
-// in flight.  Every wave therefore runs by itself: it takes every fourth (or eighth) 32-key piece of the
-// workgroup's share, stages it in its own 64 * DP bytes of LDS (the keys, then the values in the same place) and waits for
-// nothing but its own loads, which are issued a piece ahead (page numbers two pieces ahead).  With 16x16x32
-// instructions a lane holds 8 scores of a piece, and a tile of outputs takes DP / 4 registers of a lane.
-// In S^T's layout a lane (column lane % 16, g = lane / 16) holds keys 4 g + i and 16 + 4 g + i, which are
-// taken as the eight consecutive keys of its place in the second product; the transposing load reads
-// V's rows in the same order.
-// Rows in LDS are padded, so that every address is one register and a constant: by 16 bytes for the keys
-// (16 rows at one 16-byte chunk fall on 16 different slots of 256 bytes), by 32 for the values (the eight
-// rows that half a wave takes at 32 bytes of channels fall on eight different segments).
+// A decode step reads each cached byte for a handful of rows, so HBM bounds it and what counts is loads in
+// flight.  Every wave therefore runs by itself: it takes every fourth (or eighth) 32-key piece of the
+// workgroup's share, stages it in its own 64 * DP bytes of LDS (the keys, then the values in the same
+// place) and waits for nothing but its own loads, which are issued a piece ahead (page numbers two pieces
+// ahead).  With 16x16x32 instructions a lane holds 8 scores of a piece, and a tile of outputs takes DP / 4
+// registers of a lane. (Tiles shared by the workgroup, with the kernel below and its barriers, took a step
+// of 64 sequences of up to 16384 tokens, 64 heads over 8 key heads of 128 channels in e4m3, 837 us; this
+// takes 261 us, 5.4 TB/s, where a large copy reaches 4.9.  Three sequences of up to 131000 tokens in e2m1:
+// 75 us, 4.4 TB/s; 16 of up to 4096 with 8 drafts each, f32, 32 heads: 83 us, 4.4 TB/s.  One token of 32
+// heads over 777 keys in bf16 takes 7.5 us and the join 4: a chain of six loads, each waiting for the one
+// before.) In S^T's layout a lane (column lane % 16, g = lane / 16) holds keys 4 g + i and 16 + 4 g + i,
+// which are taken as the eight consecutive keys of its place in the second product; the transposing load
+// reads V's rows in the same order. Rows in LDS are padded, so that every address is one register and a
+// constant: by 16 bytes for the keys (16 rows at one 16-byte chunk fall on 16 different slots of 256
+// bytes), by 32 for the values (the eight rows that half a wave takes at 32 bytes of channels fall on eight
+// different segments).
 template <int DP>
 struct FewLds {
   static constexpr int kKeyRow = DP * 2 + 16, kValueRow = DP * 2 + 32;
@@ -577,13 +583,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   }
 }
 
-// Many rows: 128 or 256 rows of a (sequence, key head), 32 columns a wave, tiles shared by the four or eight waves.
+// Many rows: 128 or 256 rows of a (sequence, key head), 32 columns a wave, tiles shared by the four or
+// eight waves.
 //
 // A chunk of a prompt reuses every key for many rows, so the matrix instructions bound it, next to exp and
-// what else the softmax costs on the vector units.  Two waves a SIMD (of two workgroups, or of what registers
-// allow) let one's softmax run under the other's products.  Tiles are double-buffered in LDS: after the one barrier
-// of a round the next tile, whose codes were loaded a round ago, is expanded into the other buffer, the loads of the one after it are issued,
-// and the round's products are taken.  32x32x16 instructions read an operand of 32 keys for 32 columns.
+// what else the softmax costs on the vector units (a matrix instruction of 32 cycles makes 512 scores of a
+// key step of 16 channels; exp alone is 8 cycles for 64 of them).  Two waves a SIMD let one's softmax run
+// under the other's products.  Tiles are double-buffered in LDS: after the one barrier of a round come the
+// first product and the softmax, then the next tile, whose codes were loaded a round ago, is expanded into
+// the other buffer and the loads of the one after it are issued, then the second product.  Operands are
+// read four instructions ahead in a pinned order.
+//
+// Measured at 2 x 2048 new tokens over 8192, 32 heads of 128 channels in e4m3: 490 us, 980 TFLOP/s, 82 % of
+// what a large bf16 library product reaches.  Without the staging 80 us less, without the softmax 65,
+// without both 370 us, near the 290 us that the same instructions take alone (the clock falls under them).
+// 64-wide heads have twice the softmax a product: 24 heads over 4 key heads in e2m1, window 1000, 79 us,
+// 415 TFLOP/s.
+//
+// Heads of more than 128 channels are taken in two halves of the output by two workgroups, which both take
+// the first product: half again the products, but what a wave holds fits two waves a SIMD (16 heads of 256
+// channels in bf16, 3 x 700 over 3500: 220 us instead of 391 at the time).
 template <int KIND, int DP, int NT, int WAVES>
 struct ManyShape {
   static constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES;
@@ -598,8 +617,8 @@ struct ManyShape {
   // registers: queries, outputs, scores, P, operands read ahead, chunks in flight
   static constexpr int kHeld = NT * DP / 4 + kOutDim / 2 + 16 * kSub + 8 * NT * kSub + 16 + 30 +
                                5 * (kKeys * code_bytes(KIND, DP + kOutDim) / 16 / kThreads);
-  // waves a SIMD; narrow heads spend their time on the softmax, not on products, and gain from a third (ragged chunks
-  // of 64-wide heads: 88 us instead of 105)
+  // waves a SIMD; narrow heads spend their time on the softmax, not on products, and gain from a third
+  // (ragged chunks of 64-wide heads: 88 us instead of 105)
   static constexpr int kWaves = DP == 64 && NT == 1 && WAVES == 4 ? 3 : kHeld <= 256 ? 2 : 1;
   static constexpr int kAhead = DP == 64 ? 2 : 4;            // operands read ahead
 };
@@ -637,8 +656,8 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   __shared__ uint32_t bad_keys[3][kSub];
   using Where = Place<KIND, DP>;
   __shared__ Where places[2][kKeys];
-  // of a tile: keys that are not there, and keys with a value that is not finite (in the quantised kinds, where the
-  // scales tell)
+  // of a tile: keys that are not there, and keys with a value that is not finite (in the quantised kinds,
+  // where the scales tell)
   __shared__ uint64_t missing[2], spoilt[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -975,8 +994,9 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
 
 // Joins the splits of a row under their common maximum.  A lane first takes the maximum and sum of two
 // splits, so that the weights of all are known after one round of loads; then 64 / LANES splits of a wave
-// are read side by side, four channels a lane, and what the waves of a row have is added in order through LDS.  WAVES
-// waves a row: one where rows are many and splits few, four where a long axis left few rows of many splits.
+// are read side by side, four channels a lane, and what the waves of a row have is added in order through
+// LDS.  WAVES waves a row: one where rows are many and splits few, four where a long axis left few rows of
+// many splits.
 constexpr int kMaxSplits = 128;
 
 template <bool F32, int LANES, int WAVES>

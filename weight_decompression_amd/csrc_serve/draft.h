@@ -1,14 +1,14 @@
-// The check of drafted tokens.  Draft i of a sequence, drawn from q_i, is accepted while
-// u_i q_i(x_i) < p_i(x_i) (u uniform in [0, 1): with probability min(1, p / q)); the first one that is not
-// is replaced by a token drawn from the rest, max(p - q, 0), and after all of them one more is drawn from p.
-// A draw from weights w is argmax_v w_v / e_v with e exponential: the race whose winner is v with
-// probability w_v / sum w.  It needs no sum, so no order of summation can change a token.
+// The check of drafted tokens.  Draft i of a sequence, drawn from q_i, is accepted while u_i q_i(x_i) <
+// p_i(x_i) (u uniform in [0, 1): with probability min(1, p / q)); the first one that is not is replaced by
+// a token drawn from the rest, max(p - q, 0), and after all of them one more is drawn from p. A draw from
+// weights w is argmax_v w_v / e_v with e exponential: the race whose winner is v with probability w_v / sum
+// w.  It needs no sum, so no order of summation can change a token.
 //
 // Only the row that the sequence draws from is read: p, q and e once, which HBM bounds for many sequences
-// and the launches for few.  The vocabulary is split over workgroups; each finds the first
-// unaccepted draft by itself (a few scalars) and leaves one key for each of the two draws (the rest, and p alone for
-// the case that the rest is empty): the score's bits above the complement of the index, so that
-// the largest key is the best score at the lowest index.  The second kernel takes the largest.
+// and the launches for few.  The vocabulary is split over workgroups; each finds the first unaccepted draft
+// by itself (a few scalars) and leaves one key for each of the two draws (the rest, and p alone for the
+// case that the rest is empty): the score's bits above the complement of the index, so that the largest key
+// is the best score at the lowest index.  The second kernel takes the largest.
 #pragma once
 
 #include "serve_common.h"
@@ -66,9 +66,9 @@ struct Best {
   float score = 0.0f;
   int at = -1;
 
-  // Whether w / e may pass the score: at most one entry in a few hundred does, so the division is only taken
-  // for those.  fl(w / e) > score needs w > score * e * (1 - 2^-24); the product's own rounding is 2^-24 (not where it is
-  // subnormal: the test is passed there), and the factor below leaves room for both.
+  // Whether w / e may pass the score: at most one entry in a few hundred does, so the division is only
+  // taken for those.  fl(w / e) > score needs w > score * e * (1 - 2^-24); the product's own rounding is
+  // 2^-24 (not where it is subnormal: the test is passed there), and the factor below leaves room for both.
   __device__ __forceinline__ bool may(float w, float e) const {
     const float t = score * e;
     return w > 0.0f && e >= 0.0f && !(w < t * 0.999999f && t > 1e-30f);

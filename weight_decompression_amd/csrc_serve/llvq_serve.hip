@@ -101,7 +101,8 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
   const bool vec = wide(k, k_token, k_head, size) && wide(v, v_token, v_head, size);
   const KvRows r = {k, v, k_token, k_head, v_token, v_head};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  // Four tokens a wave once that fills the chip: four loads in flight, and neighbours of a page written together
+  // Four tokens a wave once that fills the chip: four loads in flight, and neighbours of a page written
+  // together
   const bool four = (int64_t)c.tokens * c.heads * c.dim >= 1 << 22;
 #define LLVQ_KV_KIND(KIND) four ? launch_kv<KIND, WRITE, 4>(c, r, f32, vec, err, s) : launch_kv<KIND, WRITE, 1>(c, r, f32, vec, err, s)
   switch (d->kind) {
@@ -130,29 +131,33 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   if (rows * seqs > (1ll << 33)) return LLVQ_EINVAL;
   cut->waves = 4;
   cut->cols = rows > 64 ? 0 : rows <= 16 || !few_pairs(d->kind, dim, terms) ? 1 : 2;
-  // Eight waves stage a tile for 256 rows: 539 us instead of 594 at chunks of 2 x 2048 rows of 128-wide heads over 8192
-  // keys, 220 instead of 391 at 256-wide heads.  64-wide heads run better with three workgroups of four a compute unit,
-  // and where 256 rows a workgroup leave compute units idle, 128 do better (369 rows of 32 heads: 17 us instead of 19)
+  // Eight waves stage a tile for 256 rows: 478 us instead of 530 at chunks of 2 x 2048 of 32 128-wide heads
+  // over 8192 keys, 196 instead of 218 at 256-wide heads.  64-wide heads run better with three workgroups
+  // of four a compute unit (87 us, 113 with eight waves), and where 256 rows a workgroup leave compute
+  // units idle, 128 do better (369 rows of 32 heads: 17 us instead of 19)
   if (!cut->cols && !f32 && dim > 64 && rows > 128 && (rows + 255) / 256 * seqs * parts >= 256) cut->waves = 8;
   const int64_t per = cut->cols ? 16 * cut->cols : 32 * cut->waves;
   const int64_t blocks = (rows + per - 1) / per, base = blocks * seqs;
   if (base > (1ll << 29)) return LLVQ_EINVAL;
   int64_t s;
   if (cut->cols) {
-    // One round of resident workgroups where a sequence is cut into many parts (three sequences of 131000 keys in e2m1:
-    // 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all lengths (64 of up to 16384 in
-    // e4m3: 268 us at 2048, 295 at 1024), no split where they fill the chip twice (57 x 32 of up to 176 keys: 54 us, 72 split)
+    // One round of resident workgroups where a sequence is cut into many parts (three sequences of 131000
+    // keys in e2m1: 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all
+    // lengths (64 of up to 16384 in e4m3: 268 us at 2048, 295 at 1024), no split where they fill the chip
+    // twice (57 x 32 of up to 176 keys: 54 us, 72 split)
     const int64_t resident = 256 * few_waves(d->kind, dim, terms, cut->cols);
     s = base >= 2 * resident ? 1 : base > resident / 2 ? (2048 + base - 1) / base : resident / base;
     const int64_t most = ((int64_t)max_len + 127) / 128;
     if (s > most) s = most;
-    // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to three pieces (at
-    // 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups 7.4 us and the join 4.6 after it)
+    // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to
+    // three pieces (at 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups
+    // 7.4 us and the join 4.6 after it)
     if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= 768) cut->waves = 8, s = 1;
   } else {
-    // A split shortens a workgroup's way (about 1 us a tile of 64 keys; f32 and wide heads more) and costs its sums' way
-    // out and back (8 bytes a channel of every row at 5 TB/s): the least of tiles / s + cost * s, up to two rounds of
-    // workgroups (3 x 295 rows of 12 heads in a window of 1932 keys: 37 us at 6 splits, 56 at 12)
+    // A split shortens a workgroup's way (about 1 us a tile of 64 keys; f32 and wide heads more) and costs
+    // its sums' way out and back (8 bytes a channel of every row at 5 TB/s): the least of tiles / s + cost
+    // * s, up to two rounds of workgroups (3 x 295 rows of 12 heads in a window of 1932 keys: 37 us at 6
+    // splits, 56 at 12)
     const int64_t slots = 256 * (cut->waves == 8 ? 1 : dim == 64 && !f32 ? 3 : 2);
     const double tiles = max_len / 64.0 * (f32 ? 2.5 : 1.0) * parts, cost = (double)rows * seqs * d->head_dim * 8.0 / 5e6;
     s = (2 * slots + base * parts / 2) / (base * parts);
@@ -238,8 +243,8 @@ int launch_join_dim(const AttnArgs& a, hipStream_t s) {
   }
 }
 
-// Workgroups that share out a row; 1: one of 1024 threads does it all in one launch (one compute unit alone draws no more
-// than 40 GB/s: a row of 32000 takes it 14 us, 16 workgroups 5 us and the second launch 2).
+// Workgroups that share out a row; 1: one of 1024 threads does it all in one launch (one compute unit alone
+// draws no more than 40 GB/s: a row of 32000 takes it 14 us, 16 workgroups 5 us and the second launch 2).
 int draft_parts(int32_t batch, int32_t vocab) {
   if (vocab <= 8192 || batch >= 512) return 1;
   // about 1024 workgroups in all, each of at least 2048 entries
