@@ -37,7 +37,7 @@ struct AttnArgs {
   float* stats;  // [splits][tokens * heads][2], running maximum (in log2 units) and sum
   int64_t q_token, q_head, out_token, out_head;
   Divider share;  // query heads per key head
-  int32_t row_blocks, splits, window, causal, q_vec;
+  int32_t row_blocks, splits, units, window, causal, q_vec;  // units: row blocks of all sequences and splits
   float scale_log2;
   int32_t* err;
 };
@@ -277,23 +277,30 @@ constexpr int few_waves(int kind, int dp, int nt, int ct) {
 // Two column tiles share a staged piece where two waves a SIMD still fit.
 constexpr bool few_pairs(int kind, int dp, int nt) { return few_waves(kind, dp, nt, 2) >= 2; }
 
-template <int KIND, int DP, int NT, int CT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
+// TEAM: the waves that share out the keys of a row block.  1: a workgroup's four waves have a row block
+// each, and no barrier; for so many short sequences that they fill the chip this way, where a team's start
+// and its joining would take longer than the keys (57 sequences of up to 176 tokens, 32 key heads of 192
+// channels in e2m1, 5 new tokens: 42 us, 54 with teams of four; 64 of up to 1000, 32 heads of 128 in e4m3:
+// 77 us, 4.6 TB/s).
+template <int KIND, int DP, int NT, int CT, int TEAM>
+__global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
+  constexpr int kWaves = TEAM == 1 ? 4 : TEAM;
   constexpr int kRaw = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
   constexpr int kLoads = 32 * kRaw / kWave;        // chunks a lane loads of a piece
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
   constexpr int kSteps = DP / 32, kOut = DP / 16;
   const Cache& c = a.c;
   using Lds = FewLds<DP>;
-  __shared__ __align__(16) uint8_t lds[WAVES * Lds::kWaveBytes];
-  __shared__ float wave_m[WAVES][16], wave_l[WAVES][16];
+  __shared__ __align__(16) uint8_t lds[kWaves * Lds::kWaveBytes];
+  __shared__ float wave_m[TEAM][16], wave_l[TEAM][16];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_id = __builtin_amdgcn_readfirstlane(tid >> 6), wave = TEAM == 1 ? 0 : wave_id;
   const int g = lane >> 4, col = lane & 15;
-  uint8_t* mine = lds + wave * Lds::kWaveBytes;
+  uint8_t* mine = lds + wave_id * Lds::kWaveBytes;
 
-  int id = blockIdx.x;
+  int id = TEAM == 1 ? (int)blockIdx.x * 4 + wave_id : (int)blockIdx.x;
+  if (id >= a.units) return;
   const int head = id % c.heads;
   id /= c.heads;
   const int split = id % a.splits;
@@ -302,10 +309,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   const int b = id / a.row_blocks;
   const Seq s = sequence(c, b);
   const int share = (int)a.share.by, rows = s.n * share;
-  if (a.err && tid == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * 16 * CT)) atomicAdd(a.err, 1);
+  if (a.err && lane == 0 && wave == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * 16 * CT)) atomicAdd(a.err, 1);
   const int row0 = rb * 16 * CT;
   if (row0 >= rows) return;
-  const Span w = span_of(a, s, row0, 16 * CT, 32 * WAVES, split);
+  const Span w = span_of(a, s, row0, 16 * CT, 32 * TEAM, split);
 
   const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
@@ -315,7 +322,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   // the page number of this lane's key of a piece (lanes 32..63 as 0..31)
   auto is_key = [&](int tile, int j) { return tile < w.tile_hi && j >= w.first_key && j < w.last_key; };
   auto page_of = [&](int tile) -> int32_t {
-    const int j = (tile * WAVES + wave) * 32 + (lane & 31);
+    const int j = (tile * TEAM + wave) * 32 + (lane & 31);
     return is_key(tile, j) ? table[divide((uint32_t)j, c.page)] : 0;
   };
   // A lane's key of a piece, lane % 32, tells where the piece's rows lie, and with lane / 32 whose scales it
@@ -329,7 +336,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   u32x4 raw_k[kLoads], raw_v[kLoads];
   uint32_t scales[kWords], next_scales[kWords], gone = 0, next_gone = 0;  // of the piece that is staged, and of the next
   auto locate = [&](int tile, int32_t ids) {
-    const uint32_t j = (uint32_t)((tile * WAVES + wave) * 32 + (lane & 31));
+    const uint32_t j = (uint32_t)((tile * TEAM + wave) * 32 + (lane & 31));
     const bool key = is_key(tile, (int)j), ok = key && ids >= 0 && ids < c.pages;
     lost |= key && !ok;
     next_gone = (uint32_t)__ballot(!ok);
@@ -407,7 +414,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   }
 
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
-    const int key_base = (tile * WAVES + wave) * 32;
+    const int key_base = (tile * TEAM + wave) * 32;
     const bool more = tile + 1 < w.tile_hi;
     // the keys
     gone = next_gone;
@@ -542,6 +549,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 
+  if constexpr (TEAM == 1) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const float l = quad_sum((l4[ct][0] + l4[ct][1]) + (l4[ct][2] + l4[ct][3]));
+      if (!live[ct]) continue;
+      const int64_t row = (int64_t)(s.first + t[ct]) * c.heads * share + qhead[ct];
+      const int64_t out_at = (int64_t)(s.first + t[ct]) * a.out_token + (int64_t)qhead[ct] * a.out_head;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible key: the row is zero
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) store_row4<NT>(a, row, out_at, 0, d * 16 + g * 4, acc[ct][d], inv);
+    }
+    return;
+  }
   // the waves' parts are joined through LDS under their common maximum and added in the waves' order
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
@@ -551,7 +571,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_m[i][col]);
+    for (int i = 0; i < TEAM; ++i) top = fmaxf(top, wave_m[i][col]);
     const float f = m[ct] == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(m[ct] - top);
     if (g == 0) wave_l[wave][col] = l * f;
     float* sums = reinterpret_cast<float*>(lds);  // [wave][16 columns][DP], quads of channels swizzled by the column
@@ -561,7 +581,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
     __syncthreads();
     float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i) total += wave_l[i][col];
+    for (int i = 0; i < TEAM; ++i) total += wave_l[i][col];
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // no visible key: the row is zero
     if (live[ct]) {
       const int64_t row = (int64_t)(s.first + t[ct]) * c.heads * share + qhead[ct];
@@ -572,10 +592,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : few_waves(KIND, DP, NT
         a.stats[(split * all + row) * 2 + 1] = total;
       }
       if (a.splits == 1 || w.tile_lo < w.tile_hi) {
-        for (int d = wave; d < kOut; d += WAVES) {  // the waves share out the channels
+        for (int d = wave; d < kOut; d += TEAM) {  // the waves share out the channels
           f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int i = 0; i < WAVES; ++i) x += *reinterpret_cast<const f32x4*>(sums + (i * 16 + col) * DP + (((d * 4 + g) ^ (col & 7)) << 2));
+          for (int i = 0; i < TEAM; ++i) x += *reinterpret_cast<const f32x4*>(sums + (i * 16 + col) * DP + (((d * 4 + g) ^ (col & 7)) << 2));
           store_row4<NT>(a, row, out_at, split, d * 16 + g * 4, x, inv);
         }
       }

@@ -113,8 +113,8 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
 #undef LLVQ_KV_KIND
 }
 
-// How a call is cut up: columns of 16 that a workgroup of the kernel for few rows holds (0: the kernel for many
-// rows), waves of a workgroup, row blocks and splits of the keys.
+// How a call is cut up: columns of 16 that a team of the kernel for few rows holds (0: the kernel for many rows), waves
+// of a team (or of a workgroup of the other kernel), row blocks and splits of the keys.
 struct Cut {
   int cols, waves, row_blocks, splits;
 };
@@ -149,6 +149,8 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
     s = base >= 2 * resident ? 1 : base > resident / 2 ? (2048 + base - 1) / base : resident / base;
     const int64_t most = ((int64_t)max_len + 127) / 128;
     if (s > most) s = most;
+    // Short sequences that fill the chip a wave each
+    if (base >= 2 * resident && max_len <= 1024) cut->waves = 1;
     // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to
     // three pieces (at 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups
     // 7.4 us and the join 4.6 after it)
@@ -192,9 +194,9 @@ int launch_many(const AttnArgs& a, unsigned grid, hipStream_t s) {
   hipLaunchKernelGGL((k_attn_many<KIND, DP, NT, WAVES>), dim3(grid * Sh::kParts), dim3(Sh::kThreads), 0, s, a);
   return launch_status();
 }
-template <int KIND, int DP, int NT, int CT, int WAVES>
+template <int KIND, int DP, int NT, int CT, int TEAM>
 int launch_few(const AttnArgs& a, unsigned grid, hipStream_t s) {
-  hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, CT, WAVES>), dim3(grid), dim3(64 * WAVES), 0, s, a);
+  hipLaunchKernelGGL((k_attn_few<KIND, DP, NT, CT, TEAM>), dim3(TEAM == 1 ? (grid + 3) / 4 : grid), dim3(TEAM == 8 ? 512 : 256), 0, s, a);
   return launch_status();
 }
 template <int KIND, int DP, int NT>
@@ -204,8 +206,10 @@ int launch_attn(const AttnArgs& a, const Cut& cut, unsigned grid, hipStream_t s)
   }
   if (cut.cols == 0) return launch_many<KIND, DP, NT, 4>(a, grid, s);
   if constexpr (few_pairs(KIND, DP, NT)) {
-    if (cut.cols == 2) return launch_few<KIND, DP, NT, 2, 4>(a, grid, s);
+    if (cut.cols == 2)
+      return cut.waves == 1 ? launch_few<KIND, DP, NT, 2, 1>(a, grid, s) : launch_few<KIND, DP, NT, 2, 4>(a, grid, s);
   }
+  if (cut.waves == 1) return launch_few<KIND, DP, NT, 1, 1>(a, grid, s);
   if constexpr (DP <= 128) {
     if (cut.waves == 8) return launch_few<KIND, DP, NT, 1, 8>(a, grid, s);
   }
@@ -341,6 +345,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const unsigned grid = (unsigned)((int64_t)c.batch * cut.row_blocks * cut.splits * c.heads);
+  a.units = (int32_t)grid;
   switch (d->kind) {
     case LLVQ_KV_BF16: st = launch_attn_dp<LLVQ_KV_BF16>(a, f32, cut, grid, s); break;
     case LLVQ_KV_FP8: st = launch_attn_dp<LLVQ_KV_FP8>(a, f32, cut, grid, s); break;
