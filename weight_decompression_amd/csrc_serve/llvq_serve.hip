@@ -143,18 +143,22 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   if (cut->cols) {
     // One round of resident workgroups where a sequence is cut into many parts (three sequences of 131000
     // keys in e2m1: 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all
-    // lengths (64 of up to 16384 in e4m3: 268 us at 2048, 295 at 1024), no split where they fill the chip
-    // twice (57 x 32 of up to 176 keys: 54 us, 72 split)
+    // lengths (64 of up to 16384 in e4m3: 268 us at 2048, 324 unsplit), no split where they fill half the
+    // chip and are short (64 x 8 in e4m3 of up to 1000 keys: 25 us, 31 in two and 34 in four; of up to 4096:
+    // 82 and 86) or fill it twice (57 x 32 of up to 176 keys: 54 us, 72 split)
     const int64_t resident = 256 * few_waves(d->kind, dim, terms, cut->cols);
-    s = base >= 2 * resident ? 1 : base > resident / 2 ? (2048 + base - 1) / base : resident / base;
+    s = base <= resident / 2                      ? resident / base
+        : base >= 2 * resident || max_len <= 4096 ? 1
+                                                  : (2048 + base - 1) / base;
     const int64_t most = ((int64_t)max_len + 127) / 128;
     if (s > most) s = most;
-    // Short sequences that fill the chip a wave each
-    if (base >= 2 * resident && max_len <= 1024) cut->waves = 1;
-    // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to
-    // three pieces (at 777 keys of 32 heads in bf16, four pieces, it takes 13.8 us; split over 7 workgroups
-    // 7.4 us and the join 4.6 after it)
-    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= 768) cut->waves = 8, s = 1;
+    // Short sequences that fill the chip a wave each (64 x 32 in e4m3 of up to 500 keys: 39 us, 42 with four
+    // waves; of up to 1000 78 and 73)
+    if (base >= 2 * resident && max_len <= 768) cut->waves = 1;
+    // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to four
+    // pieces (of up to 1000 keys 16 x 8 in e4m3 13.8 us, 16.1 split; 8 x 8 in bf16 14.8 and 14.9; of 1500 17.4
+    // and 14.7)
+    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= 1024) cut->waves = 8, s = 1;
   } else {
     // A split shortens a workgroup's way (about 1 us a tile of 64 keys; f32 and wide heads more) and costs
     // its sums' way out and back (8 bytes a channel of every row at 5 TB/s): the least of tiles / s + cost
