@@ -156,9 +156,9 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
     // waves; of up to 1000 78 and 73)
     if (base >= 2 * resident && max_len <= 768) cut->waves = 1;
     // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to four
-    // pieces (of up to 1000 keys 16 x 8 in e4m3 13.8 us, 16.1 split; 8 x 8 in bf16 14.8 and 14.9; of 1500 17.4
-    // and 14.7)
-    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= 1024) cut->waves = 8, s = 1;
+    // pieces (16 x 8 in e4m3 of up to 1000 keys 13.8 us, 16.1 split; of 1500 17.4 and 14.7), three in bf16,
+    // whose pieces take longer to come (32 heads of 777 keys: 13.8 us, 7.4 split and 4.6 for the join)
+    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= (d->kind == LLVQ_KV_BF16 ? 768 : 1024)) cut->waves = 8, s = 1;
   } else {
     // A split shortens a workgroup's way (about 1 us a tile of 64 keys; f32 and wide heads more) and costs
     // its sums' way out and back (8 bytes a channel of every row at 5 TB/s): the least of tiles / s + cost
