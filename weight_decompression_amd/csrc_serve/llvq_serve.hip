@@ -145,7 +145,7 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
     // keys in e2m1: 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all
     // lengths (64 of up to 16384 in e4m3: 268 us at 2048, 324 unsplit), no split where they fill half the
     // chip and are short (64 x 8 in e4m3 of up to 1000 keys: 25 us, 31 in two and 34 in four; of up to 2000
-    // 39 and 46; of up to 4096 with f32 queries 86, split 83) or fill it twice (57 x 32 of up to 176 keys:
+    // 39 and 46; past that splitting evens out lengths: of up to 4096 with f32 queries 86, split 85) or fill it twice (57 x 32 of up to 176 keys:
     // 54 us, 72 split)
     const int64_t resident = 256 * few_waves(d->kind, dim, terms, cut->cols);
     s = base <= resident / 2                      ? resident / base
