@@ -468,10 +468,10 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, score[ct][i / 4][i & 3]);
       top = quad_max(top) * a.scale_log2;
-      if (__any(top > m[ct] + kRescaleStep)) {
-        const float next = fmaxf(m[ct], top);
-        const float f = m[ct] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[ct] - next);
-        m[ct] = next;
+      const bool up = top > m[ct] + kRescaleStep;
+      if (__any(up)) {  // (the others' sums stay as they are: a row's roundings are its own)
+        const float f = !up ? 1.0f : m[ct] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[ct] - top);
+        m[ct] = up ? top : m[ct];
 #pragma unroll
         for (int i = 0; i < 4; ++i) l4[ct][i] *= f;
 #pragma unroll
@@ -918,11 +918,12 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[u][i]);
     top = half_max(top) * a.scale_log2;
     // The maximum is raised only when it is passed by 2^8: p stays below 2^8 and its rounding is
-    // relative, so the result is the same, and most tiles skip the rescaling of O.
-    if (__any(top > m + kRescaleStep)) {
-      const float raised = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - raised);
-      m = raised;
+    // relative, so the result is the same, and most tiles skip the rescaling of O.  Rows that are not past it
+    // keep their sums as they are: a row's roundings do not depend on keys that only its neighbours see.
+    const bool up = top > m + kRescaleStep;
+    if (__any(up)) {
+      const float f = !up ? 1.0f : m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+      m = up ? top : m;
 #pragma unroll
       for (int i = 0; i < 4; ++i) l4[i] *= f;
 #pragma unroll
