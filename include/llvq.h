@@ -339,7 +339,8 @@ int llvq_pack_fields(const llvq_desc* d, const uint64_t* fields, void* packed, v
  * even channel in the low half of a byte (LLVQ_KV_FP4).  e is the smallest integer in [-100, 119]
  * (FP8) or [-100, 125] (FP4) with max|x| <= top * 2^e, top = 448 or 6; x / 2^e is rounded to the nearest code,
  * ties to even (past the limits of e it saturates).  A group with a value that is not finite
- * has the scale byte 255 and stands for NaN.  Every other value is exact in bf16. */
+ * has the scale byte 255 and stands for NaN.  Every other value is exact in bf16.  Bytes that no write leaves have
+ * a meaning too: a scale byte past e's limit stands for NaN, and so do the e4m3 codes 0x7f and 0xff. */
 enum { LLVQ_KV_BF16 = 0, LLVQ_KV_FP8 = 1, LLVQ_KV_FP4 = 2 };
 
 #define LLVQ_MAX_HEAD_DIM 256

@@ -52,7 +52,7 @@ def values(codes, scales, kind):
     top = 128 if kind == FP8 else 8
     grid = np.concatenate((GRID[kind], [np.nan])) if kind == FP8 else GRID[kind]
     v = grid[codes % top] * np.where(codes >= top, -1.0, 1.0)
-    f = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    f = np.where(scales > E_HIGH[kind] + 127, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
     return (v.reshape(v.shape[:-1] + (-1, GROUP)) * f[..., None]).reshape(v.shape)
 
 

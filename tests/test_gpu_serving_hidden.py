@@ -1,4 +1,5 @@
-"""What a row does not see has no effect on it, to the bit: keys whose scores pass all others'."""
+"""What a row does not see has no effect on it, whatever bytes lie there: bytes that no write leaves (codes and
+scales that stand for values that are not finite), and keys whose scores pass all others'."""
 
 import numpy as np
 import pytest
@@ -23,6 +24,57 @@ class Hidden:
         at = old + self.first
         self.place = int(su.table[0][at // 16]), at % 16
         self.plan = su.plan(starts=[0, 1], lens=[at + 1])       # of that token alone
+
+    def poke(self, head, is_v, codes, scales):
+        """Bytes of the token's key or value: {offset: byte} of its codes and of its scales."""
+        lay = self.su.lay
+        for at, these in ((lay.codes, codes), (lay.scales, scales)):
+            for offset, byte in these.items():
+                self.su.pool[at(self.place[0], head, self.place[1], is_v) + offset] = byte
+
+    def read(self):
+        out = torch.empty(2, 1, 2, self.su.dim, device="cuda")
+        wd.kv_read(self.su.desc, self.su.pool, out[0], out[1], *self.plan)
+        return out[1, 0]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("max_len", [1, 100000])
+@pytest.mark.parametrize("new", [6, 140])
+@pytest.mark.parametrize("dim", [64, 128, 160, 256])
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+def test_values_of_bytes_that_no_write_leaves(kind, dim, new, max_len, dtype):
+    h = Hidden(kind, dim, new, 50, seed=dim + new)
+    su, first = h.su, h.first
+    clean = run_attn(su, h.q, dtype, max_len=max_len)
+    was = su.pool.clone()
+    ch = dim - 27                                    # a channel of the last group, in the second half of wide heads
+    group = ch // 32
+    last = 246 if kind == "fp8" else 252             # the last scale byte that stands for a power of two
+    cases = [({}, {group: byte}) for byte in (255, 254, last + 1)]
+    if kind == "fp8":
+        cases += [({ch: 0x7F}, {}), ({ch: 0xFF}, {})]
+    for codes, scales in cases:
+        su.pool.copy_(was)
+        h.poke(1, 1, codes, scales)
+        nan = torch.zeros(2, dim, dtype=torch.bool, device="cuda")
+        nan[1, ch if codes else slice(32 * group, 32 * group + 32)] = True
+        assert torch.equal(torch.isnan(h.read()), nan)
+        out = run_attn(su, h.q, dtype, max_len=max_len)
+        assert torch.equal(out[:first], clean[:first])
+        # the rows that see it: NaN there, and the rest as it was
+        rows = nan.repeat_interleave(2, 0).expand(new - first, 4, dim)
+        assert torch.equal(torch.isnan(out[first:]), rows)
+        assert torch.equal(out[first:][~rows], clean[first:][~rows])
+    # any bytes at all, keys among them
+    for seed in range(3):
+        su.pool.copy_(was)
+        noise = np.random.RandomState(seed).randint(0, 256, (2, 2, 2, 512))
+        for head in range(2):
+            for is_v in range(2):
+                h.poke(head, is_v, dict(enumerate(noise[head, is_v, 0, :su.lay.row].tolist())),
+                       dict(enumerate(noise[head, is_v, 1, :su.lay.groups].tolist())))
+        assert torch.equal(run_attn(su, h.q, dtype, max_len=max_len)[:first], clean[:first])
 
 
 @pytest.mark.parametrize("dtype", BOTH)

@@ -93,20 +93,35 @@ __device__ __forceinline__ void split_terms(const float* x, bf16x8* o) {
   }
 }
 
-// bf16 elements of four dwords that are not finite, set to zero; whether there was any.  An exponent
-// of all ones is the only one that carries into the sign's place when 1 is added to it.
-__device__ __forceinline__ bool drop_nonfinite(u32x4* w) {
+// 16 bytes of value codes that are not finite by themselves: bf16 infinities and NaN, of which an exponent of all
+// ones is the only one that carries into the sign's place when 1 is added to it, and the e4m3 NaN, 0x7f and 0xff,
+// of which the same holds for all seven bits.  e2m1 has none.
+constexpr uint32_t odd_bits(int kind) { return kind == LLVQ_KV_BF16 ? 0x80008000u : kind == LLVQ_KV_FP8 ? 0x80808080u : 0; }
+template <int KIND>
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) {  // odd_bits at those
+  return KIND == LLVQ_KV_BF16 ? (w & 0x7f807f80u) + 0x00800080u : (w & 0x7f7f7f7fu) + 0x01010101u;
+}
+
+// Those of a wave's chunks set to zero; whether there was any (the same in every lane).  Where there is none, in
+// all but damaged caches, this takes three operations a dword and one branch.
+template <int KIND, int N>
+__device__ __forceinline__ bool drop_odd(u32x4* raw) {
+  if constexpr (KIND == LLVQ_KV_FP4) return false;
   uint32_t any = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) any |= ((*w)[i] & 0x7f807f80u) + 0x00800080u;
-  if ((any & 0x80008000u) == 0) return false;
+  for (int n = 0; n < N; ++n)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t u = (*w)[i];
-    if ((u & 0x7f800000u) == 0x7f800000u) u &= 0x0000ffffu;
-    if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
-    (*w)[i] = u;
-  }
+    for (int i = 0; i < 4; ++i) any |= odd_codes<KIND>(raw[n][i]);
+  if (!__any((any & odd_bits(KIND)) != 0)) return false;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w = raw[n][i];
+      asm volatile("" : "+v"(w));  // (so that what was worked out above is not kept for here)
+      constexpr int kBits = KIND == LLVQ_KV_BF16 ? 16 : 8;
+      raw[n][i] = w & ~(((odd_codes<KIND>(w) & odd_bits(KIND)) >> (kBits - 1)) * ((1u << kBits) - 1));
+    }
   return true;
 }
 
@@ -134,8 +149,12 @@ __device__ __forceinline__ f32x4 nonfinite4(const Cache& c, const uint8_t* blk, 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if ((v[i] & 0x7f80u) == 0x7f80u) x[i] = bf16_f32(v[i]);
-  } else if (blk[c.vs_off + slot * c.groups + ch / kGroup] == 255) {
-    x = f32x4{NAN, NAN, NAN, NAN};
+  } else {
+    const bool all = blk[c.vs_off + slot * c.groups + ch / kGroup] > last_scale(KIND);
+    const uint32_t codes = KIND == LLVQ_KV_FP8 ? *reinterpret_cast<const uint32_t*>(blk + c.v_off + slot * c.row + ch) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (all || (codes >> (8 * i) & 0x7fu) == 0x7fu) x[i] = NAN;
   }
   return x;
 }
@@ -161,6 +180,16 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int row
   w.tile_lo = tile0 + min(split * per, tiles);
   w.tile_hi = min(w.tile_lo + per, tile0 + tiles);
   return w;
+}
+
+// The block that holds key j of a workgroup's, and its slot there; null if it has no such key, or no page holds it.
+__device__ __forceinline__ const uint8_t* block_of_key(const Cache& c, const Span& w, const int32_t* table, int head, int j,
+                                                       int* slot) {
+  if (j < w.first_key || j >= w.last_key) return nullptr;
+  const uint32_t page = divide((uint32_t)j, c.page);
+  const int32_t id = table[page];
+  *slot = j - (int)(page * c.page.by);
+  return id < 0 || id >= c.pages ? nullptr : c.pool + ((int64_t)id * c.heads + head) * c.block;
 }
 
 // The keys that token t sees: [lo, lo + seen).
@@ -222,10 +251,23 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* sp, int groups, in
   }
   return word;
 }
-// Whether one of four scale bytes is 255, the only one whose complement is zero.
-__device__ __forceinline__ bool has_255(uint32_t word) {
-  const uint32_t v = ~word;
-  return ((v - 0x01010101u) & word & 0x80808080u) != 0;
+// N words of scale bytes: those that stand for NaN become 255; whether there was one.  A write leaves none past the
+// type's last but 255, and few of that; whether a byte is past it is whether its complement is below 255 - last.
+template <int KIND, int N>
+__device__ __forceinline__ bool nan_scales(uint32_t* words) {
+  if constexpr (KIND == LLVQ_KV_BF16) return false;
+  constexpr uint32_t kBelow = (uint32_t)(255 - last_scale(KIND)) * 0x01010101u;
+  uint32_t any = 0;
+#pragma unroll
+  for (int n = 0; n < N; ++n) any |= (~words[n] - kBelow) & words[n] & 0x80808080u;
+  if (any != 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((words[n] >> (8 * e) & 255u) > (uint32_t)last_scale(KIND)) words[n] |= 255u << (8 * e);
+  }
+  return any != 0;
 }
 
 // Few rows: up to 64 rows of a (sequence, key head), in CT tiles of 16 columns.
@@ -413,6 +455,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
     for (int d = 0; d < kOut; ++d) acc[ct][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
+  int odd_lo = 0x7fffffff, odd_hi = -1;  // the first and the last tile with a value that is not finite
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
     const int key_base = (tile * TEAM + wave) * 32;
     const bool more = tile + 1 < w.tile_hi;
@@ -420,6 +463,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
     gone = next_gone;
 #pragma unroll
     for (int n = 0; n < kWords; ++n) scales[n] = next_scales[n];
+    const uint64_t spoilt = __ballot(nan_scales<KIND, kWords>(scales));  // keys, and from bit 32 on values
     if (gone != 0 || narrow) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
@@ -487,30 +531,18 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
 #pragma unroll
       for (int n = 0; n < NT; ++n) p[n][ct] = terms[n];
     }
-    // the values, in the keys' place.  Those that are not finite would spoil rows that do not see them
-    // (0 * NaN): they are left out here and added to the rows that do see them after the products
-    uint32_t bad = 0;  // keys that have one
-    if constexpr (KIND == LLVQ_KV_BF16) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        if (drop_nonfinite(&raw_v[i])) bad |= 1u << ((i * kWave + lane) / kRaw);
-      if (__any(bad != 0)) {
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) bad |= (uint32_t)__shfl_xor((int)bad, d);
-      }
-      bad = (uint32_t)__builtin_amdgcn_readfirstlane((int)bad);
-    } else {
-      bool spoilt = false;
-#pragma unroll
-      for (int n = 0; n < kWords; ++n) spoilt |= has_255(scales[n]);
-      bad = (uint32_t)(__ballot(spoilt) >> 32);
+    // the values, in the keys' place.  Those that are not finite would spoil rows that do not see them (0 * NaN):
+    // they are left out here and added to the rows that do see them at the end
+    if (drop_odd<KIND, kLoads>(raw_v) || (spoilt >> 32) != 0) {
+      odd_lo = min(odd_lo, tile);
+      odd_hi = tile;
     }
     wave_order();
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int key = (i * kWave + lane) / kRaw;
       uint32_t sb = scale_of(key, 1);
-      if (KIND != LLVQ_KV_BF16 && bad != 0 && sb == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sb = 127;
+      if (KIND != LLVQ_KV_BF16 && (spoilt >> 32) != 0 && sb == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sb = 127;
       u32x4 o[kOf];
       expand<KIND>(raw_v[i], sb, o);
 #pragma unroll
@@ -532,12 +564,17 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n) acc[ct][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf.v, p[n][ct], acc[ct][d], 0, 0, 0);
     }
-    while (bad) {
-      const int key = __builtin_ctz(bad), j = key_base + key;
-      bad &= bad - 1;
-      const uint32_t page = divide((uint32_t)j, c.page);
-      const int slot = j - (int)(page * c.page.by);
-      const uint8_t* blk = c.pool + (int64_t)table[page] * page_bytes + head_off;
+  }
+  if (a.err && lost) atomicAdd(a.err, 1);
+  // what was left out: p is positive where a row sees the key, so the value itself is what the sum becomes.  The
+  // keys of all tiles from the first such one to the last are looked at again, one by one: a wave keeps two numbers
+  // for this through its loop, and only a damaged cache takes it
+  for (int tile = odd_lo; tile <= odd_hi; ++tile)
+    for (int i = 0; i < 32; ++i) {
+      const int j = (tile * TEAM + wave) * 32 + i;
+      int slot;
+      const uint8_t* blk = block_of_key(c, w, table, head, j, &slot);
+      if (!blk) continue;
 #pragma unroll
       for (int d = 0; d < kOut; ++d) {
         const f32x4 x = nonfinite4<KIND>(c, blk, slot, d * 16 + 4 * g);
@@ -546,8 +583,6 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
           if ((uint32_t)(j - lo[ct]) < (uint32_t)seen[ct]) acc[ct][d] += x;
       }
     }
-  }
-  if (a.err && lost) atomicAdd(a.err, 1);
 
   if constexpr (TEAM == 1) {
 #pragma unroll
@@ -673,11 +708,10 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   using VChunks = Chunks<KIND, Sh::kOutDim, kKeys, Sh::kThreads>;
   const Cache& c = a.c;
   __shared__ __align__(16) uint8_t lds[2 * Sh::kBuffer];
-  __shared__ uint32_t bad_keys[3][kSub];
+  __shared__ int odd_tiles[2];  // the first and the last tile with a value that is not finite
   using Where = Place<KIND, DP>;
   __shared__ Where places[2][kKeys];
-  // of a tile: keys that are not there, and keys with a value that is not finite (in the quantised kinds,
-  // where the scales tell)
+  // of a tile: keys that are not there, and keys with a group of values whose scale says that they are not finite
   __shared__ uint64_t missing[2], spoilt[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -734,7 +768,6 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   u32x4 raw_k[KChunks::kPer], raw_v[VChunks::kPer];
   uint32_t sc_k[KChunks::kPer], sc_v[VChunks::kPer];
   uint64_t gone = 0, nonfinite = 0;  // of the loaded tile
-  uint64_t spoilt_now = 0, spoilt_next = 0;  // of the tile that is multiplied, and of the staged one after it
   bool lost = false;
   // Where a tile's keys lie and how they are scaled is worked out once a key, by the wave whose turn it is: the
   // page numbers are loaded five rounds ahead, the scales four, both written to LDS three and the codes loaded
@@ -774,9 +807,8 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   };
   auto write_places = [&](int tile) {
     if (wave != (tile & (WAVES - 1))) return;
-    bool bad = false;
-#pragma unroll
-    for (int n = 0; n < Where::kWords; ++n) bad |= has_255(found.scales[1][n]);
+    nan_scales<KIND, Where::kWords>(found.scales[0]);
+    const bool bad = nan_scales<KIND, Where::kWords>(found.scales[1]);
     const uint64_t no = __ballot(!found_ok), spoils = __ballot(bad);
     if (lane < kKeys) places[tile & 1][lane] = found;
     if (lane == 0) {
@@ -804,7 +836,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       sc_v[i] = at->scales[1][Where::kWords == 1 ? 0 : v_word] >> v_shift & 255;
     }
   };
-  auto stage = [&](uint8_t* buffer, uint32_t* bad_bits) {
+  auto stage = [&](uint8_t* buffer, int tile) {
     if (gone != 0 || narrow) {
 #pragma unroll
       for (int i = 0; i < KChunks::kPer; ++i)
@@ -813,20 +845,16 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       for (int i = 0; i < VChunks::kPer; ++i)
         if ((gone >> (vc.key0 + i * VChunks::kStep) & 1) || !v_in) raw_v[i] = u32x4{0, 0, 0, 0}, sc_v[i] = 127;
     }
-    // values that are not finite would spoil rows that do not see them (0 * NaN): they are left out
-    // here and added to the rows that do see them after the tile's products
-    if constexpr (KIND == LLVQ_KV_BF16) {
-#pragma unroll
-      for (int i = 0; i < VChunks::kPer; ++i) {
-        const int key = vc.key0 + i * VChunks::kStep;
-        if (drop_nonfinite(&raw_v[i])) atomicOr(&bad_bits[key >> 5], 1u << (key & 31));
-      }
-    } else if (nonfinite != 0) {
+    // values that are not finite would spoil rows that do not see them (0 * NaN): they are left out here and
+    // added to the rows that do see them at the end
+    if (drop_odd<KIND, VChunks::kPer>(raw_v) || nonfinite != 0) {
+      if (lane == 0) atomicMin(&odd_tiles[0], tile), atomicMax(&odd_tiles[1], tile);
+    }
+    if (KIND != LLVQ_KV_BF16 && nonfinite != 0) {
 #pragma unroll
       for (int i = 0; i < VChunks::kPer; ++i)
         if (sc_v[i] == 255) raw_v[i] = u32x4{0, 0, 0, 0}, sc_v[i] = 127;
     }
-    spoilt_next = nonfinite;
     u32x4 o[kOf];
     if (kc.any) {
 #pragma unroll
@@ -849,7 +877,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     }
   };
 
-  if (tid < 3 * kSub) bad_keys[tid / kSub][tid % kSub] = 0;
+  if (tid < 2) odd_tiles[tid] = tid == 0 ? 0x7fffffff : -1;
   if (w.tile_lo < w.tile_hi) {
     // (a wave has one tile of WAVES at a time)
     for (int i = 0; i < 4; ++i) load_pages(w.tile_lo + i);
@@ -858,19 +886,16 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     write_places(w.tile_lo + 1);
     __syncthreads();
     fetch(w.tile_lo);
-    stage(lds, bad_keys[0]);
-    spoilt_now = spoilt_next;
+    stage(lds, w.tile_lo);
     fetch(w.tile_lo + 1);
     __syncthreads();
     write_places(w.tile_lo + 2);
     load_pages(w.tile_lo + 4);
   }
-  int third = 0;
   for (int tile = w.tile_lo; tile < w.tile_hi; ++tile) {
-    const int par = (tile - w.tile_lo) & 1, next = third == 2 ? 0 : third + 1, after = next == 2 ? 0 : next + 1;
+    const int par = (tile - w.tile_lo) & 1;
     const uint8_t* buffer = lds + par * Sh::kBuffer;
     __syncthreads();  // this tile is staged, and the other buffer has been read
-    if (tid < kSub) bad_keys[after][tid] = 0;
     const int key_base = tile * kKeys;
     // operands are read a few instructions ahead, in an order that is pinned: left to itself the compiler reads
     // each right before its use and waits for it
@@ -947,7 +972,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
     // (the sums are taken here and not, as the compiler would have it, at the end of the round)
     asm volatile("" : "+v"(l4[0]), "+v"(l4[1]), "+v"(l4[2]), "+v"(l4[3]));
     if (tile + 1 < w.tile_hi) {
-      stage(lds + (par ^ 1) * Sh::kBuffer, bad_keys[next]);
+      stage(lds + (par ^ 1) * Sh::kBuffer, tile + 1);
       fetch(tile + 2);
       write_places(tile + 3);
       load_scales(tile + 4);
@@ -967,28 +992,27 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-      uint32_t left = KIND == LLVQ_KV_BF16 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)bad_keys[third][u]) : (uint32_t)(spoilt_now >> (32 * u));
-      while (left) {
-        const int j = key_base + u * 32 + __builtin_ctz(left);
-        left &= left - 1;
-        const uint32_t page = divide((uint32_t)j, c.page);
-        const uint8_t* blk = c.pool + (int64_t)table[page] * page_bytes + head_off;
+  }
+  if (w.tile_lo < w.tile_hi) {  // what was left out, as in the kernel for few rows
+    __syncthreads();
+    const int odd_hi = __builtin_amdgcn_readfirstlane(odd_tiles[1]);
+    for (int tile = __builtin_amdgcn_readfirstlane(odd_tiles[0]); tile <= odd_hi; ++tile)
+      for (int i = 0; i < kKeys; ++i) {
+        const int j = tile * kKeys + i;
+        int slot;
+        const uint8_t* blk = block_of_key(c, w, table, head, j, &slot);
+        if (!blk) continue;
         const bool sees = (uint32_t)(j - lo) < (uint32_t)seen;
 #pragma unroll
         for (int d = 0; d < kOut; ++d)
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 x = nonfinite4<KIND>(c, blk, j - (int)(page * c.page.by), part_dim + d * 32 + i4 * 8 + half * 4);
+            const f32x4 x = nonfinite4<KIND>(c, blk, slot, part_dim + d * 32 + i4 * 8 + half * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (sees) acc[d][i4 * 4 + i] += x[i];
+            for (int n = 0; n < 4; ++n)
+              if (sees) acc[d][i4 * 4 + n] += x[n];
           }
       }
-    }
-    third = next;
-    spoilt_now = spoilt_next;
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 

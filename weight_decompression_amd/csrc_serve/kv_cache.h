@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void k_kv_write(Cache c, KvRows in, Divider ch
         const bool nonfinite = top >= 0x7f800000u;
         // e: the exponent of max|x| less the type's, one more where the mantissa passes the type's top
         // (448 = 1.75 * 2^8, 6 = 1.5 * 2^2); a zero or subnormal maximum falls to the lower limit
-        constexpr int kExp = KIND == LLVQ_KV_FP8 ? 8 : 2, kHigh = KIND == LLVQ_KV_FP8 ? 119 : 125;
+        constexpr int kExp = KIND == LLVQ_KV_FP8 ? 8 : 2, kHigh = last_scale(KIND) - 127;
         constexpr uint32_t kMant = KIND == LLVQ_KV_FP8 ? 0x600000u : 0x400000u;
         constexpr float kTop = KIND == LLVQ_KV_FP8 ? 448.0f : 6.0f;
         int e = (int)(top >> 23) - 127 - kExp + ((top & 0x7fffffu) > kMant ? 1 : 0);
@@ -193,8 +193,9 @@ __global__ __launch_bounds__(256) void k_kv_write(Cache c, KvRows in, Divider ch
 // 8 values from their codes and scale byte.
 template <int KIND>
 __device__ __forceinline__ void values8(const u32x4 codes, uint32_t scale_byte, float* x) {
-  // a byte of 255 is an infinite f32, which the conversions turn into NaN for every code
-  const float scale = __uint_as_float(scale_byte << 23);
+  // a byte of 255 (taken for every byte past the last) is an infinite f32, which the conversions turn into NaN for
+  // every code
+  const float scale = __uint_as_float((scale_byte > (uint32_t)last_scale(KIND) ? 255u : scale_byte) << 23);
   uint32_t u[4];
   if constexpr (KIND == LLVQ_KV_BF16) {
 #pragma unroll

@@ -27,6 +27,10 @@ __host__ __device__ constexpr int code_bytes(int kind, int dim) {
   return kind == LLVQ_KV_BF16 ? 2 * dim : kind == LLVQ_KV_FP8 ? dim : dim / 2;
 }
 
+// The last scale byte that stands for a power of two (e = 119 and 125: the largest codes, 448 and 6, times 2^e stay
+// below 2^128).  Those past it stand for NaN; a write leaves none of them but 255.
+__host__ __device__ constexpr int last_scale(int kind) { return kind == LLVQ_KV_FP8 ? 246 : 252; }
+
 // n / d for 0 <= n < 2^31 as (n * mul) >> shift: with s = ceil(log2 d) and mul =
 // ceil(2^(31+s) / d) < 2^32, mul * d exceeds 2^(31+s) by less than d <= 2^s, so the quotient
 // is exact.
