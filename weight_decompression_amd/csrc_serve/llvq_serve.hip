@@ -394,7 +394,7 @@ LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dt
   a.drafts = drafts;
   a.vocab = vocab;
   a.parts = draft_parts(batch, vocab);
-  a.per = (vocab + a.parts - 1) / a.parts;
+  a.per = (int32_t)(((int64_t)vocab + a.parts - 1) / a.parts);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dtype == LLVQ_X_F32 ? launch_draft<true>(a, s) : launch_draft<false>(a, s);
 }
