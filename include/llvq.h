@@ -409,7 +409,7 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  *            may be left unwritten: counted).
  *   max_len : at least 1; about the longest length: it decides only how the keys are split, not
  *            what is computed.
- *   scale  : > 0 and finite.   window : 0 (none) .. 2^30.
+ *   scale  : > 0, and scale * log2(e) finite in f32.   window : 0 (none) .. 2^30.
  *   workspace : at least llvq_attn_workspace_bytes(...) bytes for the same arguments, 16-byte aligned
  *            (may be NULL if that is 0), contents not kept; workspace_bytes: what it holds.
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (its tokens'

@@ -316,7 +316,8 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   st = check_attn(d, heads, batch->tokens, batch->batch, max_chunk, max_len);
   if (st != LLVQ_OK) return st;
   if (dtype != LLVQ_X_F32 && dtype != LLVQ_X_BF16) return LLVQ_EINVAL;
-  if (!(scale > 0.0f) || !(scale < INFINITY) || window < 0 || window > kMaxLen) return LLVQ_EINVAL;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!(scale > 0.0f) || !(scale_log2 < INFINITY) || window < 0 || window > kMaxLen) return LLVQ_EINVAL;
   if (err_count && !aligned(err_count, 4)) return LLVQ_EINVAL;
   if (c.tokens == 0 || c.batch == 0) return LLVQ_OK;
   const bool f32 = dtype == LLVQ_X_F32;
@@ -342,7 +343,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   a.window = window;
   a.causal = causal != 0;
   a.q_vec = wide(q, q_token, q_head, size);
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.err = err_count;
   if (cut.splits > 1) {
     a.part = static_cast<float*>(workspace);
