@@ -410,7 +410,7 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  *   max_len : at least 1; about the longest length: it decides only how the keys are split, not
  *            what is computed.
  *   scale  : > 0, and scale * log2(e) finite in f32.   window : 0 (none) .. 2^30.
- *   workspace : at least llvq_attn_workspace_bytes(...) bytes for the same arguments, 16-byte aligned
+ *   workspace : llvq_attn_workspace_bytes(...) bytes for these or larger arguments, 16-byte aligned
  *            (may be NULL if that is 0), contents not kept; workspace_bytes: what it holds.
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (its tokens'
  *            keys and values are then taken as zeros), starts or lengths had to be cut, or a sequence has more rows than max_chunk.
@@ -421,7 +421,9 @@ int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_
               int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,
               int64_t workspace_bytes, int32_t* err_count, void* stream);
 
-/* Bytes of llvq_attn's workspace, or LLVQ_EINVAL.  Host only. */
+/* Bytes of a workspace that serves every call of llvq_attn on such a cache with `heads` heads whose tokens, batch,
+ * max_chunk and max_len are no larger, of either dtype and any window (one call alone may need less: fewer sequences
+ * are split into more parts), or LLVQ_EINVAL.  Host only. */
 int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch,
                                   int32_t max_chunk, int32_t max_len);
 
@@ -446,7 +448,8 @@ int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, cons
                       int32_t drafts, int32_t vocab, int32_t* accepted, int32_t* out, void* workspace,
                       int64_t workspace_bytes, int32_t* err_count, void* stream);
 
-/* Bytes of llvq_draft_verify's workspace, or LLVQ_EINVAL.  Host only. */
+/* Bytes of a workspace that serves every call of llvq_draft_verify whose batch and vocabulary are no larger, or
+ * LLVQ_EINVAL.  Host only. */
 int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab);
 
 #ifdef __cplusplus

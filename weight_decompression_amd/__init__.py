@@ -543,6 +543,7 @@ def kv_read(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
 
 
 def attn_workspace_bytes(desc, heads, tokens, batch, max_chunk, max_len) -> int:
+    """Bytes of a workspace for every attn call of no more tokens, sequences, new tokens of one and keys than these."""
     n = load_library().llvq_attn_workspace_bytes(desc, heads, tokens, batch, max_chunk, max_len)
     if n < 0:
         raise LlvqError(int(n), "llvq_attn_workspace_bytes")
@@ -571,11 +572,12 @@ def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len,
     if code:
         need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
         if size < need:
-            raise ValueError(f"{call}: workspace holds {size} bytes; the call needs at least {need}")
+            raise ValueError(f"{call}: invalid argument, or the workspace is short: it holds {size} bytes, {need} are enough")
         raise LlvqError(code, call)
 
 
 def draft_workspace_bytes(batch, vocab) -> int:
+    """Bytes of a workspace for every draft_verify call of no more sequences and entries than these."""
     n = load_library().llvq_draft_workspace_bytes(batch, vocab)
     if n < 0:
         raise LlvqError(int(n), "llvq_draft_workspace_bytes")
@@ -618,5 +620,5 @@ def draft_verify(target, draft, tokens, uniforms, noise, accepted, out, workspac
     if code:
         need = draft_workspace_bytes(b, v)
         if size < need:
-            raise ValueError(f"{call}: workspace holds {size} bytes; the call needs at least {need}")
+            raise ValueError(f"{call}: invalid argument, or the workspace is short: it holds {size} bytes, {need} are enough")
         raise LlvqError(code, call)

@@ -178,9 +178,17 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   return base * cut->splits * parts * 64 * cut->waves >= (1ll << 32) ? LLVQ_EINVAL : LLVQ_OK;
 }
 
-// The splits' sums, maxima and sums of p.
-int64_t workspace_of(const Cut& cut, const llvq_kv_desc* d, int32_t heads, int64_t tokens) {
-  return (int64_t)cut.splits * tokens * heads * (d->head_dim + 2) * 4;
+// The sums, maxima and sums of p of that many (row, split) pairs.
+int64_t workspace_of(const llvq_kv_desc* d, int64_t rows) { return rows * (d->head_dim + 2) * 4; }
+
+// (row, split) pairs that no split call passes.  Few rows: a call of base workgroups is split into resident / base or
+// ceil(2048 / base) parts, so into fewer than 4096 workgroups, of up to 32 rows.  Many: into s >= 2 parts of base *
+// parts * (s - 1/2) <= 2 slots, so into at most 8/3 slots workgroups, of 128 or 256 rows, 2^16 (64-wide heads: 3 *
+// 2^15) on all slots.
+int64_t most_split_rows(int head_dim) {
+  const int dim = padded_dim(head_dim);
+  const int64_t few = 4096 * 32, many = (dim == 64 ? 3ll << 15 : 1ll << 16) * 8 / 3 / (dim > 128 ? 2 : 1);
+  return few > many ? few : many;
 }
 
 int check_attn(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch, int32_t max_chunk, int32_t max_len) {
@@ -295,15 +303,16 @@ LLVQ_API int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads,
                                            int32_t max_chunk, int32_t max_len) {
   int st = check_attn(d, heads, tokens, batch, max_chunk, max_len);
   if (st != LLVQ_OK) return st;
-  int64_t most = 0;
   for (const bool f32 : {false, true}) {  // either type of query
     Cut cut;
     st = cut_of(d, heads / d->kv_heads, batch, max_chunk, max_len, 0, f32, &cut);
     if (st != LLVQ_OK) return st;
-    const int64_t n = cut.splits > 1 ? workspace_of(cut, d, heads, tokens) : 0;
-    if (n > most) most = n;
   }
-  return most;
+  // fewer sequences are split into more parts: the most that any call of no larger arguments needs
+  const int64_t splits = ((int64_t)max_len + 127) / 128;
+  if (splits <= 1) return 0;
+  const int64_t rows = (splits < kMaxSplits ? splits : kMaxSplits) * tokens * heads, most = most_split_rows(d->head_dim);
+  return workspace_of(d, rows < most ? rows : most);
 }
 
 LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
@@ -327,7 +336,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
   Cut cut;
   st = cut_of(d, heads / d->kv_heads, c.batch, max_chunk, max_len, window, f32, &cut);
   if (st != LLVQ_OK) return st;
-  const int64_t need = cut.splits > 1 ? workspace_of(cut, d, heads, c.tokens) : 0;
+  const int64_t need = cut.splits > 1 ? workspace_of(d, (int64_t)cut.splits * c.tokens * heads) : 0;
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LLVQ_EINVAL;
   AttnArgs a = {};
   a.c = c;
@@ -363,7 +372,9 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
 
 LLVQ_API int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab) {
   if (batch < 0 || batch > LLVQ_MAX_SEQS || vocab < 1) return LLVQ_EINVAL;
-  return (int64_t)batch * draft_parts(batch, vocab) * 8;
+  // the most keys of any smaller batch too: batch * parts < 1024 + batch where a row is shared out
+  const int64_t whole = batch, shared = (int64_t)batch * draft_parts(1, vocab), most = 1023 + whole;
+  return 8 * (shared < most ? shared : most);
 }
 
 LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
@@ -379,7 +390,7 @@ LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dt
   if (!aligned(target, size) || !aligned(draft, size) || !aligned(tokens, 4) || !aligned(counts, 4) || !aligned(uniforms, 4) ||
       !aligned(noise, 4) || !aligned(accepted, 4) || !aligned(out, 4) || !aligned(workspace, 8))
     return LLVQ_EINVAL;
-  if (workspace_bytes < llvq_draft_workspace_bytes(batch, vocab)) return LLVQ_EINVAL;
+  if (workspace_bytes < (int64_t)batch * draft_parts(batch, vocab) * 8) return LLVQ_EINVAL;
   DraftArgs a = {};
   a.target = target;
   a.draft = draft;
