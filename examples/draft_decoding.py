@@ -111,6 +111,8 @@ class Decoder:
 
     def forward(self, rows, lens, caches):
         """The model on new tokens rows[b], the last of lens[b] cached ones."""
+        if max(lens) > self.model.max_len:
+            raise ValueError(f"a text of {max(lens)} tokens passes the model's {self.model.max_len} places")
         starts = np.concatenate(([0], np.cumsum([len(r) for r in rows])))
         positions = np.concatenate([np.arange(n - len(r), n) for r, n in zip(rows, lens)])
         dev = lambda x, t: torch.tensor(np.asarray(x), dtype=t, device="cuda")  # noqa: E731
@@ -123,8 +125,10 @@ class Decoder:
 
     def round(self, drafts):
         """One round: drafts tokens a sequence proposed, checked and taken over."""
-        b, v = len(self.text), self.model.vocab
         base = [len(t) for t in self.text]
+        if max(base) + drafts > self.model.max_len:
+            raise ValueError(f"{drafts} drafts after a text of {max(base)} tokens pass the model's {self.model.max_len} places")
+        b, v = len(self.text), self.model.vocab
         probs = torch.empty(b, drafts, v, device="cuda")
         rows = [[t[-1]] for t in self.text]
         tokens = torch.empty(b, drafts, dtype=torch.int32, device="cuda")
@@ -162,12 +166,14 @@ def main():
     model = Model(a.kind)
     prompts = [rng.randint(0, model.vocab, n).tolist() for n in (37, 5, 120)]
     run = Decoder(model, prompts)
-    for _ in range(a.rounds):
+    rounds = 0
+    while rounds < a.rounds and max(map(len, run.text)) + a.drafts <= model.max_len:
         run.round(a.drafts)
+        rounds += 1
     for p, t in zip(prompts, run.text):
         print(f"{len(p)} tokens of prompt, then {t[len(p):]}")
     new = sum(map(len, run.text)) - sum(map(len, prompts))
-    print(f"{run.accepted} of {run.proposed} drafts accepted, {new / (a.rounds * len(prompts)):.2f} tokens a sequence and round")
+    print(f"{run.accepted} of {run.proposed} drafts accepted, {new / max(rounds * len(prompts), 1):.2f} tokens a sequence and round")
 
 
 if __name__ == "__main__":
