@@ -141,25 +141,38 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
   if (base > (1ll << 29)) return LLVQ_EINVAL;
   int64_t s;
   if (cut->cols) {
-    // One round of resident workgroups where a sequence is cut into many parts (three sequences of 131000
-    // keys in e2m1: 81 us at 768 workgroups, 93 at 2048), several where sequences are many and of all
-    // lengths (64 of up to 16384 in e4m3: 268 us at 2048, 324 unsplit), no split where they fill half the
-    // chip and are short (64 x 8 in e4m3 of up to 1000 keys: 25 us, 31 in two and 34 in four; of up to 2000
-    // 39 and 46; past that splitting evens out lengths: of up to 4096 with f32 queries 86, split 85) or fill it twice (57 x 32 of up to 176 keys:
-    // 54 us, 72 split)
+    // Up to half a chip's workgroups: as many parts as fill one round of resident ones (three sequences of 131000
+    // keys in e2m1: 81 us at 768 workgroups, 93 at 2048).  Twice a chip: no split (57 x 32 of up to 176 keys: 54
+    // us, 72 split).  Between, a split fills what the last round leaves idle and evens out lengths, and costs its
+    // sums' way out and back: it needs long sequences, and longer ones where one round is nearly full.  Times split
+    // over unsplit, geometric means of equal and of ragged lengths (a quarter of max_len on) and of bf16 and f32
+    // queries with own and shared keys, 128-wide heads in e4m3, at workgroups over resident ones of
+    //             0.55  0.65  0.75  0.85  1.0   1.2   1.5
+    //   2000 keys 1.18  1.19  1.16  1.22  1.32  1.09  1.15
+    //   3000      1.05  1.04  1.07  1.14  1.22  0.99  1.07
+    //   4096      0.99  1.02  1.02  1.09  1.16  0.97  1.06
+    //   6000      0.92  1.01  0.97  1.07  1.11  0.92  1.00
+    //   8192      0.87  0.97  0.99  1.00  1.07  0.88  1.00
+    // bf16 at 4096 0.90 to 1.04, e2m1 0.91 to 1.11, 64-wide bf16 0.93 to 1.03, 256-wide e4m3 0.97 to 1.40.  The means
+    // hide the lengths' spread: 424 e4m3 workgroups of 4096 keys, 0.91 ragged and 1.19 equal.
     const int64_t resident = 256 * few_waves(d->kind, dim, terms, cut->cols);
-    s = base <= resident / 2                      ? resident / base
-        : base >= 2 * resident || max_len <= 2048 ? 1
-                                                  : (2048 + base - 1) / base;
+    const bool full = base > resident * 4 / 5 && base <= resident;
+    s = base <= resident / 2                                      ? resident / base
+        : base >= 2 * resident || max_len <= (full ? 8192 : 4096) ? 1
+                                                                  : (2048 + base - 1) / base;
     const int64_t most = ((int64_t)max_len + 127) / 128;
     if (s > most) s = most;
     // Short sequences that fill the chip a wave each (64 x 32 in e4m3 of up to 500 keys: 39 us, 42 with four
     // waves; of up to 1000 78 and 73)
     if (base >= 2 * resident && max_len <= 768) cut->waves = 1;
-    // Few short sequences: eight waves a workgroup and no splits, so one launch, while a wave has up to four
-    // pieces (16 x 8 in e4m3 of up to 1000 keys 13.8 us, 16.1 split; of 1500 17.4 and 14.7), three in bf16,
-    // whose pieces take longer to come (32 heads of 777 keys: 13.8 us, 7.4 split and 4.6 for the join)
-    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= (d->kind == LLVQ_KV_BF16 ? 768 : 1024)) cut->waves = 8, s = 1;
+    // Eight waves a workgroup and no split, so one launch: 5 us and about 2.1 more for each 256 keys, while a split
+    // call of few workgroups takes 10 us on the device and 13 in a stream of calls.  Up to 64 workgroups the one launch
+    // pays up to 768 keys (8 x 4 heads of shared keys in e4m3: of 768 keys 11.4 us, split 10.1, in a stream 11.8 and
+    // 13.5; of 896 13.6 and 10.3, in a stream 14.0 and 13.1; bf16, e2m1 and f32 queries alike).  More workgroups leave a
+    // split less to fill.  Split over one launch: 128 workgroups of 1024 keys 0.93 to 1.11, 1280 0.90 to 1.23, 1536
+    // 0.87 to 1.12; 192 of 2048 0.91 to 1.16, 2560 0.95 to 1.13; 256 of 2560 1.02 to 1.12, 3072 0.94 to 1.12.
+    const int64_t one_launch = 10 * base > 768 ? 10 * base : 768;
+    if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= one_launch) cut->waves = 8, s = 1;
   } else {
     // A split shortens a workgroup's way (about 1 us a tile of 64 keys; f32 and wide heads more) and costs
     // its sums' way out and back (8 bytes a channel of every row at 5 TB/s): the least of tiles / s + cost
