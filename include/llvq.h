@@ -414,8 +414,8 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  *            (may be NULL if that is 0), contents not kept; workspace_bytes: what it holds.
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (its tokens'
  *            keys and values are then taken as zeros), starts or lengths had to be cut, or a sequence has more rows than max_chunk.
- * Sums, maxima and outputs are f32; bf16 queries take P in bf16, f32 queries take Q and P in three
- * bf16 terms.  Deterministic.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+ * Sums, maxima and outputs are f32.  f32 queries take Q and P in three bf16 terms; bf16 queries take P in two where a
+ * (sequence, key head) has up to 64 rows (max_chunk * heads / kv_heads), rounded to bf16 where it has more.  Deterministic.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
               int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
               int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,

@@ -80,6 +80,29 @@ def test_values_of_bytes_that_no_write_leaves(kind, dim, new, max_len, dtype):
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("max_len", [1, 100000])
 @pytest.mark.parametrize("new", [6, 140])
+@pytest.mark.parametrize("dim", [64, 128, 160, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_written_values_that_are_not_finite(kind, dim, new, max_len, dtype):
+    h = Hidden(kind, dim, new, 50, seed=dim + new)
+    su, first = h.su, h.first
+    clean = run_attn(su, h.q, dtype, max_len=max_len)
+    k, v = torch.randn(2, 1, 2, dim, device="cuda")
+    v[0, 0, dim - 1], v[0, 1, 3] = float("-inf"), float("nan")
+    wd.kv_write(su.desc, su.pool, k, v, *h.plan)
+    held = h.read()
+    odd = ~torch.isfinite(held)
+    assert odd.sum() == (2 if kind == "bf16" else 64)
+    out = run_attn(su, h.q, dtype, max_len=max_len)
+    assert torch.equal(out[:first], clean[:first])
+    rows = odd.repeat_interleave(2, 0).expand(new - first, 4, dim)
+    assert torch.equal(~torch.isfinite(out[first:]), rows)
+    if kind == "bf16":
+        assert (out[first:, :2, dim - 1] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("max_len", [1, 100000])
+@pytest.mark.parametrize("new", [6, 140])
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 def test_a_large_key_that_a_row_does_not_see(kind, new, max_len, dtype):
     h = Hidden(kind, 128, new, 370, seed=new)

@@ -15,10 +15,14 @@
 // a time.
 //
 // Codes become bf16 exactly (at most 4 significant bits times a power of two), so staging a tile as bf16 in
-// LDS loses nothing.  Scores, maxima, sums and outputs are f32.  P is rounded to bf16 (relative 2^-8 at
-// most, the same as the rounding of a bf16 output), and the sum of P is that of the rounded values, so that
-// their common part cancels.  For f32 queries both Q and P are split into three bf16 terms (x = hi + mid +
-// lo, what is left is below 2^-26 |x|), three matrix instructions in the place of one.
+// LDS loses nothing.  Scores, maxima, sums and outputs are f32.  For f32 queries both Q and P are split into three
+// bf16 terms (x = hi + mid + lo, what is left is below 2^-26 |x|), three matrix instructions in the place of one.  For
+// bf16 queries of few rows P is split into two (2^-17), so that the output's rounding is the only one that counts;
+// that costs 1 % of a decode step in e4m3 (268 us, 271), 3 % in e2m1 (77.6, 80.2) and up to 12 % where two tiles of
+// shared heads read e2m1 (4 new tokens of 64 sequences, 64 heads over 8: 71.9, 80.6).  Of many rows, where the matrix
+// instructions are the bound and a second term would cost a quarter, P is rounded to bf16 (relative 2^-8 at most, as a
+// bf16 output is), and the sum of P is that of the rounded values, so that their common part cancels: the error
+// against 64 bits is 0.0021 of the result's norm, 0.0017 from the output's rounding alone.
 //
 // Two kernels share this: k_attn_few for up to 64 rows of a (sequence, key head), where a workgroup's waves
 // share out the keys, and k_attn_many, where they share out the rows.
@@ -125,11 +129,11 @@ __device__ __forceinline__ bool drop_odd(u32x4* raw) {
   return true;
 }
 
-// A lane's eight p, added to its four sums.  bf16 queries: the rounded values, two at a time, so that what all
-// of a row's roundings have in common cancels.
-template <int NT>
+// A lane's eight p, added to its four sums.  Where one term is all of P: the rounded values, two at a time, so that what
+// all of a row's roundings have in common cancels.
+template <int TERMS>
 __device__ __forceinline__ void sum_p(const float* x, const bf16x8& rounded, float* l4) {
-  if constexpr (NT == 1) {
+  if constexpr (TERMS == 1) {
     const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
 #pragma unroll
     for (int e = 0; e < 4; ++e) l4[e] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{rounded[2 * e], rounded[2 * e + 1]}, one, l4[e], false);
@@ -331,6 +335,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
   constexpr int kLoads = 32 * kRaw / kWave;        // chunks a lane loads of a piece
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
   constexpr int kSteps = DP / 32, kOut = DP / 16;
+  constexpr int kTerms = NT == 1 ? 2 : NT;  // of P: with one, its roundings do not average out over few keys
   const Cache& c = a.c;
   using Lds = FewLds<DP>;
   __shared__ __align__(16) uint8_t lds[kWaves * Lds::kWaveBytes];
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
       }
     }
     const bool whole = key_base >= w.all_lo && key_base + 32 <= w.all_hi && key_base + 32 <= s.len;
-    bf16x8 p[NT][CT];
+    bf16x8 p[kTerms][CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       if (!whole) {
@@ -525,11 +530,11 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(score[ct][i / 4][i & 3], a.scale_log2, -ms));
-      bf16x8 terms[NT];
-      split_terms<NT>(x, terms);
-      sum_p<NT>(x, terms[0], l4[ct]);
+      bf16x8 terms[kTerms];
+      split_terms<kTerms>(x, terms);
+      sum_p<kTerms>(x, terms[0], l4[ct]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) p[n][ct] = terms[n];
+      for (int n = 0; n < kTerms; ++n) p[n][ct] = terms[n];
     }
     // the values, in the keys' place.  Those that are not finite would spoil rows that do not see them (0 * NaN):
     // they are left out here and added to the rows that do see them at the end
@@ -562,7 +567,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int n = NT - 1; n >= 0; --n) acc[ct][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf.v, p[n][ct], acc[ct][d], 0, 0, 0);
+        for (int n = kTerms - 1; n >= 0; --n) acc[ct][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf.v, p[n][ct], acc[ct][d], 0, 0, 0);
     }
   }
   if (a.err && lost) atomicAdd(a.err, 1);
