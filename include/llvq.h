@@ -391,7 +391,8 @@ int llvq_kv_write(const llvq_kv_desc* d, void* pool, const void* k, int64_t k_to
 
 /* Read cached tokens back: the same rows and positions as llvq_kv_write (starts = running sums
  * of lens reads whole sequences).  bf16 and f32 outputs hold the cached values exactly; a token
- * that has no place reads as zeros and is counted.  Arguments as for llvq_kv_write. */
+ * that has no place reads as zeros and is counted.  Arguments as for llvq_kv_write; k and v overlap neither each other
+ * nor the pool. */
 int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_token, int64_t k_head, void* v,
                  int64_t v_token, int64_t v_head, int32_t dtype, const llvq_batch* batch, int32_t* err_count,
                  void* stream);
@@ -404,7 +405,10 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  * that a row does not see have no effect on it, whatever they hold.
  *   q, out : [tokens][heads][head_dim], LLVQ_X_F32 or LLVQ_X_BF16 (`dtype`, both), channels contiguous; strides in
  *            elements, >= 0; out aligned to 4 elements, its strides multiples of 4.
- *   heads  : a multiple of kv_heads.
+ *            out overlaps neither q nor the pool.
+ *   heads  : a multiple of kv_heads, up to 65536; tokens * heads and max_chunk * heads below 2^31.  A launch has
+ *            fewer than 2^32 threads: batch * kv_heads * R up to 2^27, R = max_chunk * heads / kv_heads rounded up
+ *            to a multiple of 256, is always taken, some of what is larger refused.
  *   max_chunk : at least the new tokens of any sequence, and batch * max_chunk >= tokens (rows of a sequence past it
  *            may be left unwritten: counted).
  *   max_len : at least 1; about the longest length: it decides only how the keys are split, not
@@ -415,7 +419,9 @@ int llvq_kv_read(const llvq_kv_desc* d, const void* pool, void* k, int64_t k_tok
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (its tokens'
  *            keys and values are then taken as zeros), starts or lengths had to be cut, or a sequence has more rows than max_chunk.
  * Sums, maxima and outputs are f32.  f32 queries take Q and P in three bf16 terms; bf16 queries take P in two where a
- * (sequence, key head) has up to 64 rows (max_chunk * heads / kv_heads), rounded to bf16 where it has more.  Deterministic.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+ * (sequence, key head) has up to 64 rows (max_chunk * heads / kv_heads), rounded to bf16 where it has more.  p * V is
+ * summed before it is divided, with p up to 2^8: |V| * max_len has to stay below 2^119.  Deterministic.
+ * Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
               int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
               int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, void* workspace,

@@ -538,7 +538,8 @@ def kv_write(desc, pool, k, v, starts, lens, table, err_count=None, stream=None)
 
 
 def kv_read(desc, pool, k, v, starts, lens, table, err_count=None, stream=None):
-    """Read the same rows back into k and v (fp32 or bf16), as the values they stand for."""
+    """Read the same rows back into k and v (fp32 or bf16; apart from each other and the pool), as the values they stand
+    for."""
     _kv_call("llvq_kv_read", desc, pool, k, v, starts, lens, table, err_count, stream)
 
 
@@ -554,8 +555,8 @@ def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len,
          err_count=None, stream=None):
     """out[i][h] = softmax(scale * q[i][h] . K) V over the cached tokens that new token i sees.
     q and out: [tokens][heads][head_dim], fp32 or bf16; scale: 1 / sqrt(head_dim) if None; max_chunk: at least any
-    sequence's new tokens; max_len: about the longest length (decides only how the keys are split);
-    workspace: attn_workspace_bytes(...) bytes (None if that is 0)."""
+    sequence's new tokens; max_len: about the longest length (decides only how the keys are split); out overlaps neither q
+    nor the pool; workspace: attn_workspace_bytes(...) bytes for these or larger arguments (None if that is 0)."""
     import torch
     call = "llvq_attn"
     heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0

@@ -283,9 +283,9 @@ __device__ __forceinline__ bool nan_scales(uint32_t* words) {
 // ahead).  With 16x16x32 instructions a lane holds 8 scores of a piece, and a tile of outputs takes DP / 4
 // registers of a lane. (Tiles shared by the workgroup, with the kernel below and its barriers, took a step
 // of 64 sequences of up to 16384 tokens, 64 heads over 8 key heads of 128 channels in e4m3, 837 us; this
-// takes 261 us, 5.4 TB/s, where a large copy reaches 4.9.  Three sequences of up to 131000 tokens in e2m1:
-// 75 us, 4.4 TB/s; 16 of up to 4096 with 8 drafts each, f32, 32 heads: 83 us, 4.4 TB/s.  One token of 32
-// heads over 777 keys in bf16 takes 7.5 us and the join 4: a chain of six loads, each waiting for the one
+// takes 267 us, 5.3 TB/s, where a large copy reaches 4.9.  Three sequences of up to 131000 tokens in e2m1:
+// 78 us, 4.3 TB/s; 16 of up to 4096 with 8 drafts each, f32, 32 heads: 87 us, 4.2 TB/s.  One token of 32
+// heads over 777 keys in bf16 takes 7.4 us and the join 4: a chain of six loads, each waiting for the one
 // before.) In S^T's layout a lane (column lane % 16, g = lane / 16) holds keys 4 g + i and 16 + 4 g + i,
 // which are taken as the eight consecutive keys of its place in the second product; the transposing load
 // reads V's rows in the same order. Rows in LDS are padded, so that every address is one register and a
@@ -326,8 +326,8 @@ constexpr bool few_pairs(int kind, int dp, int nt) { return few_waves(kind, dp, 
 // TEAM: the waves that share out the keys of a row block.  1: a workgroup's four waves have a row block
 // each, and no barrier; for so many short sequences that they fill the chip this way, where a team's start
 // and its joining would take longer than the keys (57 sequences of up to 176 tokens, 32 key heads of 192
-// channels in e2m1, 5 new tokens: 42 us, 54 with teams of four; 64 of up to 1000, 32 heads of 128 in e4m3:
-// 77 us, 4.6 TB/s).
+// channels in e2m1, 5 new tokens: 42 us, 54 with teams of four; 64 of up to 500, 32 heads of 128 in e4m3:
+// 43 us, 4.1 TB/s).
 template <int KIND, int DP, int NT, int CT, int TEAM>
 __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
   constexpr int kWaves = TEAM == 1 ? 4 : TEAM;
@@ -654,15 +654,16 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
 // the other buffer and the loads of the one after it are issued, then the second product.  Operands are
 // read four instructions ahead in a pinned order.
 //
-// Measured at 2 x 2048 new tokens over 8192, 32 heads of 128 channels in e4m3: 490 us, 980 TFLOP/s, 82 % of
-// what a large bf16 library product reaches.  Without the staging 80 us less, without the softmax 65,
-// without both 370 us, near the 290 us that the same instructions take alone (the clock falls under them).
-// 64-wide heads have twice the softmax a product: 24 heads over 4 key heads in e2m1, window 1000, 79 us,
-// 415 TFLOP/s.
+// Measured at 2 x 2048 new tokens over 8192, 32 heads of 128 channels in e4m3: 480 to 513 us a call over several
+// cards, 940 to 1000 TFLOP/s, about 80 % of what a large bf16 library product reaches (the kernel alone under a
+// tracer, which leaves the chip idle between launches, 540).  Taken apart when it stood at 490: without the staging 80
+// us less, without the softmax 65, without both 370 us, near the 290 us that the same instructions take alone (the
+// clock falls under them).  64-wide heads have twice the softmax a product: 24 heads over 4 key heads in e2m1, window
+// 1000, 75 us, 438 TFLOP/s.  f32 queries take three times the instructions: 1193 us at the first of these sizes.
 //
 // Heads of more than 128 channels are taken in two halves of the output by two workgroups, which both take
 // the first product: half again the products, but what a wave holds fits two waves a SIMD (16 heads of 256
-// channels in bf16, 3 x 700 over 3500: 220 us instead of 391 at the time).
+// channels in bf16, 3 x 700 over 3500: 220 us instead of 391 when this was done; 192 now with its join of 18).
 template <int KIND, int DP, int NT, int WAVES>
 struct ManyShape {
   static constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES;

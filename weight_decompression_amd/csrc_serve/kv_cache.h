@@ -1,17 +1,17 @@
 // The paged key/value cache: quantised as it is written, read back as the values it stands for.
 //
 // A group of 32 channels of one token and head is held as codes with one power-of-two scale: value = code *
-// 2^e, e the smallest integer with max|x| <= top * 2^e (top = 448 for e4m3, 6 for e2m1), so that nothing
-// saturates.  Dividing by 2^e and multiplying back are exact in f32; the only rounding is the code's own,
-// to nearest, ties to even.  A value has at most 4 significant bits and an exponent that e's limits keep
+// 2^e, e the smallest integer with max|x| <= top * 2^e (top = 448 for e4m3, 6 for e2m1), held within [-100, 119 or
+// 125]: values saturate only within the last factor of f32's range, past top * 2^119 or 2^125.  Dividing by 2^e and
+// multiplying back are exact in f32; the only rounding is the code's own, to nearest, ties to even.  A value has at most 4 significant bits and an exponent that e's limits keep
 // normal, so it is exact in bf16.  A group with a value that is not finite has the scale byte 255 and reads
 // back as NaN.
 //
 // Both kernels move each byte once and compute little: HBM bounds them.  A wave holds one token or four
 // (their sequences, positions and pages are the wave's, found once), one lane 8 channels; four lanes share
-// a group. Measured: 14.6 k new tokens of 32 heads of 128 channels, bf16 to e2m1, written in 67 us (4.5
-// TB/s) and read back in 45 us; a cache of 8 heads in e4m3 read whole to bf16, 804 MB in and out, in 137 us
-// (5.9 TB/s).  A large copy reaches 4.9 TB/s.  Few tokens take 3 us, a launch's least.
+// a group. Measured (medians): 12.3 k new tokens of 32 heads of 128 channels, bf16 to e2m1, written in 67 to 73 us
+// (3.5 to 3.8 TB/s) and read back in 46 us (5.5); a cache of 8 heads in e4m3 read whole to bf16, 804 MB in and out, in 159 us
+// (5.0 TB/s).  A large copy reaches 4.9 TB/s.  Few tokens take 3 us, a launch's least.
 #pragma once
 
 #include "serve_common.h"
@@ -40,7 +40,7 @@ __device__ __forceinline__ bool place_of(const Cache& c, int t, int64_t* base, i
   return true;
 }
 
-// STREAM: what is read once does not displace the cache's own lines (a prompt of 14.6 k tokens of 32 heads
+// STREAM: what is read once does not displace the cache's own lines (a prompt of 12.3 k tokens of 32 heads
 // in e2m1: 69 us instead of 82).
 template <bool F32, bool VEC, bool STREAM = false>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float* x) {
