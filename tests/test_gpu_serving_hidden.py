@@ -118,3 +118,23 @@ def test_a_large_key_that_a_row_does_not_see(kind, new, max_len, dtype):
 def dev_sign(q):
     """The signs of the last row's queries, a head of each pair: its score with such a key is large."""
     return torch.from_numpy(np.sign(q[-1:, ::2])).cuda()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("max_len", [1, 100000])
+@pytest.mark.parametrize("new", [9, 150])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_a_padded_chunk_over_places_never_written(kind, new, max_len, dtype):
+    """A chunk padded to a fixed length in a pool of arbitrary bytes: the rows before the padding are those of the
+    unpadded chunk."""
+    pad = new // 3
+    su = Setup(kind, 2, 128, 16, [new], [new + 40], seed=new)
+    su.pool.copy_(torch.from_numpy(su.rng.randint(0, 256, su.pool.numel()).astype(np.uint8)))
+    total = new + 40 - pad
+    k, v = torch.randn(2, total, 2, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(new))
+    wd.kv_write(su.desc, su.pool, k, v, *su.plan(starts=[0, total], lens=[total]))
+    q = torch.from_numpy(su.rng.randn(new, 4, 128).astype(np.float32)).cuda().to(dtype)
+    padded = run_attn(su, q, dtype, max_len=max_len)
+    short = run_attn(su, q[:new - pad].contiguous(), dtype, max_len=max_len, max_chunk=new,
+                     plan=su.plan(starts=[0, new - pad], lens=[total]))
+    assert torch.isfinite(short).all() and torch.equal(padded[:new - pad], short)
