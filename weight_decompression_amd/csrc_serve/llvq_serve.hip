@@ -170,7 +170,7 @@ int cut_of(const llvq_kv_desc* d, int64_t share, int32_t batch, int32_t max_chun
     // pays up to 768 keys (8 x 4 heads of shared keys in e4m3: of 768 keys 11.4 us, split 10.1, in a stream 11.8 and
     // 13.5; of 896 13.6 and 10.3, in a stream 14.0 and 13.1; bf16, e2m1 and f32 queries alike).  More workgroups leave a
     // split less to fill.  Split over one launch: 128 workgroups of 1024 keys 0.93 to 1.11, 1280 0.90 to 1.23, 1536
-    // 0.87 to 1.12; 192 of 2048 0.91 to 1.16, 2560 0.95 to 1.13; 256 of 2560 1.02 to 1.12, 3072 0.94 to 1.12.
+    // 0.87 to 1.12; 192 of 2048 0.91 to 1.16, 2560 0.95 to 1.13; 256 of 2560 1.02 to 1.12.
     const int64_t one_launch = 10 * base > 768 ? 10 * base : 768;
     if (cut->cols == 1 && dim <= 128 && base <= 256 && max_len <= one_launch) cut->waves = 8, s = 1;
   } else {
