@@ -348,6 +348,7 @@ enum { LLVQ_KV_BF16 = 0, LLVQ_KV_FP8 = 1, LLVQ_KV_FP4 = 2 };
 #define LLVQ_MAX_SEQS 32768
 #define LLVQ_MAX_TOKENS (1 << 27)
 #define LLVQ_MAX_DRAFTS 63
+#define LLVQ_MAX_NODES 64
 
 typedef struct {
   int32_t kind;        /* LLVQ_KV_*                                               */
@@ -432,6 +433,30 @@ int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_
  * are split into more parts), or LLVQ_EINVAL.  Host only. */
 int64_t llvq_attn_workspace_bytes(const llvq_kv_desc* d, int32_t heads, int64_t tokens, int32_t batch,
                                   int32_t max_chunk, int32_t max_len);
+
+/* llvq_attn that also gives lse[i * heads + h] = log sum_j exp(scale * q[i][h] . K_j) over the keys that the row sees
+ * (minus infinity if there is none): f32 [tokens][heads], contiguous, 4-byte aligned; rows that belong to no sequence are left
+ * as they were.  The other arguments, the workspace's size and out are those of llvq_attn; where the keys are split and q is
+ * bf16, the last bits of out may differ from llvq_attn's. */
+int llvq_attn_lse(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
+                  int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
+                  int32_t max_chunk, int32_t max_len, float scale, int32_t causal, int32_t window, float* lse,
+                  void* workspace, int64_t workspace_bytes, int32_t* err_count, void* stream);
+
+/* Attention of drafted trees.  A sequence's n = starts[b+1] - starts[b] <= LLVQ_MAX_NODES new tokens are the nodes 0 .. n-1 of
+ * a tree (or of several); they lie at the positions lens[b] - n + i as in llvq_kv_write, after the text.  parents[starts[b] + i]
+ * is node i's parent, an earlier node of the sequence, or -1: the node follows the text.  With T = lens[b] - n and the depth
+ * d_i = d_parent + 1 (0 after the text), node i stands for position T + d_i: it sees the text's positions j < T, itself and
+ * the nodes above it, of all these with window > 0 only those that stand for a position above T + d_i - window.
+ *   parents   : [tokens], 4-byte aligned.   max_chunk : 1 .. LLVQ_MAX_NODES.
+ *   err_count : as for llvq_attn, and + 1 or more for a sequence with a parent that is no earlier node (then taken as -1) or
+ *               more than LLVQ_MAX_NODES new tokens (a node past them is seen by none and sees the text alone).
+ * The other arguments, the workspace's size, roundings and results are those of llvq_attn; a chain (parents -1, 0, 1, ..) gives
+ * what llvq_attn gives with causal. */
+int llvq_attn_tree(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
+                   int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
+                   const int32_t* parents, int32_t max_chunk, int32_t max_len, float scale, int32_t window, void* workspace,
+                   int64_t workspace_bytes, int32_t* err_count, void* stream);
 
 /* Check drafted tokens against the target's probabilities.  With n = counts[b] (or drafts),
  * draft i < n is accepted while uniforms[b][i] * draft[b][i][x_i] < target[b][i][x_i] and all before it were,

@@ -22,6 +22,7 @@ KV_BF16 = 0
 KV_FP8 = 1
 KV_FP4 = 2
 MAX_DRAFTS = 63
+MAX_NODES = 64
 
 _ERRORS = {0: "ok", -1: "invalid argument", -2: "unsupported request", -3: "HIP launch error",
            -4: "request larger than the library's fixed workspace"}
@@ -36,7 +37,7 @@ EXPORTED_SYMBOLS = ("llvq_index_count", "llvq_packed_bytes", "llvq_error_string"
                     "llvq_quantize_noalloc_max_blocks", "llvq_gptq_workspace_bytes", "llvq_gptq_factor",
                     "llvq_gptq_begin", "llvq_gptq_column", "llvq_device_checks", "llvq_kv_pool_bytes",
                     "llvq_kv_write", "llvq_kv_read", "llvq_attn", "llvq_attn_workspace_bytes",
-                    "llvq_draft_verify", "llvq_draft_workspace_bytes")
+                    "llvq_draft_verify", "llvq_draft_workspace_bytes", "llvq_attn_lse", "llvq_attn_tree")
 
 
 class LlvqError(RuntimeError):
@@ -141,6 +142,10 @@ def load_library(path=LIB_PATH):
         getattr(lib, name).restype = ctypes.c_int
     lib.llvq_attn.argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, i32, bp, i32, i32, f32, i32, i32, vp, i64, vp, vp]
     lib.llvq_attn.restype = ctypes.c_int
+    lib.llvq_attn_lse.argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, i32, bp, i32, i32, f32, i32, i32, vp, vp, i64, vp, vp]
+    lib.llvq_attn_lse.restype = ctypes.c_int
+    lib.llvq_attn_tree.argtypes = [kp, vp, vp, i64, i64, vp, i64, i64, i32, i32, bp, vp, i32, i32, f32, i32, vp, i64, vp, vp]
+    lib.llvq_attn_tree.restype = ctypes.c_int
     lib.llvq_attn_workspace_bytes.argtypes = [kp, i32, i64, i32, i32, i32]
     lib.llvq_attn_workspace_bytes.restype = i64
     lib.llvq_draft_verify.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, i64, vp, vp]
@@ -551,14 +556,10 @@ def attn_workspace_bytes(desc, heads, tokens, batch, max_chunk, max_len) -> int:
     return n
 
 
-def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, scale=None, causal=True, window=0,
-         err_count=None, stream=None):
-    """out[i][h] = softmax(scale * q[i][h] . K) V over the cached tokens that new token i sees.
-    q and out: [tokens][heads][head_dim], fp32 or bf16; scale: 1 / sqrt(head_dim) if None; max_chunk: at least any
-    sequence's new tokens; max_len: about the longest length (decides only how the keys are split); out overlaps neither q
-    nor the pool; workspace: attn_workspace_bytes(...) bytes for these or larger arguments (None if that is 0)."""
+def _attn_call(call, desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, err_count, stream, between):
+    """The checks and the call that attn's forms share; between: the C entry's arguments from the batch to the workspace, or a
+    function of the device and [tokens, heads] that checks and gives them."""
     import torch
-    call = "llvq_attn"
     heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
     if heads < 1 or desc.kv_heads < 1 or heads % desc.kv_heads:
         raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
@@ -568,13 +569,54 @@ def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len,
     at, batch = _paged(desc, pool, starts, lens, table, q.shape[0], device, call)
     ws, size = (None, 0) if workspace is None else _space(workspace, device, call)
     err = None if err_count is None else _count(err_count, device, call)
-    code = _launch(load_library().llvq_attn, device, stream, desc, at, *rows, dtype, heads, batch, max_chunk, max_len,
-                   desc.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, size, err)
+    code = _launch(getattr(load_library(), call), device, stream, desc, at, *rows, dtype, heads, batch,
+                   *(between if type(between) is tuple else between(device, (q.shape[0], heads))), ws, size, err)
     if code:
         need = attn_workspace_bytes(desc, heads, q.shape[0], batch.batch, max_chunk, max_len)
         if size < need:
             raise ValueError(f"{call}: invalid argument, or the workspace is short: it holds {size} bytes, {need} are enough")
         raise LlvqError(code, call)
+
+
+def _vector(t, call, name, dtype, shape, device):
+    """Checks a contiguous device tensor of that shape; returns its address."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _buffer(t, call, name, dtype)
+        _one_device(call, device, t)
+        raise ValueError(f"{call}: {name} must be {list(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def attn(desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, scale=None, causal=True, window=0,
+         err_count=None, stream=None, lse=None):
+    """out[i][h] = softmax(scale * q[i][h] . K) V over the cached tokens that new token i sees.
+    q and out: [tokens][heads][head_dim], fp32 or bf16; scale: 1 / sqrt(head_dim) if None; max_chunk: at least any
+    sequence's new tokens; max_len: about the longest length (decides only how the keys are split); out overlaps neither q
+    nor the pool; workspace: attn_workspace_bytes(...) bytes for these or larger arguments (None if that is 0); lse: if given,
+    fp32 [tokens][heads], receives log sum exp(scale * q[i][h] . K) of each row."""
+    import torch
+    scale = desc.head_dim ** -0.5 if scale is None else scale
+    if lse is None:
+        _attn_call("llvq_attn", desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, err_count, stream,
+                   (max_chunk, max_len, scale, 1 if causal else 0, window))
+    else:
+        _attn_call("llvq_attn_lse", desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, err_count, stream,
+                   lambda device, shape: (max_chunk, max_len, scale, 1 if causal else 0, window,
+                                          _vector(lse, "llvq_attn_lse", "lse", torch.float32, shape, device)))
+
+
+def attn_tree(desc, pool, q, out, starts, lens, table, parents, workspace, max_chunk, max_len, scale=None, window=0,
+              err_count=None, stream=None):
+    """attn for trees of drafted tokens: a sequence's new tokens are the nodes of a tree, parents [tokens] (int32) gives each
+    node's parent among them (-1: it follows the text), and a node sees the text, the nodes above it and itself.  At most
+    MAX_NODES new tokens a sequence; the workspace is attn's."""
+    import torch
+    call = "llvq_attn_tree"
+    scale = desc.head_dim ** -0.5 if scale is None else scale
+    _attn_call(call, desc, pool, q, out, starts, lens, table, workspace, max_chunk, max_len, err_count, stream,
+               lambda device, shape: (_vector(parents, call, "parents", torch.int32, shape[:1], device), max_chunk, max_len, scale,
+                                      window))
 
 
 def draft_workspace_bytes(batch, vocab) -> int:

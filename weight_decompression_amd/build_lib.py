@@ -5,7 +5,7 @@ Steps:
   2. run it to write the table header (and a JSON dump of the same tables), the
      generated device code of the nearest-point search, and the class records of the
      general decoder (shells beyond 10, fields beyond 64 bits; also dumped as JSON);
-  3. compile csrc/llvq.hip and csrc_serve/llvq_serve.hip for gfx950 with hipcc into
+  3. compile csrc/llvq.hip and the units of csrc_serve for gfx950 with hipcc into
      weight_decompression_amd/libllvq.so.
 
 Generated files go to <repo>/_build/ (not committed).  Packed-fp32 VALU instructions
@@ -21,6 +21,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 CSRC_SERVE = os.path.join(PKG_DIR, "csrc_serve")
+SERVE_UNITS = ("llvq_serve.hip", "llvq_tree.hip", "llvq_evict.hip")
 INCLUDE = os.path.join(REPO_DIR, "include")
 BUILD_DIR = os.path.join(REPO_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libllvq.so")
@@ -91,8 +92,8 @@ def build(verbose=True, device_checks=False):
     ]
     if device_checks:
         cmd.insert(1, "-DLLVQ_DEVICE_CHECKS")
-    # the two units are compiled side by side, into names private to this process
-    units = [os.path.join(CSRC, "llvq.hip"), os.path.join(CSRC_SERVE, "llvq_serve.hip")]
+    # the units are compiled side by side, into names private to this process
+    units = [os.path.join(CSRC, "llvq.hip")] + [os.path.join(CSRC_SERVE, name) for name in SERVE_UNITS]
     objects = [os.path.join(BUILD_DIR, f"{os.path.basename(out)}.{i}.{os.getpid()}.tmp.o") for i in range(len(units))]
     try:
         runs = []

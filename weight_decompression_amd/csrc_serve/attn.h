@@ -44,7 +44,45 @@ struct AttnArgs {
   int32_t row_blocks, splits, units, window, causal, q_vec;  // units: row blocks of all sequences and splits
   float scale_log2;
   int32_t* err;
+  const int32_t* parents;  // kTree: [tokens]
+  float* lse;              // kLse: [tokens][heads]
 };
+
+// Forms of the kernels.  kTree: a sequence's new tokens are the nodes of a tree, and a node sees the text before them
+// and the nodes above it.  kLse: log sum_j exp(scale q_i . k_j) of every row is written as well.
+enum { kPlain, kTree, kLse };
+
+// What each node of a sequence's tree sees of the others, itself included: lane i holds node i's set, and its depth.
+// A lane starts with its node and its parent; in each round it takes over what its 2^k-th ancestor has found, so a
+// tree of depth 7 takes three rounds of shuffles, where the walk up would wait for a load a step.
+struct Node {
+  uint64_t above;
+  int depth;
+  bool bad;  // a parent that is not an earlier node (taken as none), or more nodes than a tree may have
+};
+__device__ __forceinline__ Node node_of(const AttnArgs& a, const Seq& s) {
+  const int lane = threadIdx.x & 63;
+  const bool in = lane < s.n;
+  int up = in ? a.parents[s.first + lane] : -1;
+  Node x;
+  x.bad = up < -1 || up >= lane || s.n > LLVQ_MAX_NODES;
+  if (up < -1 || up >= lane) up = -1;
+  x.above = in ? 1ull << lane : 0;
+  while (__any(up >= 0)) {
+    const uint64_t more = (uint64_t)__shfl((unsigned long long)x.above, up & 63);
+    const int next = __shfl(up, up & 63);
+    if (up >= 0) x.above |= more, up = next;
+  }
+  x.depth = in ? __popcll(x.above) - 1 : 0;
+  // parents come before their children: the nearest are the highest bits
+  if (a.window > 0)
+    for (int over = x.depth + 1 - a.window; over > 0; --over) x.above &= x.above - 1;
+  return x;
+}
+
+__device__ __forceinline__ float log_sum(float m, float l) {  // of a maximum in log2 units and the sum under it
+  return l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+}
 
 constexpr float kRescaleStep = 8.0f;  // log2: how far a maximum may be passed before the sums are rescaled
 
@@ -168,15 +206,17 @@ __device__ __forceinline__ f32x4 nonfinite4(const Cache& c, const uint8_t* blk, 
 struct Span {
   int first_key, last_key, all_lo, all_hi, tile_lo, tile_hi;
 };
+template <int MODE>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int row0, int block_rows, int keys, int split) {
   const int rows = s.n * (int)a.share.by;
   const int t0 = (int)divide((uint32_t)row0, a.share);
   const int t1 = (int)divide((uint32_t)(min(row0 + block_rows, rows) - 1), a.share);
-  const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
+  // (a node is at a depth from 0 up to its index, and sees no later one)
+  const int p0 = s.len - s.n + (MODE == kTree ? 0 : t0), p1 = s.len - s.n + t1;
   Span w;
   w.last_key = a.causal ? min(max(p1 + 1, 0), s.len) : s.len;
   w.first_key = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
-  w.all_hi = a.causal ? p0 + 1 : s.len;
+  w.all_hi = MODE == kTree ? p0 : a.causal ? p0 + 1 : s.len;
   w.all_lo = a.window > 0 ? max(p1 - a.window + 1, 0) : 0;
   const int tile0 = w.first_key / keys;
   const int tiles = w.last_key > w.first_key ? (w.last_key + keys - 1) / keys - tile0 : 0;
@@ -202,6 +242,18 @@ __device__ __forceinline__ void seen_of(const AttnArgs& a, const Seq& s, int t, 
   const int hi = a.causal ? min(max(pos + 1, 0), s.len) : s.len;
   *lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
   *seen = live ? max(hi - *lo, 0) : 0;
+}
+
+// The same for a node at that depth: of the text, [lo, lo + seen); the nodes it sees are in its set.
+__device__ __forceinline__ void seen_of_node(const AttnArgs& a, const Seq& s, int depth, bool live, int* lo, int* seen) {
+  const int text = s.len - s.n;
+  *lo = a.window > 0 ? max(text + depth - a.window + 1, 0) : 0;
+  *seen = live ? max(text - *lo, 0) : 0;
+}
+template <int MODE>
+__device__ __forceinline__ bool sees(int j, int lo, int seen, int text, uint64_t above) {
+  if ((uint32_t)(j - lo) < (uint32_t)seen) return true;
+  return MODE == kTree && (uint32_t)(j - text) < 64u && (above >> ((j - text) & 63) & 1) != 0;
 }
 
 // 8 channels of a query row as NT bf16 terms.
@@ -236,8 +288,9 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t row, int64
 }
 
 // Scores of keys that a row does not see do not count.
-__device__ __forceinline__ float masked(float s, int j, int lo, int seen) {
-  return (uint32_t)(j - lo) < (uint32_t)seen ? s : -INFINITY;
+template <int MODE>
+__device__ __forceinline__ float masked(float s, int j, int lo, int seen, int text, uint64_t above) {
+  return sees<MODE>(j, lo, seen, text, above) ? s : -INFINITY;
 }
 
 // Four scale bytes of a token (from byte 4 n on; 127, one, past the last), in loads as wide as their place
@@ -328,7 +381,7 @@ constexpr bool few_pairs(int kind, int dp, int nt) { return few_waves(kind, dp, 
 // and its joining would take longer than the keys (57 sequences of up to 176 tokens, 32 key heads of 192
 // channels in e2m1, 5 new tokens: 42 us, 54 with teams of four; 64 of up to 500, 32 heads of 128 in e4m3:
 // 43 us, 4.1 TB/s).
-template <int KIND, int DP, int NT, int CT, int TEAM>
+template <int KIND, int DP, int NT, int CT, int TEAM, int MODE>
 __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KIND, DP, NT, CT)) void k_attn_few(AttnArgs a) {
   constexpr int kWaves = TEAM == 1 ? 4 : TEAM;
   constexpr int kRaw = code_bytes(KIND, DP) / 16;  // 16-byte chunks of a row of codes
@@ -340,6 +393,8 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
   using Lds = FewLds<DP>;
   __shared__ __align__(16) uint8_t lds[kWaves * Lds::kWaveBytes];
   __shared__ float wave_m[TEAM][16], wave_l[TEAM][16];
+  // the nodes' sets, looked up only at the pieces that hold nodes (the waves of a team write the same)
+  __shared__ uint64_t nodes[MODE == kTree ? (TEAM == 1 ? 4 : 1) : 1][MODE == kTree ? kWave : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave_id = __builtin_amdgcn_readfirstlane(tid >> 6), wave = TEAM == 1 ? 0 : wave_id;
@@ -359,7 +414,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
   if (a.err && lane == 0 && wave == 0 && head == 0 && split == 0 && rb == 0 && (s.bad || rows > a.row_blocks * 16 * CT)) atomicAdd(a.err, 1);
   const int row0 = rb * 16 * CT;
   if (row0 >= rows) return;
-  const Span w = span_of(a, s, row0, 16 * CT, 32 * TEAM, split);
+  const Span w = span_of<MODE>(a, s, row0, 16 * CT, 32 * TEAM, split);
 
   const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
@@ -428,6 +483,15 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
     fetch_values();
     ids = page_of(w.tile_lo + 1);
   }
+  Node node;
+  uint64_t* above = nodes[TEAM == 1 && MODE == kTree ? wave_id : 0];
+  const int text = s.len - s.n;
+  if constexpr (MODE == kTree) {
+    node = node_of(a, s);
+    above[lane] = node.above;
+    wave_order();
+    if (a.err && wave == 0 && head == 0 && split == 0 && rb == 0 && __any(node.bad) && lane == 0) atomicAdd(a.err, 1);
+  }
   // (the queries after the first piece's loads: they are a load away, the piece two)
   int lo[CT], seen[CT], t[CT], qhead[CT];
   bool live[CT];
@@ -438,7 +502,12 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
     live[ct] = row < rows;
     t[ct] = live[ct] ? (int)divide((uint32_t)row, a.share) : 0;
     qhead[ct] = head * share + (live[ct] ? row - t[ct] * share : 0);
-    seen_of(a, s, t[ct], live[ct], &lo[ct], &seen[ct]);
+    if constexpr (MODE == kTree) {
+      const int depth = __shfl(node.depth, t[ct] & 63);
+      seen_of_node(a, s, t[ct] < LLVQ_MAX_NODES ? depth : 0, live[ct], &lo[ct], &seen[ct]);
+    } else {
+      seen_of(a, s, t[ct], live[ct], &lo[ct], &seen[ct]);
+    }
     const int64_t at = (int64_t)(s.first + t[ct]) * a.q_token + (int64_t)qhead[ct] * a.q_head;
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
@@ -448,6 +517,8 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
       for (int n = 0; n < NT; ++n) q[n][ct][st] = terms[n];
     }
   }
+
+  auto above_of = [&](int ct) -> uint64_t { return MODE == kTree && live[ct] && t[ct] < LLVQ_MAX_NODES ? above[t[ct] & 63] : 0; };
 
   f32x4 acc[CT][kOut];
   float m[CT], l4[CT][4];
@@ -508,10 +579,12 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       if (!whole) {
+        const uint64_t up = above_of(ct);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) score[ct][u][i] = masked(score[ct][u][i], key_base + u * 16 + 4 * g + i, lo[ct], seen[ct]);
+          for (int i = 0; i < 4; ++i)
+            score[ct][u][i] = masked<MODE>(score[ct][u][i], key_base + u * 16 + 4 * g + i, lo[ct], seen[ct], text, up);
       }
       float top = -INFINITY;
 #pragma unroll
@@ -585,7 +658,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
         const f32x4 x = nonfinite4<KIND>(c, blk, slot, d * 16 + 4 * g);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-          if ((uint32_t)(j - lo[ct]) < (uint32_t)seen[ct]) acc[ct][d] += x;
+          if (sees<MODE>(j, lo[ct], seen[ct], text, above_of(ct))) acc[ct][d] += x;
       }
     }
 
@@ -595,6 +668,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
       const float l = quad_sum((l4[ct][0] + l4[ct][1]) + (l4[ct][2] + l4[ct][3]));
       if (!live[ct]) continue;
       const int64_t row = (int64_t)(s.first + t[ct]) * c.heads * share + qhead[ct];
+      if (MODE == kLse && g == 0) a.lse[row] = log_sum(m[ct], l);
       const int64_t out_at = (int64_t)(s.first + t[ct]) * a.out_token + (int64_t)qhead[ct] * a.out_head;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible key: the row is zero
 #pragma unroll
@@ -631,6 +705,7 @@ __global__ __launch_bounds__(TEAM == 8 ? 512 : 256, TEAM == 8 ? 2 : few_waves(KI
         a.stats[(split * all + row) * 2] = top;
         a.stats[(split * all + row) * 2 + 1] = total;
       }
+      if (MODE == kLse && a.splits == 1 && wave == 0 && g == 0) a.lse[row] = log_sum(top, total);
       if (a.splits == 1 || w.tile_lo < w.tile_hi) {
         for (int d = wave; d < kOut; d += TEAM) {  // the waves share out the channels
           f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -705,7 +780,7 @@ struct alignas(16) Place {
   uint32_t scales[2][kWords];         // keys', values'
 };
 
-template <int KIND, int DP, int NT, int WAVES>
+template <int KIND, int DP, int NT, int WAVES, int MODE>
 __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves)) void k_attn_many(AttnArgs a) {
   using Sh = ManyShape<KIND, DP, NT, WAVES>;
   constexpr int kKeys = Sh::kKeys, kSub = Sh::kSub, kSteps = DP / 16, kOut = Sh::kOutDim / 32, kRows = Sh::kRows;
@@ -719,6 +794,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   __shared__ Where places[2][kKeys];
   // of a tile: keys that are not there, and keys with a group of values whose scale says that they are not finite
   __shared__ uint64_t missing[2], spoilt[2];
+  __shared__ uint64_t nodes[MODE == kTree ? kWave : 1];  // (the waves write the same)
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -738,14 +814,25 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
   if (a.err && tid == 0 && head == 0 && split == 0 && part == 0 && rb == 0 && (s.bad || rows > a.row_blocks * kRows)) atomicAdd(a.err, 1);
   const int row0 = rb * kRows;
   if (row0 >= rows) return;
-  const Span w = span_of(a, s, row0, kRows, kKeys, split);
+  const Span w = span_of<MODE>(a, s, row0, kRows, kKeys, split);
 
   const int row = row0 + wave * 32 + col;
   const bool live = row < rows;
   const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
   const int qhead = head * share + (live ? row - t * share : 0);
   int lo, seen;
-  seen_of(a, s, t, live, &lo, &seen);
+  const int text = s.len - s.n;
+  if constexpr (MODE == kTree) {
+    const Node node = node_of(a, s);
+    nodes[lane] = node.above;
+    wave_order();
+    const int depth = __shfl(node.depth, t & 63);
+    seen_of_node(a, s, t < LLVQ_MAX_NODES ? depth : 0, live, &lo, &seen);
+    if (a.err && wave == 0 && head == 0 && split == 0 && part == 0 && rb == 0 && __any(node.bad) && lane == 0) atomicAdd(a.err, 1);
+  } else {
+    seen_of(a, s, t, live, &lo, &seen);
+  }
+  auto above = [&]() -> uint64_t { return MODE == kTree && live && t < LLVQ_MAX_NODES ? nodes[t & 63] : 0; };
   bf16x8 q[NT][kSteps];
 #pragma unroll
   for (int st = 0; st < kSteps; ++st) {
@@ -758,6 +845,9 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
 #pragma unroll
   for (int i = 0; i < kOut; ++i) acc[i] = f32x16{0.0f};
   float m = -INFINITY, l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (four sums: one chain of additions is slow)
+  // The log-sum is that of p as it is; what divides the output is the sum of p as the second product takes it, rounded
+  constexpr bool kTrue = MODE == kLse && NT == 1;
+  float e4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 
   const int64_t head_off = (int64_t)head * c.block, page_bytes = (int64_t)c.heads * c.block;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
@@ -937,10 +1027,12 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       return vf.v;
     };
     if (!(key_base >= w.all_lo && key_base + kKeys <= w.all_hi && key_base + kKeys <= s.len)) {
+      const uint64_t up = above();
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[u][i] = masked(sc[u][i], key_base + u * 32 + 8 * (i / 4) + 4 * half + (i & 3), lo, seen);
+        for (int i = 0; i < 16; ++i)
+          sc[u][i] = masked<MODE>(sc[u][i], key_base + u * 32 + 8 * (i / 4) + 4 * half + (i & 3), lo, seen, text, up);
     }
     float top = -INFINITY;
 #pragma unroll
@@ -957,6 +1049,10 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
       m = up ? top : m;
 #pragma unroll
       for (int i = 0; i < 4; ++i) l4[i] *= f;
+      if constexpr (kTrue) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e4[i] *= f;
+      }
 #pragma unroll
       for (int i = 0; i < kOut; ++i) acc[i] *= f;
     }
@@ -972,6 +1068,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
         bf16x8 terms[NT];
         split_terms<NT>(x, terms);
         sum_p<NT>(x, terms[0], l4);
+        if constexpr (kTrue) sum_p<2>(x, terms[0], e4);
 #pragma unroll
         for (int n = 0; n < NT; ++n) p[n][u * 2 + h2] = terms[n];
       }
@@ -1008,7 +1105,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
         int slot;
         const uint8_t* blk = block_of_key(c, w, table, head, j, &slot);
         if (!blk) continue;
-        const bool sees = (uint32_t)(j - lo) < (uint32_t)seen;
+        const bool seen_j = sees<MODE>(j, lo, seen, text, above());
 #pragma unroll
         for (int d = 0; d < kOut; ++d)
 #pragma unroll
@@ -1016,22 +1113,29 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
             const f32x4 x = nonfinite4<KIND>(c, blk, slot, part_dim + d * 32 + i4 * 8 + half * 4);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-              if (sees) acc[d][i4 * 4 + n] += x[n];
+              if (seen_j) acc[d][i4 * 4 + n] += x[n];
           }
       }
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 
   const float l = half_sum((l4[0] + l4[1]) + (l4[2] + l4[3]));
+  const float true_l = kTrue ? half_sum((e4[0] + e4[1]) + (e4[2] + e4[3])) : l;
   if (!live) return;
   const int64_t at = (int64_t)(s.first + t) * c.heads * share + qhead;
+  if (MODE == kLse && a.splits == 1 && half == 0 && part == 0) a.lse[at] = log_sum(m, true_l);
   if (a.splits > 1) {
     if (half == 0 && part == 0) {
       const int64_t all = (int64_t)c.tokens * c.heads * share;
       a.stats[(split * all + at) * 2] = m;
-      a.stats[(split * all + at) * 2 + 1] = l;
+      a.stats[(split * all + at) * 2 + 1] = true_l;
     }
     if (w.tile_lo >= w.tile_hi) return;
+    if constexpr (kTrue) {  // the split's mean is of the rounded p, its weight in the join the true sum
+      const float f = l == 0.0f ? 1.0f : true_l / l;
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) acc[d] *= f;
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no visible key: the row is zero
   const int64_t out_at = (int64_t)(s.first + t) * a.out_token + (int64_t)qhead * a.out_head;
@@ -1050,7 +1154,7 @@ __global__ __launch_bounds__(64 * WAVES, (ManyShape<KIND, DP, NT, WAVES>::kWaves
 // many splits.
 constexpr int kMaxSplits = 128;
 
-template <bool F32, int LANES, int WAVES>
+template <bool F32, int LANES, int WAVES, int MODE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int kSide = kWave / LANES;
   const Cache& c = a.c;
@@ -1084,6 +1188,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   }
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) l += __shfl_xor(l, d);
+  if (MODE == kLse && live && lane == 0 && wave % WAVES == 0) a.lse[row] = log_sum(top, l);
 
   const int side = lane / LANES, ch = (lane % LANES) * 4, part = wave % WAVES;
   f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
