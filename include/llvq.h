@@ -483,6 +483,84 @@ int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, cons
  * LLVQ_EINVAL.  Host only. */
 int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab);
 
+/* Check drafted trees against the target's probabilities.  A sequence's rows starts[b] .. starts[b+1]-1 are the nodes of its
+ * tree, as for llvq_attn_tree: node 0 is the last token of the text, the others are drafts that were picked (each certain, as
+ * with no draft probabilities in llvq_draft_verify).  From node c = 0 on, the children of c are taken in the order of
+ * their indexes: child i with the token x is accepted while uniforms[i] * max(S, 0) < w, w = target[c][x] (0 if a refused child of c
+ * has that token, or if it is not positive), S = 1 less the w of the children of c refused before; c becomes i, or i is refused.
+ * After the last child one token is drawn from target[c] without the refused tokens (from target[c] if nothing of it is
+ * left), as llvq_draft_verify draws.  S and the products are in 64 bits.
+ *   target   : [nodes][vocab], LLVQ_X_F32 or LLVQ_X_BF16 (`dtype`): the probabilities after each node.
+ *   starts   : [batch + 1], as in llvq_batch.   tokens, parents : [nodes].   uniforms : [nodes] in [0, 1) (a root's is not read).
+ *   noise    : [batch][vocab], exponential, >= 0 (a NaN or negative one is never drawn).
+ *   width    : 1 .. LLVQ_MAX_NODES; at most width - 1 drafts are accepted, and a node that many steps down is drawn from.
+ *   accepted : [batch]: the number a of accepted drafts.
+ *   path     : [batch][width]: the nodes 0, .., of the accepted path (a + 1 of them), then -1.
+ *   out      : [batch][width]: the a accepted tokens, the drawn one (-1 if no probability is positive: counted), then -1.
+ *              A sequence without nodes: accepted 0, path and out all -1.
+ *   workspace : at least llvq_tree_workspace_bytes(batch, vocab) bytes, 8-byte aligned, contents not kept.
+ *   err_count : nullable; + 1 for a sequence with a node whose parent is no earlier node (never reached), a draft outside the
+ *               vocabulary (never accepted), more than LLVQ_MAX_NODES nodes (those past them are not looked at) or starts that had to be cut.
+ * All arrays contiguous.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_tree_verify(const void* target, int32_t dtype, const int32_t* starts, const int32_t* tokens, const int32_t* parents,
+                     const float* uniforms, const float* noise, int32_t batch, int32_t nodes, int32_t vocab, int32_t width,
+                     int32_t* accepted, int32_t* path, int32_t* out, void* workspace, int64_t workspace_bytes,
+                     int32_t* err_count, void* stream);
+
+/* Bytes of a workspace that serves every call of llvq_tree_verify whose batch and vocabulary are no larger, or LLVQ_EINVAL.
+ * Host only. */
+int64_t llvq_tree_workspace_bytes(int32_t batch, int32_t vocab);
+
+/* ---------------------------------------------------------------------------
+ * Eviction: a sequence that has passed its budget keeps, in every key head, its first and its newest tokens and those that have
+ * received the most attention.  Keys hold their positions (or none), so what stays simply moves together; the
+ * sequence is shorter from then on, and its pages' tail is free.
+ *
+ * Weights: f32 [pages][kv_heads][page_tokens], one number for each cached token and key head, at the token's place.
+ *
+ * Add up what the cached tokens receive from the new ones:
+ *     weights[j] (+)= sum_i exp(scale * q[i][h] . K_j - lse[i][h])
+ * over the rows i and heads h of the key head that see j (the mask of llvq_attn).  Places of the sequence's new tokens start
+ * from zero, whatever they held; the others are added to, or start from zero too if fresh != 0.  A sequence without new tokens is
+ * left as it is.
+ *   q      : [tokens][heads][head_dim] as for llvq_attn.   lse : f32 [tokens][heads], contiguous: what llvq_attn_lse gave for
+ *            these rows with the same scale and mask (rows may be left out: the last 32 of a prompt, say).
+ *   max_chunk : at least the new tokens of any sequence (rows past it are left out and counted).   max_len : about the longest
+ *            length: it decides only how the keys are shared out.
+ *   err_count : nullable; + 1 or more if a page number outside the pool was met (nothing is added there), starts or lengths had to
+ *            be cut, or a sequence has more rows than max_chunk.
+ * Sums are f32, in a fixed order: deterministic.  A key that is not finite makes its own weight NaN, no other.  weights overlaps
+ * none of the inputs.  The limits on heads, tokens and launches are those of llvq_attn.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_kv_weigh(const llvq_kv_desc* d, const void* pool, float* weights, const void* q, int64_t q_token, int64_t q_head,
+                  int32_t dtype, int32_t heads, const float* lse, const llvq_batch* batch, int32_t max_chunk, int32_t max_len,
+                  float scale, int32_t causal, int32_t window, int32_t fresh, int32_t* err_count, void* stream);
+
+/* Choose the tokens that stay.  Of a sequence of m = lens[b] > budget tokens each key head keeps the first `sinks`, the last
+ * `recent`, and of those between the budget - sinks - recent with the largest weights, the lowest position of equals (NaN counts
+ * as the smallest weight).  A sequence of m <= budget keeps all.
+ *   batch  : lens and table; its starts and tokens are not used.
+ *   budget : >= 1; sinks, recent >= 0, sinks + recent <= budget.
+ *   keep   : [batch][kv_heads][budget]: the positions that stay, ascending, then -1.   counts : [batch]: min(m, budget).
+ *   err_count : nullable; + 1 or more for a length that had to be cut or a page number outside the pool (its weights count as NaN).
+ * batch * kv_heads below 2^22.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const llvq_batch* batch, int32_t budget, int32_t sinks,
+                   int32_t recent, int32_t* keep, int32_t* counts, int32_t* err_count, void* stream);
+
+/* Move the tokens that stay together, in place: in sequence b and key head h, the token at place F + keep[b][h][i] goes to
+ * place F + i, codes, scales and (if given) weight, for i < counts[b].  F is 0, or, if the batch has starts, the place of the
+ * sequence's first new token, lens[b] - (starts[b+1] - starts[b]): with lists = 1 and llvq_tree_verify's path the accepted nodes of a
+ * tree move to the end of the text.  Places past the last one written keep what they held.  The sequence's new length is the caller's:
+ * F + counts[b].
+ *   weights : f32 [pages][kv_heads][page_tokens] or NULL.   batch : lens, table and (nullable) starts; its tokens are not used.
+ *   keep    : [batch][lists][width], ascending, each entry at least its index; lists is kv_heads, or 1 for all heads alike.  An
+ *             entry of -1, and one that equals its index, moves nothing.
+ *   counts  : [batch] or NULL (width for all).
+ *   err_count : nullable; + 1 for a (sequence, key head) with an entry that is out of order or past the length, or a page number
+ *             outside the pool (the entry moves nothing), with a count, starts or a length that had to be cut.
+ * No page may belong to two sequences of the call.  batch * kv_heads * (head_dim / 16 + 2) below 2^24.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, const llvq_batch* batch, const int32_t* keep, int32_t lists,
+                 int32_t width, const int32_t* counts, int32_t* err_count, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -61,6 +61,7 @@ def verify(target, starts, tokens, parents, uniforms, noise, width):
                 continue
             x = int(tokens[at + i])
             w = float(target[at + cur][x]) if 0 <= x < vocab and x not in gone else 0.0
+            w = w if w > 0 else 0.0
             if float(uniforms[at + i]) * max(left, 0.0) < w:
                 cur, left, gone = i, 1.0, set()
                 walk.append(i)

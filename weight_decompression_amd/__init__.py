@@ -37,7 +37,8 @@ EXPORTED_SYMBOLS = ("llvq_index_count", "llvq_packed_bytes", "llvq_error_string"
                     "llvq_quantize_noalloc_max_blocks", "llvq_gptq_workspace_bytes", "llvq_gptq_factor",
                     "llvq_gptq_begin", "llvq_gptq_column", "llvq_device_checks", "llvq_kv_pool_bytes",
                     "llvq_kv_write", "llvq_kv_read", "llvq_attn", "llvq_attn_workspace_bytes",
-                    "llvq_draft_verify", "llvq_draft_workspace_bytes", "llvq_attn_lse", "llvq_attn_tree")
+                    "llvq_draft_verify", "llvq_draft_workspace_bytes", "llvq_attn_lse", "llvq_attn_tree",
+                    "llvq_tree_verify", "llvq_tree_workspace_bytes", "llvq_kv_weigh", "llvq_kv_choose", "llvq_kv_keep")
 
 
 class LlvqError(RuntimeError):
@@ -152,6 +153,16 @@ def load_library(path=LIB_PATH):
     lib.llvq_draft_verify.restype = ctypes.c_int
     lib.llvq_draft_workspace_bytes.argtypes = [i32, i32]
     lib.llvq_draft_workspace_bytes.restype = i64
+    lib.llvq_tree_verify.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i64, vp, vp]
+    lib.llvq_tree_verify.restype = ctypes.c_int
+    lib.llvq_tree_workspace_bytes.argtypes = [i32, i32]
+    lib.llvq_tree_workspace_bytes.restype = i64
+    lib.llvq_kv_weigh.argtypes = [kp, vp, vp, vp, i64, i64, i32, i32, vp, bp, i32, i32, f32, i32, i32, i32, vp, vp]
+    lib.llvq_kv_weigh.restype = ctypes.c_int
+    lib.llvq_kv_choose.argtypes = [kp, vp, bp, i32, i32, i32, vp, vp, vp, vp]
+    lib.llvq_kv_choose.restype = ctypes.c_int
+    lib.llvq_kv_keep.argtypes = [kp, vp, vp, bp, vp, i32, i32, vp, vp, vp]
+    lib.llvq_kv_keep.restype = ctypes.c_int
     _libs[path] = lib
     return lib
 
@@ -664,4 +675,131 @@ def draft_verify(target, draft, tokens, uniforms, noise, accepted, out, workspac
         need = draft_workspace_bytes(b, v)
         if size < need:
             raise ValueError(f"{call}: invalid argument, or the workspace is short: it holds {size} bytes, {need} are enough")
+        raise LlvqError(code, call)
+
+
+def tree_workspace_bytes(batch, vocab) -> int:
+    """Bytes of a workspace for every tree_verify call of no more sequences and entries than these."""
+    n = load_library().llvq_tree_workspace_bytes(batch, vocab)
+    if n < 0:
+        raise LlvqError(int(n), "llvq_tree_workspace_bytes")
+    return n
+
+
+def tree_verify(target, starts, tokens, parents, uniforms, noise, accepted, path, out, workspace, err_count=None, stream=None):
+    """Check trees of drafts that were picked: target [nodes][V] (fp32 or bf16 probabilities after each node), starts [B + 1],
+    tokens and parents [nodes] (int32; node 0 of a sequence is the last token of its text), uniforms [nodes] and exponential
+    noise [B][V] (fp32).  accepted [B]; path [B][W]: the accepted nodes from 0 on, then -1; out [B][W]: the accepted tokens, one
+    drawn token, then -1 (int32); at most W - 1 drafts are accepted."""
+    import torch
+    call = "llvq_tree_verify"
+    i32, f32 = torch.int32, torch.float32
+    dtype = target.dtype if isinstance(target, torch.Tensor) else None
+    at = _buffer(target, call, "target")
+    if dtype is not f32 and dtype is not torch.bfloat16:
+        raise TypeError(f"{call}: target must have dtype torch.float32 or torch.bfloat16, got {dtype}")
+    _buffer(noise, call, "noise", f32)
+    _buffer(path, call, "path", i32)
+    if target.dim() != 2 or noise.dim() != 2 or path.dim() != 2:
+        raise ValueError(f"{call}: target, noise and path must be [nodes][vocab], [B][vocab] and [B][width], got "
+                         f"{tuple(target.shape)}, {tuple(noise.shape)} and {tuple(path.shape)}")
+    (n, v), (b, width), device = target.shape, path.shape, target.get_device()
+    each = [_vector(t, call, name, kind, shape, device) for t, name, kind, shape in (
+        (starts, "starts", i32, (b + 1,)), (tokens, "tokens", i32, (n,)), (parents, "parents", i32, (n,)),
+        (uniforms, "uniforms", f32, (n,)), (noise, "noise", f32, (b, v)), (accepted, "accepted", i32, (b,)),
+        (path, "path", i32, (b, width)), (out, "out", i32, (b, width)))]
+    ws, size = _space(workspace, device, call)
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(load_library().llvq_tree_verify, device, stream, at, X_F32 if dtype is f32 else X_BF16, *each[:5], b, n, v, width,
+                   *each[5:], ws, size, err)
+    if code:
+        need = tree_workspace_bytes(b, v)
+        if size < need:
+            raise ValueError(f"{call}: invalid argument, or the workspace is short: it holds {size} bytes, {need} are enough")
+        raise LlvqError(code, call)
+
+
+# ---------------------------------------------------------------------------
+# eviction: what cached tokens have received, which of them stay, their move to the front
+
+def _weights(desc, weights, device, call):
+    import torch
+    return _vector(weights, call, "weights", torch.float32, (desc.pages, desc.kv_heads, desc.page_tokens), device)
+
+
+def _lists(lens, table, starts, device, call):
+    """llvq_batch of lens [B], table [B][max_pages] and, if any, starts [B + 1] (int32)."""
+    import torch
+    i32 = torch.int32
+    _buffer(lens, call, "lens", i32)
+    _buffer(table, call, "table", i32)
+    if starts is not None:
+        _buffer(starts, call, "starts", i32)
+    _one_device(call, device, lens, table, *(() if starts is None else (starts,)))
+    n, shape = lens.shape, table.shape
+    if len(n) != 1 or len(shape) != 2 or shape[0] != n[0] or (starts is not None and starts.shape != (n[0] + 1,)):
+        raise ValueError(f"{call}: lens, table and starts must be [B], [B][max_pages] and [B + 1] or None, got {tuple(n)}, {tuple(shape)} "
+                         f"and {None if starts is None else tuple(starts.shape)}")
+    return Batch(None if starts is None else starts.data_ptr(), lens.data_ptr(), table.data_ptr(), n[0], shape[1], 0)
+
+
+def kv_weigh(desc, pool, weights, q, lse, starts, lens, table, max_chunk, max_len, scale=None, causal=True, window=0, fresh=False,
+             err_count=None, stream=None):
+    """weights[j] += sum of exp(scale * q[i][h] . K_j - lse[i][h]) over the new tokens i and heads h of a key head that see the
+    cached token j.  weights: fp32 [pages][kv_heads][page_tokens], at the tokens' places; those of the new tokens start from
+    zero, with fresh=True those of all.  q: [tokens][heads][head_dim], fp32 or bf16; lse: fp32 [tokens][heads], as attn gives it for
+    the same rows, scale and mask; max_chunk: at least any sequence's new tokens; max_len: about the longest length."""
+    import torch
+    call = "llvq_kv_weigh"
+    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    if heads < 1 or desc.kv_heads < 1 or heads % desc.kv_heads:
+        raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
+    rows = _rows(q, call, "q", heads, desc.head_dim)
+    device = q.get_device()
+    at, batch = _paged(desc, pool, starts, lens, table, q.shape[0], device, call)
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(load_library().llvq_kv_weigh, device, stream, desc, at, _weights(desc, weights, device, call), *rows,
+                   X_F32 if q.dtype is torch.float32 else X_BF16, heads,
+                   _vector(lse, call, "lse", torch.float32, (q.shape[0], heads), device), batch, max_chunk, max_len,
+                   desc.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, 1 if fresh else 0, err)
+    if code:
+        raise LlvqError(code, call)
+
+
+def kv_choose(desc, weights, lens, table, keep, counts, sinks=0, recent=0, err_count=None, stream=None):
+    """keep [B][kv_heads][budget] (int32): the positions that stay of each sequence and key head, ascending, then -1: the first
+    `sinks`, the last `recent`, and between them the largest weights, the lowest position of equals.  counts [B] (int32): how many."""
+    import torch
+    call = "llvq_kv_choose"
+    _buffer(keep, call, "keep", torch.int32)
+    device = keep.get_device()
+    batch = _lists(lens, table, None, device, call)
+    if keep.dim() != 3 or keep.shape[:2] != (batch.batch, desc.kv_heads):
+        raise ValueError(f"{call}: keep must be [{batch.batch}][{desc.kv_heads}][budget], got {tuple(keep.shape)}")
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(load_library().llvq_kv_choose, device, stream, desc, _weights(desc, weights, device, call), batch, keep.shape[2],
+                   sinks, recent, keep.data_ptr(), _vector(counts, call, "counts", torch.int32, (batch.batch,), device), err)
+    if code:
+        raise LlvqError(code, call)
+
+
+def kv_keep(desc, pool, keep, lens, table, counts=None, starts=None, weights=None, err_count=None, stream=None):
+    """Move the cached token at place keep[b][h][i] of sequence b and key head h to place i, in place, for i < counts[b] (all
+    entries without counts; -1 moves nothing).  keep: int32 [B][kv_heads][N], or [B][1][N] for all heads alike, ascending.  With
+    starts [B + 1], places count from the sequence's first new token, so that tree_verify's path[:, None] moves the accepted
+    nodes together.  weights: moved along if given."""
+    import torch
+    call = "llvq_kv_keep"
+    _buffer(keep, call, "keep", torch.int32)
+    device = keep.get_device()
+    at = _buffer(pool, call, "pool", torch.uint8, _pool_nbytes(desc))
+    _one_device(call, device, pool)
+    batch = _lists(lens, table, starts, device, call)
+    if keep.dim() != 3 or keep.shape[0] != batch.batch or keep.shape[1] not in (1, desc.kv_heads):
+        raise ValueError(f"{call}: keep must be [{batch.batch}][{desc.kv_heads} or 1][entries], got {tuple(keep.shape)}")
+    err = None if err_count is None else _count(err_count, device, call)
+    code = _launch(load_library().llvq_kv_keep, device, stream, desc, at,
+                   None if weights is None else _weights(desc, weights, device, call), batch, keep.data_ptr(), keep.shape[1],
+                   keep.shape[2], None if counts is None else _vector(counts, call, "counts", torch.int32, (batch.batch,), device), err)
+    if code:
         raise LlvqError(code, call)

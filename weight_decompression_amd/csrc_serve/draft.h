@@ -31,6 +31,21 @@ struct DraftArgs {
   int32_t batch, drafts, vocab, parts, per;  // per: entries of a part
 };
 
+// Workgroups that share out a row; 1: one of 1024 threads does it all in one launch (one compute unit alone
+// draws no more than 40 GB/s: a row of 32000 takes it 14 us, 16 workgroups 5 us and the second launch 2).
+inline int draft_parts(int32_t batch, int32_t vocab) {
+  if (vocab <= 8192 || batch >= 512) return 1;
+  // about 1024 workgroups in all, each of at least 2048 entries
+  const int64_t most = ((int64_t)vocab + 2047) / 2048, want = (1024 + (batch > 0 ? batch : 1) - 1) / (batch > 0 ? batch : 1);
+  return (int)(want < most ? want : most);
+}
+
+// Bytes of the parts' keys, of any smaller batch too: batch * parts < 1024 + batch where a row is shared out.
+inline int64_t draft_keys_bytes(int32_t batch, int32_t vocab) {
+  const int64_t whole = batch, shared = (int64_t)batch * draft_parts(1, vocab), most = 1023 + whole;
+  return 8 * (shared < most ? shared : most);
+}
+
 template <bool F32>
 __device__ __forceinline__ float prob(const void* p, int64_t at) {
   if constexpr (F32)

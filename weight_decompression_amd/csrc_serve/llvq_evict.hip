@@ -1,6 +1,10 @@
 // Eviction from the paged cache: attention that gives its rows' log-sums, the attention weight that every cached token
 // has received, the choice of the tokens that stay and their move to the front.
 #include "attn_host.h"
+#include "choose.h"
+#include "keep.h"
+#include "serve_host.h"
+#include "weigh.h"
 
 using namespace serve;
 
@@ -10,4 +14,133 @@ LLVQ_API int llvq_attn_lse(const llvq_kv_desc* d, const void* pool, const void* 
                            void* workspace, int64_t workspace_bytes, int32_t* err_count, void* stream) {
   return attn_call<kLse>(d, pool, q, q_token, q_head, out, out_token, out_head, dtype, heads, batch, nullptr, max_chunk, max_len,
                          scale, causal, window, lse, workspace, workspace_bytes, err_count, stream);
+}
+
+namespace {
+
+template <int KIND, int DP>
+int launch_weigh(const WeighArgs& a, bool f32, unsigned grid, hipStream_t s) {
+  if (f32)
+    hipLaunchKernelGGL((k_weigh<KIND, DP, 3>), dim3(grid), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_weigh<KIND, DP, 1>), dim3(grid), dim3(256), 0, s, a);
+  return launch_status();
+}
+template <int KIND>
+int launch_weigh_dim(const WeighArgs& a, bool f32, unsigned grid, hipStream_t s) {
+  switch (padded_dim(a.c.dim)) {
+    case 64: return launch_weigh<KIND, 64>(a, f32, grid, s);
+    case 128: return launch_weigh<KIND, 128>(a, f32, grid, s);
+    default: return launch_weigh<KIND, 256>(a, f32, grid, s);
+  }
+}
+
+// A cache without rows of new tokens: what the choice and the move need of a batch.
+int make_lists(const llvq_kv_desc* d, const void* pool, const llvq_batch* n, Cache* c) {
+  if (!n || n->batch < 0 || n->batch > LLVQ_MAX_SEQS || n->max_pages < 0) return LLVQ_EINVAL;
+  if (n->batch > 0 && (!n->lens || (n->max_pages > 0 && !n->table))) return LLVQ_EINVAL;
+  if (!aligned(pool, 16) || !aligned(n->starts, 4) || !aligned(n->lens, 4) || !aligned(n->table, 4)) return LLVQ_EINVAL;
+  const llvq_batch none = {n->starts, n->lens, n->table, n->batch, n->max_pages, 0};
+  return make_cache(d, pool, &none, c);
+}
+
+}  // namespace
+
+LLVQ_API int llvq_kv_weigh(const llvq_kv_desc* d, const void* pool, float* weights, const void* q, int64_t q_token, int64_t q_head,
+                           int32_t dtype, int32_t heads, const float* lse, const llvq_batch* batch, int32_t max_chunk,
+                           int32_t max_len, float scale, int32_t causal, int32_t window, int32_t fresh, int32_t* err_count,
+                           void* stream) {
+  Cache c;
+  int st = make_cache(d, pool, batch, &c);
+  if (st != LLVQ_OK) return st;
+  st = check_attn(d, heads, batch->tokens, batch->batch, max_chunk, max_len);
+  if (st != LLVQ_OK) return st;
+  if (dtype != LLVQ_X_F32 && dtype != LLVQ_X_BF16) return LLVQ_EINVAL;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!(scale > 0.0f) || !(scale_log2 < INFINITY) || window < 0 || window > kMaxLen) return LLVQ_EINVAL;
+  if (err_count && !aligned(err_count, 4)) return LLVQ_EINVAL;
+  if (c.tokens == 0 || c.batch == 0) return LLVQ_OK;
+  const bool f32 = dtype == LLVQ_X_F32;
+  const int size = f32 ? 4 : 2;
+  if (!q || !lse || !weights || !aligned(q, size) || !aligned(lse, 4) || !aligned(weights, 4)) return LLVQ_EINVAL;
+  if (q_token < 0 || q_head < 0) return LLVQ_EINVAL;
+  WeighArgs a = {};
+  a.c = c;
+  a.q = q;
+  a.lse = lse;
+  a.weights = weights;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.share = make_divider((uint32_t)(heads / d->kv_heads));
+  a.window = window;
+  a.causal = causal != 0;
+  a.fresh = fresh != 0;
+  a.max_rows = max_chunk;
+  a.q_vec = wide(q, q_token, q_head, size);
+  a.scale_log2 = scale_log2;
+  a.err = err_count;
+  const int keys = padded_dim(d->head_dim) <= 128 ? 256 : 128;
+  const int64_t seqs = (int64_t)c.batch * c.heads, most = (1ll << 23) / seqs;
+  int64_t tiles = ((int64_t)max_len + keys - 1) / keys;
+  if (tiles > most) tiles = most < 1 ? 1 : most;
+  a.tiles = (int32_t)tiles;
+  if (seqs * tiles * 256 >= (1ll << 32)) return LLVQ_EINVAL;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const unsigned grid = (unsigned)(seqs * tiles);
+  switch (d->kind) {
+    case LLVQ_KV_BF16: return launch_weigh_dim<LLVQ_KV_BF16>(a, f32, grid, s);
+    case LLVQ_KV_FP8: return launch_weigh_dim<LLVQ_KV_FP8>(a, f32, grid, s);
+    default: return launch_weigh_dim<LLVQ_KV_FP4>(a, f32, grid, s);
+  }
+}
+
+LLVQ_API int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const llvq_batch* batch, int32_t budget, int32_t sinks,
+                            int32_t recent, int32_t* keep, int32_t* counts, int32_t* err_count, void* stream) {
+  Cache c;
+  const int st = make_lists(d, nullptr, batch, &c);
+  if (st != LLVQ_OK) return st;
+  if (budget < 1 || budget > kMaxLen || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget) return LLVQ_EINVAL;
+  if (err_count && !aligned(err_count, 4)) return LLVQ_EINVAL;
+  if (c.batch == 0) return LLVQ_OK;
+  if (!weights || !keep || !counts || !aligned(weights, 4) || !aligned(keep, 4) || !aligned(counts, 4)) return LLVQ_EINVAL;
+  if ((int64_t)c.batch * c.heads * kChooseThreads >= (1ll << 32)) return LLVQ_EINVAL;
+  ChooseArgs a = {};
+  a.c = c;
+  a.weights = weights;
+  a.keep = keep;
+  a.counts = counts;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.err = err_count;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL((k_choose<32>), dim3((unsigned)(c.batch * c.heads)), dim3(kChooseThreads), 0, s, a);
+  return launch_status();
+}
+
+LLVQ_API int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, const llvq_batch* batch, const int32_t* keep,
+                          int32_t lists, int32_t width, const int32_t* counts, int32_t* err_count, void* stream) {
+  Cache c;
+  const int st = make_lists(d, pool, batch, &c);
+  if (st != LLVQ_OK) return st;
+  if ((lists != 1 && lists != d->kv_heads) || width < 0 || width > kMaxLen) return LLVQ_EINVAL;
+  if (!aligned(weights, 4) || !aligned(keep, 4) || !aligned(counts, 4) || (err_count && !aligned(err_count, 4))) return LLVQ_EINVAL;
+  if (c.batch == 0 || width == 0) return LLVQ_OK;
+  if (!pool || !keep) return LLVQ_EINVAL;
+  KeepArgs a = {};
+  a.c = c;
+  a.weights = weights;
+  a.keep = keep;
+  a.counts = counts;
+  a.lists = lists;
+  a.width = width;
+  a.from_new = batch->starts != nullptr;
+  a.err = err_count;
+  a.slices = (c.row + 63) / 64;
+  a.parts = 2 * a.slices + (c.groups > 0) + (weights != nullptr);
+  const int64_t grid = (int64_t)c.batch * c.heads * a.parts;
+  if (grid * kKeepThreads >= (1ll << 32)) return LLVQ_EINVAL;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(k_keep, dim3((unsigned)grid), dim3(kKeepThreads), 0, s, a);
+  return launch_status();
 }

@@ -59,15 +59,6 @@ int kv_call(const llvq_kv_desc* d, const void* pool, const void* k, int64_t k_to
 #undef LLVQ_KV_KIND
 }
 
-// Workgroups that share out a row; 1: one of 1024 threads does it all in one launch (one compute unit alone
-// draws no more than 40 GB/s: a row of 32000 takes it 14 us, 16 workgroups 5 us and the second launch 2).
-int draft_parts(int32_t batch, int32_t vocab) {
-  if (vocab <= 8192 || batch >= 512) return 1;
-  // about 1024 workgroups in all, each of at least 2048 entries
-  const int64_t most = ((int64_t)vocab + 2047) / 2048, want = (1024 + (batch > 0 ? batch : 1) - 1) / (batch > 0 ? batch : 1);
-  return (int)(want < most ? want : most);
-}
-
 template <bool F32>
 int launch_draft(const DraftArgs& a, hipStream_t s) {
   if (a.parts == 1) {
@@ -124,9 +115,7 @@ LLVQ_API int llvq_attn(const llvq_kv_desc* d, const void* pool, const void* q, i
 
 LLVQ_API int64_t llvq_draft_workspace_bytes(int32_t batch, int32_t vocab) {
   if (batch < 0 || batch > LLVQ_MAX_SEQS || vocab < 1) return LLVQ_EINVAL;
-  // the most keys of any smaller batch too: batch * parts < 1024 + batch where a row is shared out
-  const int64_t whole = batch, shared = (int64_t)batch * draft_parts(1, vocab), most = 1023 + whole;
-  return 8 * (shared < most ? shared : most);
+  return draft_keys_bytes(batch, vocab);
 }
 
 LLVQ_API int llvq_draft_verify(const void* target, const void* draft, int32_t dtype, const int32_t* tokens,
