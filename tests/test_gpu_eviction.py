@@ -119,12 +119,13 @@ def test_weights(kind, kv_heads, share, dim, page, new, lens, window, causal, dt
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 256])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_weights_of_every_type_and_width(kind, dim, dtype):
-    su = Setup(kind, 2, dim, 16, [45, 1], [300, 290], seed=dim)
+@pytest.mark.parametrize("new", [5, 10, 45])               # rows of a key head: up to 16, up to 32, more
+def test_weights_of_every_type_and_width(kind, dim, dtype, new):
+    su = Setup(kind, 2, dim, 16, [new, 1], [300, 290], seed=dim)
     caches = su.fill()
-    wide = torch.zeros(46, 7, dim + 3, device="cuda", dtype=dtype)              # rows that start off 16 bytes
+    wide = torch.zeros(new + 1, 7, dim + 3, device="cuda", dtype=dtype)         # rows that start off 16 bytes
     q = wide[:, 1:7, 2:dim + 2]
-    q.copy_(dev(1.5 * su.rng.randn(46, 6, dim).astype(np.float32)))
+    q.copy_(dev(1.5 * su.rng.randn(new + 1, 6, dim).astype(np.float32)))
     lse = true_lse(su, caches, f64(q), 0, True)
     before = np.zeros((su.pages, 2, 16), np.float32)
     weights = dev(before)

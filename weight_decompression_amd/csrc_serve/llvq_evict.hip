@@ -18,20 +18,54 @@ LLVQ_API int llvq_attn_lse(const llvq_kv_desc* d, const void* pool, const void* 
 
 namespace {
 
-template <int KIND, int DP>
-int launch_weigh(const WeighArgs& a, bool f32, unsigned grid, hipStream_t s) {
-  if (f32)
-    hipLaunchKernelGGL((k_weigh<KIND, DP, 3>), dim3(grid), dim3(256), 0, s, a);
+// Row tiles of 16 that the kernel for few rows takes (0: the kernel for many), workgroups that share out a sequence's keys.
+struct WeighCut {
+  int tiles, groups;
+};
+
+inline WeighCut weigh_cut(int64_t rows, int dim, bool f32, int64_t seqs, int32_t max_len) {
+  WeighCut w;
+  w.tiles = rows <= 16 ? 1 : rows <= 32 && !(f32 && dim > 128) ? 2 : 0;
+  const int64_t pieces = ((int64_t)max_len + 127) / 128;  // of four waves
+  if (w.tiles) {
+    // up to 16 pieces a wave, fewer while that leaves places on the chip empty
+    int64_t each = pieces * seqs / 2048;
+    each = each < 1 ? 1 : each > 16 ? 16 : each;
+    w.groups = (int)((pieces + each - 1) / each);
+  } else {
+    w.groups = (int)(dim <= 128 ? (pieces + 1) / 2 : pieces);
+  }
+  // (a launch has fewer than 2^32 threads)
+  const int64_t most = ((1ll << 24) - 1) / seqs;
+  if (w.groups > most) w.groups = (int)(most < 1 ? 1 : most);
+  return w;
+}
+
+template <int KIND, int DP, int NT>
+int launch_weigh_nt(const WeighArgs& a, int tiles, hipStream_t s) {
+  const dim3 grid((unsigned)a.units);
+  if constexpr (NT == 1 || DP <= 128) {
+    if (tiles == 2) {
+      hipLaunchKernelGGL((k_weigh_few<KIND, DP, NT, 2>), grid, dim3(256), 0, s, a);
+      return launch_status();
+    }
+  }
+  if (tiles == 1)
+    hipLaunchKernelGGL((k_weigh_few<KIND, DP, NT, 1>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_weigh<KIND, DP, 1>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_weigh_many<KIND, DP, NT>), grid, dim3(256), 0, s, a);
   return launch_status();
 }
+template <int KIND, int DP>
+int launch_weigh(const WeighArgs& a, bool f32, int tiles, hipStream_t s) {
+  return f32 ? launch_weigh_nt<KIND, DP, 3>(a, tiles, s) : launch_weigh_nt<KIND, DP, 1>(a, tiles, s);
+}
 template <int KIND>
-int launch_weigh_dim(const WeighArgs& a, bool f32, unsigned grid, hipStream_t s) {
+int launch_weigh_dim(const WeighArgs& a, bool f32, int tiles, hipStream_t s) {
   switch (padded_dim(a.c.dim)) {
-    case 64: return launch_weigh<KIND, 64>(a, f32, grid, s);
-    case 128: return launch_weigh<KIND, 128>(a, f32, grid, s);
-    default: return launch_weigh<KIND, 256>(a, f32, grid, s);
+    case 64: return launch_weigh<KIND, 64>(a, f32, tiles, s);
+    case 128: return launch_weigh<KIND, 128>(a, f32, tiles, s);
+    default: return launch_weigh<KIND, 256>(a, f32, tiles, s);
   }
 }
 
@@ -79,18 +113,16 @@ LLVQ_API int llvq_kv_weigh(const llvq_kv_desc* d, const void* pool, float* weigh
   a.q_vec = wide(q, q_token, q_head, size);
   a.scale_log2 = scale_log2;
   a.err = err_count;
-  const int keys = padded_dim(d->head_dim) <= 128 ? 256 : 128;
-  const int64_t seqs = (int64_t)c.batch * c.heads, most = (1ll << 23) / seqs;
-  int64_t tiles = ((int64_t)max_len + keys - 1) / keys;
-  if (tiles > most) tiles = most < 1 ? 1 : most;
-  a.tiles = (int32_t)tiles;
-  if (seqs * tiles * 256 >= (1ll << 32)) return LLVQ_EINVAL;
+  const int64_t seqs = (int64_t)c.batch * c.heads;
+  if (seqs >= 1 << 24) return LLVQ_EINVAL;
+  const WeighCut cut = weigh_cut((int64_t)max_chunk * a.share.by, padded_dim(d->head_dim), f32, seqs, max_len);
+  a.tiles = cut.groups;
+  a.units = (int32_t)(seqs * cut.groups);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const unsigned grid = (unsigned)(seqs * tiles);
   switch (d->kind) {
-    case LLVQ_KV_BF16: return launch_weigh_dim<LLVQ_KV_BF16>(a, f32, grid, s);
-    case LLVQ_KV_FP8: return launch_weigh_dim<LLVQ_KV_FP8>(a, f32, grid, s);
-    default: return launch_weigh_dim<LLVQ_KV_FP4>(a, f32, grid, s);
+    case LLVQ_KV_BF16: return launch_weigh_dim<LLVQ_KV_BF16>(a, f32, cut.tiles, s);
+    case LLVQ_KV_FP8: return launch_weigh_dim<LLVQ_KV_FP8>(a, f32, cut.tiles, s);
+    default: return launch_weigh_dim<LLVQ_KV_FP4>(a, f32, cut.tiles, s);
   }
 }
 

@@ -28,37 +28,263 @@ struct WeighArgs {
   float* weights;    // [pages][heads][page]
   int64_t q_token, q_head;
   Divider share;
-  int32_t tiles;     // workgroups of keys of a sequence; a longer one takes turns
+  int32_t tiles;     // workgroups that share out the keys of a sequence
+  int32_t units;     // of all sequences and key heads
   int32_t window, causal, fresh, max_rows, q_vec;
   float scale_log2;
   int32_t* err;
 };
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kNoRow = -0x7fffffff;  // the position of a row that is none
+
+// 8 channels of a query row as they are loaded, and as NT bf16 terms.
+template <bool F32>
+struct Raw8 {
+  u32x4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> raw_query(const WeighArgs& a, int64_t at, int ch, bool live) {
+  Raw8<F32> r;
+  r.w[0] = u32x4{0, 0, 0, 0};
+  if constexpr (F32) r.w[1] = r.w[0];
+  if (!live || ch >= a.c.dim) return r;
+  if (a.q_vec) {
+    const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.q) + (at + ch) * (F32 ? 4 : 2));
+    r.w[0] = from[0];
+    if constexpr (F32) r.w[1] = from[1];
+  } else if constexpr (F32) {
+    const uint32_t* from = static_cast<const uint32_t*>(a.q) + at + ch;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i / 4][i & 3] = from[i];
+  } else {
+    const uint16_t* from = static_cast<const uint16_t*>(a.q) + at + ch;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[0][i] = from[2 * i] | (uint32_t)from[2 * i + 1] << 16;
+  }
+  return r;
+}
+template <int NT>
+__device__ __forceinline__ void query_terms(const Raw8<NT == 3>& r, bf16x8* terms) {
+  if constexpr (NT == 1) {
+    terms[0] = __builtin_bit_cast(bf16x8, r.w[0]);
+  } else {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i / 4][i & 3]);
+    split_terms<NT>(x, terms);
+  }
+}
+
+// The channels that a lane holds in step st of a product, lanes of `part` (of 64 / width parts) side by side.  A lane's 16 raw
+// bytes are 1, 2 or 4 steps of 8 channels.
+template <int KIND, int PARTS>
+__device__ __forceinline__ constexpr int channel_of(int st, int part) {
+  constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;
+  return ((st / kOf) * PARTS + part) * 8 * kOf + st % kOf * 8;
+}
+
+// Where a key of a sequence lies.  The page number is loaded without waiting for the sequence's length.
+template <int KIND, int DP>
+struct KeyPlace {
+  static constexpr int kWords = KIND == LLVQ_KV_BF16 ? 1 : DP <= 128 ? 1 : 2;  // of four scale bytes
+  const uint8_t* blk;  // null if it has no place
+  float* weight;
+  int slot;
+  __device__ __forceinline__ void find(const WeighArgs& a, int j, int len, int32_t id, int head, bool* lost) {
+    const Cache& c = a.c;
+    const bool in = j < len, ok = in && id >= 0 && id < c.pages;
+    *lost |= in && !ok;
+    slot = j - (int)(divide((uint32_t)j, c.page) * c.page.by);
+    const int64_t at = (int64_t)(ok ? id : 0) * c.heads + head;
+    blk = ok ? c.pool + at * c.block : nullptr;
+    weight = ok ? a.weights + at * c.page.by + slot : nullptr;
+  }
+  __device__ __forceinline__ u32x4 chunk(const Cache& c, int ch) const {
+    return blk && ch * 16 < c.row ? *reinterpret_cast<const u32x4*>(blk + slot * c.row + ch * 16) : u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void scales(const Cache& c, uint32_t* words) const {
+#pragma unroll
+    for (int n = 0; n < kWords; ++n) {
+      words[n] = 0x7f7f7f7fu;
+      if (KIND != LLVQ_KV_BF16 && blk) words[n] = scale_word(blk + c.ks_off + slot * c.groups, c.groups, n);
+    }
+  }
+  static __device__ __forceinline__ uint32_t scale_of(const uint32_t* words, int group) {
+    if constexpr (KIND == LLVQ_KV_BF16) return 127;
+    const uint32_t word = kWords == 2 && group >= 4 ? words[kWords - 1] : words[0];
+    return word >> (8 * (group & 3)) & 255;
+  }
+};
+__device__ __forceinline__ int32_t page_id(const Cache& c, const int32_t* table, int j) {
+  const uint32_t page = divide((uint32_t)j, c.page);
+  return page < (uint32_t)c.max_pages ? table[page] : -1;
+}
+
+// Few rows: up to 16 RT of a (sequence, key head).  Every wave runs by itself over pieces of 32 keys, the codes, scales and
+// weights of the next piece and the page numbers of the one after it under way; the rows are operands in registers for the
+// whole call.  16x16x32 instructions: a lane holds one key of 16 and 4 rows, four lanes of a key read 64 consecutive bytes.
+template <int KIND, int DP, int NT, int RT>
+__global__ __launch_bounds__(256) void k_weigh_few(WeighArgs a) {
+  constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;  // steps of a 16-byte chunk
+  constexpr int kChunks = (DP / 32 + kOf - 1) / kOf, kSteps = kChunks * kOf;   // (e2m1, 64 wide: half the lanes have zeros)
+  using Key = KeyPlace<KIND, DP>;
+  const Cache& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  int id = blockIdx.x;
+  const int head = id % c.heads;
+  id /= c.heads;
+  const int b = id / a.tiles, tile = id % a.tiles;
+  const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  const int stride = a.tiles * 4;
+  int piece = tile * 4 + wave;
+  // (a piece's keys stay below 2^31: a sequence has up to 2^30)
+  int32_t ids[2], next_ids[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) ids[u] = page_id(c, table, piece * 32 + u * 16 + col);
+  const Seq s = sequence(c, b);
+  const int share = (int)a.share.by, tokens = min(s.n, a.max_rows), rows = tokens * share, text = s.len - s.n, heads = c.heads * share;
+  if (a.err && tid == 0 && head == 0 && tile == 0 && (s.bad || s.n > a.max_rows)) atomicAdd(a.err, 1);
+  if (s.n == 0) return;
+  // Without a fresh start, text before every row's window stays as it is
+  const int low = !a.fresh && a.window > 0 ? max(text - a.window + 1, 0) : 0;
+  if (low >= 32) {
+    const int skip = low / 32;
+    if (piece < skip) piece += (skip - piece + stride - 1) / stride * stride;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) ids[u] = page_id(c, table, piece * 32 + u * 16 + col);
+  }
+  bool lost = false;
+  Key key[2];
+  u32x4 raw[2][kChunks];
+  uint32_t words[2][Key::kWords];
+  float old[2];
+  auto fetch = [&](int p) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = p * 32 + u * 16 + col;
+      key[u].find(a, j, s.len, ids[u], head, &lost);
+#pragma unroll
+      for (int m = 0; m < kChunks; ++m) raw[u][m] = key[u].chunk(c, 4 * m + g);
+      key[u].scales(c, words[u]);
+      old[u] = key[u].weight && !a.fresh && j < text ? *key[u].weight : 0.0f;
+    }
+  };
+  const int pieces = (s.len + 31) / 32;
+  if (piece < pieces) {
+    fetch(piece);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) next_ids[u] = page_id(c, table, min(piece + stride, pieces) * 32 + u * 16 + col);
+  }
+  // the rows: as operands by lane (row col), log-sums and positions by register (row 4 g + i)
+  bf16x8 q[NT][RT][kSteps];
+  float lse[RT][4];
+  int pos[RT][4];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = rt * 16 + col;
+    const bool live = row < rows;
+    const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
+    const int64_t at = (int64_t)(s.first + t) * a.q_token + (int64_t)(head * share + (live ? row - t * share : 0)) * a.q_head;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      bf16x8 terms[NT];
+      query_terms<NT>(raw_query<NT == 3>(a, at, channel_of<KIND, 4>(st, g), live), terms);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) q[n][rt][st] = terms[n];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = rt * 16 + 4 * g + i;
+      const int tt = r < rows ? (int)divide((uint32_t)r, a.share) : 0;
+      lse[rt][i] = r < rows ? a.lse[(int64_t)(s.first + tt) * heads + head * share + (r - tt * share)] * kLog2e : 0.0f;
+      pos[rt][i] = r < rows ? text + tt : kNoRow;
+    }
+  }
+  const bool full = rows == 16 * RT;
+  while (piece < pieces) {
+    const int next = piece + stride;
+    bf16x8 k[2][kSteps];
+    float* to[2];
+    float was[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      nan_scales<KIND, Key::kWords>(words[u]);
+#pragma unroll
+      for (int m = 0; m < kChunks; ++m) {
+        u32x4 o[kOf];
+        expand<KIND>(raw[u][m], Key::scale_of(words[u], KIND == LLVQ_KV_FP8 ? 2 * m + (g >> 1) : 4 * m + g), o);
+#pragma unroll
+        for (int e = 0; e < kOf; ++e)
+          k[u][m * kOf + e] = __builtin_bit_cast(bf16x8, o[e]);
+      }
+      to[u] = key[u].weight;
+      was[u] = old[u];
+    }
+    if (next < pieces) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) ids[u] = next_ids[u];
+      fetch(next);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) next_ids[u] = page_id(c, table, min(next + stride, pieces) * 32 + u * 16 + col);
+    }
+    // whether every row sees every key
+    const bool whole = full && (!a.causal || piece * 32 + 31 <= text) && (a.window == 0 || piece * 32 > text + tokens - 1 - a.window);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = piece * 32 + u * 16 + col;
+      float sum = 0.0f;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (int n = NT - 1; n >= 0; --n) sc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[n][rt][st], k[u][st], sc, 0, 0, 0);
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], a.scale_log2, -lse[rt][i]));
+          if (!whole) {
+            const bool see = pos[rt][i] != kNoRow && (!a.causal || j <= pos[rt][i]) && (a.window == 0 || j > pos[rt][i] - a.window);
+            p[i] = see ? p[i] : 0.0f;
+          }
+        }
+        sum += (p[0] + p[1]) + (p[2] + p[3]);
+      }
+      sum = quad_sum(sum);
+      if (g == 0 && to[u]) *to[u] = was[u] + sum;
+    }
+    piece = next;
+  }
+  if (a.err && lost) atomicAdd(a.err, 1);
+}
+
+// Many rows.  A workgroup's four waves hold 64 keys each (32 of wide heads) and walk the rows that see them, in blocks that the
+// workgroup stages in LDS: a block's rows are loaded while the one before is worked on, and written to the other buffer after it.
 template <int DP, int NT>
 struct WeighShape {
   static constexpr int kTiles = DP <= 128 ? 2 : 1;     // of 32 keys that a wave holds
   static constexpr int kKeys = 4 * 32 * kTiles;        // of a workgroup
+  static constexpr int kSub = NT == 1 ? 2 : 1;         // pieces of 32 rows of a block
+  static constexpr int kRows = 32 * kSub;
   static constexpr int kRow = DP * 2 + 16;             // bytes of a row in LDS, padded as attention's keys are
 };
 
-// The channels of step st that lanes of `half` hold.
-template <int KIND>
-__device__ __forceinline__ constexpr int channel_of(int st, int half) {
-  return KIND == LLVQ_KV_BF16 ? 16 * st + 8 * half : KIND == LLVQ_KV_FP8 ? 32 * (st / 2) + 16 * half + 8 * (st & 1) : 64 * (st / 4) + 32 * half + 8 * (st & 3);
-}
-
 template <int KIND, int DP, int NT>
-__global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh(WeighArgs a) {
+__global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_many(WeighArgs a) {
   using Sh = WeighShape<DP, NT>;
-  constexpr int kSteps = DP / 16, kTiles = Sh::kTiles;
+  using Key = KeyPlace<KIND, DP>;
+  constexpr int kSteps = DP / 16, kTiles = Sh::kTiles, kSub = Sh::kSub, kRows = Sh::kRows;
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;  // steps of a 16-byte chunk
   constexpr int kChunks = kSteps / kOf;                                        // chunks of a lane and key
-  constexpr int kWords = KIND == LLVQ_KV_BF16 ? 1 : DP <= 128 ? 1 : 2;
-  constexpr int kParts = 32 * (DP / 8) / 256;                                  // 8-channel parts of a row block a thread stages
+  constexpr int kParts = kRows * (DP / 8) / 256;                               // 8-channel parts of a block that a thread stages
   const Cache& c = a.c;
-  __shared__ __align__(16) uint8_t rows_lds[2][NT][32 * Sh::kRow];
-  __shared__ float lse_lds[2][32];
-  __shared__ int pos_lds[2][32];  // a row's position, or far below any for none
+  __shared__ __align__(16) uint8_t rows_lds[2][NT][kRows * Sh::kRow];
+  __shared__ __align__(16) float lse_lds[2][kRows];
+  __shared__ __align__(16) int pos_lds[2][kRows];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -68,140 +294,136 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh(Wei
   id /= c.heads;
   const int b = id / a.tiles, tile0 = id % a.tiles;
   const Seq s = sequence(c, b);
-  const int share = (int)a.share.by, rows = min(s.n, a.max_rows) * share, text = s.len - s.n, heads = c.heads * share;
+  const int share = (int)a.share.by, tokens = min(s.n, a.max_rows), rows = tokens * share, text = s.len - s.n, heads = c.heads * share;
   if (a.err && tid == 0 && head == 0 && tile0 == 0 && (s.bad || s.n > a.max_rows)) atomicAdd(a.err, 1);
   if (s.n == 0) return;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
   bool lost = false;
 
   for (int tile = tile0; (int64_t)tile * Sh::kKeys < s.len; tile += a.tiles) {
-    const int key0 = tile * Sh::kKeys + wave * 32 * kTiles;
-    // the rows that see any key of the workgroup's: tokens [t0, t1)
-    const int first_key = tile * Sh::kKeys, last_key = min(first_key + Sh::kKeys, s.len) - 1;
+    const int first_key = tile * Sh::kKeys, key0 = first_key + wave * 32 * kTiles;
+    const int last_key = min(first_key + Sh::kKeys, s.len) - 1;
+    // the tokens that see any key of the workgroup's: [t0, t1)
     const int t0 = a.causal ? max(first_key - text, 0) : 0;
     const int64_t reach = (int64_t)last_key - text + a.window;
-    const int t1 = a.window > 0 ? (int)min((int64_t)min(s.n, a.max_rows), max(reach, (int64_t)0)) : min(s.n, a.max_rows);
-    const int block0 = t0 * share / 32, block1 = t1 > t0 ? (t1 * share + 31) / 32 : block0;
+    const int t1 = a.window > 0 ? (int)min((int64_t)tokens, max(reach, (int64_t)0)) : tokens;
+    const int block0 = t0 * share / kRows, block1 = t1 > t0 ? (int)(((int64_t)t1 * share + kRows - 1) / kRows) : block0;
+    if (block0 >= block1 && !a.fresh && last_key < text) continue;  // nothing is added
 
-    // the keys
-    float* at[kTiles];
-    bf16x8 k[kTiles][kSteps];
-    float sum[kTiles];
-#pragma unroll
-    for (int u = 0; u < kTiles; ++u) {
-      const int j = key0 + u * 32 + col;
-      const uint32_t page = divide((uint32_t)j, c.page);
-      const int32_t pid = j < s.len ? table[page] : -1;
-      const bool ok = pid >= 0 && pid < c.pages;
-      lost |= j < s.len && !ok;
-      const int slot = j - (int)(page * c.page.by);
-      at[u] = ok ? a.weights + ((int64_t)pid * c.heads + head) * c.page.by + slot : nullptr;
-      const uint8_t* blk = c.pool + (ok ? ((int64_t)pid * c.heads + head) * c.block : 0);
-      const uint8_t* row = blk + (ok ? slot * c.row : 0);
-      u32x4 raw[kChunks];
-      uint32_t words[kWords];
-#pragma unroll
-      for (int m = 0; m < kChunks; ++m) {
-        const int ch = 2 * m + half;
-        raw[m] = u32x4{0, 0, 0, 0};
-        if (ok && ch * 16 < c.row) raw[m] = *reinterpret_cast<const u32x4*>(row + ch * 16);
-      }
-#pragma unroll
-      for (int n = 0; n < kWords; ++n) {
-        words[n] = 0x7f7f7f7fu;
-        if (KIND != LLVQ_KV_BF16 && ok) words[n] = scale_word(blk + c.ks_off + slot * c.groups, c.groups, n);
-      }
-      nan_scales<KIND, kWords>(words);
-#pragma unroll
-      for (int m = 0; m < kChunks; ++m) {
-        const int group = channel_of<KIND>(m * kOf, half) / 32;
-        const uint32_t sb = KIND == LLVQ_KV_BF16 ? 127 : words[group / 4 % kWords] >> (8 * (group % 4)) & 255;
-        u32x4 o[kOf];
-        expand<KIND>(raw[m], sb, o);
-#pragma unroll
-        for (int e = 0; e < kOf; ++e) k[u][m * kOf + e] = __builtin_bit_cast(bf16x8, o[e]);
-      }
-      sum[u] = 0.0f;
-    }
-
-    // a block of rows into LDS
-    auto stage = [&](int block, int buffer) {
+    Raw8<NT == 3> staged[kParts];
+    float staged_lse = 0.0f;
+    int staged_pos = kNoRow;
+    auto load = [&](int block) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         const int part = i * 256 + tid, r = part / (DP / 8), ch = part % (DP / 8) * 8;
-        const int row = block * 32 + r;
+        const int row = block * kRows + r;
         const bool live = row < rows;
         const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
         const int64_t from = (int64_t)(s.first + t) * a.q_token + (int64_t)(head * share + (live ? row - t * share : 0)) * a.q_head;
-        float x[8];
+        staged[i] = raw_query<NT == 3>(a, from, ch, live);
+      }
+      if (tid < kRows) {
+        const int row = block * kRows + tid;
+        const bool live = row < rows;
+        const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
+        staged_lse = live ? a.lse[(int64_t)(s.first + t) * heads + head * share + (row - t * share)] : 0.0f;
+        staged_pos = live ? text + t : kNoRow;
+      }
+    };
+    auto write = [&](int buffer) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-        if (live && ch < c.dim) {
-          if (a.q_vec)
-            load8<NT == 3, true>(a.q, from + ch, x);
-          else
-            load8<NT == 3, false>(a.q, from + ch, x);
-        }
+      for (int i = 0; i < kParts; ++i) {
+        const int part = i * 256 + tid, r = part / (DP / 8), ch = part % (DP / 8) * 8;
         bf16x8 terms[NT];
-        split_terms<NT>(x, terms);
+        query_terms<NT>(staged[i], terms);
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<bf16x8*>(&rows_lds[buffer][n][r * Sh::kRow + ch * 2]) = terms[n];
       }
-      if (tid < 32) {
-        const int row = block * 32 + tid;
-        const bool live = row < rows;
-        const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
-        const float l = live ? a.lse[(int64_t)(s.first + t) * heads + head * share + (row - t * share)] : 0.0f;
-        lse_lds[buffer][tid] = l * 1.4426950408889634f;
-        pos_lds[buffer][tid] = live ? text + t : -0x7fffffff;
+      if (tid < kRows) {
+        lse_lds[buffer][tid] = staged_lse * kLog2e;
+        pos_lds[buffer][tid] = staged_pos;
       }
     };
 
+    if (block0 < block1) load(block0);
+    // the keys
+    float* to[kTiles];
+    float old[kTiles], sum[kTiles];
+    bf16x8 k[kTiles][kSteps];
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u) {
+      const int j = key0 + u * 32 + col;
+      Key key;
+      key.find(a, j, s.len, page_id(c, table, j), head, &lost);
+      u32x4 raw[kChunks];
+      uint32_t words[Key::kWords];
+#pragma unroll
+      for (int m = 0; m < kChunks; ++m) raw[m] = key.chunk(c, 2 * m + half);
+      key.scales(c, words);
+      to[u] = key.weight;
+      old[u] = key.weight && !a.fresh && j < text ? *key.weight : 0.0f;
+      sum[u] = 0.0f;
+      nan_scales<KIND, Key::kWords>(words);
+#pragma unroll
+      for (int m = 0; m < kChunks; ++m) {
+        u32x4 o[kOf];
+        expand<KIND>(raw[m], Key::scale_of(words, KIND == LLVQ_KV_FP8 ? m : 2 * m + half), o);
+#pragma unroll
+        for (int e = 0; e < kOf; ++e) k[u][m * kOf + e] = __builtin_bit_cast(bf16x8, o[e]);
+      }
+    }
     __syncthreads();  // (the tile before has been worked through)
-    if (block0 < block1) stage(block0, 0);
+    if (block0 < block1) write(0);
     for (int block = block0; block < block1; ++block) {
       const int buffer = (block - block0) & 1;
       __syncthreads();
-      if (block + 1 < block1) stage(block + 1, buffer ^ 1);
-      const int p0 = pos_lds[buffer][0], p1 = pos_lds[buffer][31];
-      // whether every row sees every key of the wave's
-      const int hi = key0 + 32 * kTiles - 1;
-      const bool whole = p1 >= text && (!a.causal || hi <= p0) && (a.window == 0 || key0 > p1 - a.window);
+      if (block + 1 < block1) load(block + 1);
 #pragma unroll
-      for (int u = 0; u < kTiles; ++u) {
-        f32x16 sc = {0.0f};
+      for (int sub = 0; sub < kSub; ++sub) {
+        const int p0 = __builtin_amdgcn_readfirstlane(pos_lds[buffer][sub * 32]), p1 = __builtin_amdgcn_readfirstlane(pos_lds[buffer][sub * 32 + 31]);
+        // whether every row sees every key of the wave's
+        const bool whole = p1 >= text && (!a.causal || key0 + 32 * kTiles - 1 <= p0) && (a.window == 0 || key0 > p1 - a.window);
+        f32x16 sc[kTiles];
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) sc[u] = f32x16{0.0f};
 #pragma unroll
         for (int st = 0; st < kSteps; ++st)
 #pragma unroll
           for (int n = NT - 1; n >= 0; --n) {
-            const bf16x8 qf = *reinterpret_cast<const bf16x8*>(&rows_lds[buffer][n][col * Sh::kRow + channel_of<KIND>(st, half) * 2]);
-            sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, k[u][st], sc, 0, 0, 0);
+            const bf16x8 qf = *reinterpret_cast<const bf16x8*>(
+                &rows_lds[buffer][n][(sub * 32 + col) * Sh::kRow + channel_of<KIND, 2>(st, half) * 2]);
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, k[u][st], sc[u], 0, 0, 0);
           }
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const int j = key0 + u * 32 + col;
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[buffer][i4 * 8 + half * 4]);
+        for (int u = 0; u < kTiles; ++u) {
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const int j = key0 + u * 32 + col;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float p = __builtin_amdgcn_exp2f(fmaf(sc[i4 * 4 + i], a.scale_log2, -l[i]));
-            if (!whole) {
-              const int pos = pos_lds[buffer][i4 * 8 + half * 4 + i];
-              const bool see = pos != -0x7fffffff && (!a.causal || j <= pos) && (a.window == 0 || j > pos - a.window);
-              p = see ? p : 0.0f;
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[buffer][sub * 32 + i4 * 8 + half * 4]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float p = __builtin_amdgcn_exp2f(fmaf(sc[u][i4 * 4 + i], a.scale_log2, -l[i]));
+              if (!whole) {
+                const int pos = pos_lds[buffer][sub * 32 + i4 * 8 + half * 4 + i];
+                const bool see = pos != kNoRow && (!a.causal || j <= pos) && (a.window == 0 || j > pos - a.window);
+                p = see ? p : 0.0f;
+              }
+              part[i] += p;
             }
-            part[i] += p;
           }
+          sum[u] += (part[0] + part[1]) + (part[2] + part[3]);
         }
-        sum[u] += (part[0] + part[1]) + (part[2] + part[3]);
       }
+      if (block + 1 < block1) write(buffer ^ 1);
     }
     // what the new tokens' places held is of earlier tokens
 #pragma unroll
     for (int u = 0; u < kTiles; ++u) {
       const float got = half_sum(sum[u]);
-      const int j = key0 + u * 32 + col;
-      if (half == 0 && at[u]) *at[u] = (a.fresh || j >= text ? 0.0f : *at[u]) + got;
+      if (half == 0 && to[u]) *to[u] = old[u] + got;
     }
   }
   if (a.err && lost) atomicAdd(a.err, 1);
