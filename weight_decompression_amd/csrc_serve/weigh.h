@@ -16,6 +16,8 @@
 // each key: the matrix instructions and the exponentials, a fused multiply-add, an exp and an add a score, share the time.
 #pragma once
 
+#include <type_traits>
+
 #include "attn.h"
 #include "serve_common.h"
 
@@ -36,7 +38,19 @@ struct WeighArgs {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kNoRow = -0x7fffffff;  // the position of a row that is none
+
+// The keys that a row at a position sees: lo, .., lo + many - 1 (none where the row is none).
+struct Seen {
+  int lo;
+  uint32_t many;
+  __device__ __forceinline__ Seen(const WeighArgs& a, int pos, bool live) {
+    lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int hi = a.causal ? pos + 1 : 0x7fffffff;
+    many = live ? (uint32_t)max(hi - lo, 0) : 0;
+  }
+  __device__ __forceinline__ Seen(int lo_, int many_) : lo(lo_), many((uint32_t)many_) {}
+  __device__ __forceinline__ bool holds(int j) const { return (uint32_t)(j - lo) < many; }
+};
 
 // 8 channels of a query row as they are loaded, and as NT bf16 terms.
 template <bool F32>
@@ -181,7 +195,7 @@ __global__ __launch_bounds__(256) void k_weigh_few(WeighArgs a) {
   // the rows: as operands by lane (row col), log-sums and positions by register (row 4 g + i)
   bf16x8 q[NT][RT][kSteps];
   float lse[RT][4];
-  int pos[RT][4];
+  int lo[RT][4], many[RT][4];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = rt * 16 + col;
@@ -200,7 +214,9 @@ __global__ __launch_bounds__(256) void k_weigh_few(WeighArgs a) {
       const int r = rt * 16 + 4 * g + i;
       const int tt = r < rows ? (int)divide((uint32_t)r, a.share) : 0;
       lse[rt][i] = r < rows ? a.lse[(int64_t)(s.first + tt) * heads + head * share + (r - tt * share)] * kLog2e : 0.0f;
-      pos[rt][i] = r < rows ? text + tt : kNoRow;
+      const Seen seen(a, text + tt, r < rows);
+      lo[rt][i] = seen.lo;
+      many[rt][i] = (int)seen.many;
     }
   }
   const bool full = rows == 16 * RT;
@@ -232,31 +248,34 @@ __global__ __launch_bounds__(256) void k_weigh_few(WeighArgs a) {
     }
     // whether every row sees every key
     const bool whole = full && (!a.causal || piece * 32 + 31 <= text) && (a.window == 0 || piece * 32 > text + tokens - 1 - a.window);
+    auto work = [&](auto all) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int j = piece * 32 + u * 16 + col;
-      float sum = 0.0f;
+      for (int u = 0; u < 2; ++u) {
+        const int j = piece * 32 + u * 16 + col;
+        float sum = 0.0f;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int rt = 0; rt < RT; ++rt) {
+          f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st)
+          for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-          for (int n = NT - 1; n >= 0; --n) sc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[n][rt][st], k[u][st], sc, 0, 0, 0);
-        float p[4];
+            for (int n = NT - 1; n >= 0; --n) sc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[n][rt][st], k[u][st], sc, 0, 0, 0);
+          float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], a.scale_log2, -lse[rt][i]));
-          if (!whole) {
-            const bool see = pos[rt][i] != kNoRow && (!a.causal || j <= pos[rt][i]) && (a.window == 0 || j > pos[rt][i] - a.window);
-            p[i] = see ? p[i] : 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], a.scale_log2, -lse[rt][i]));
+            if (!decltype(all)::value) p[i] = Seen(lo[rt][i], many[rt][i]).holds(j) ? p[i] : 0.0f;
           }
+          sum += (p[0] + p[1]) + (p[2] + p[3]);
         }
-        sum += (p[0] + p[1]) + (p[2] + p[3]);
+        sum = quad_sum(sum);
+        if (g == 0 && to[u]) *to[u] = was[u] + sum;
       }
-      sum = quad_sum(sum);
-      if (g == 0 && to[u]) *to[u] = was[u] + sum;
-    }
+    };
+    if (whole)
+      work(std::true_type());
+    else
+      work(std::false_type());
     piece = next;
   }
   if (a.err && lost) atomicAdd(a.err, 1);
@@ -284,7 +303,7 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
   const Cache& c = a.c;
   __shared__ __align__(16) uint8_t rows_lds[2][NT][kRows * Sh::kRow];
   __shared__ __align__(16) float lse_lds[2][kRows];
-  __shared__ __align__(16) int pos_lds[2][kRows];
+  __shared__ __align__(16) int lo_lds[2][kRows], many_lds[2][kRows];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -312,7 +331,7 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
 
     Raw8<NT == 3> staged[kParts];
     float staged_lse = 0.0f;
-    int staged_pos = kNoRow;
+    int staged_lo = 0, staged_many = 0;
     auto load = [&](int block) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
@@ -328,7 +347,9 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
         const bool live = row < rows;
         const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
         staged_lse = live ? a.lse[(int64_t)(s.first + t) * heads + head * share + (row - t * share)] : 0.0f;
-        staged_pos = live ? text + t : kNoRow;
+        const Seen seen(a, text + t, live);
+        staged_lo = seen.lo;
+        staged_many = (int)seen.many;
       }
     };
     auto write = [&](int buffer) {
@@ -342,7 +363,8 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
       }
       if (tid < kRows) {
         lse_lds[buffer][tid] = staged_lse * kLog2e;
-        pos_lds[buffer][tid] = staged_pos;
+        lo_lds[buffer][tid] = staged_lo;
+        many_lds[buffer][tid] = staged_many;
       }
     };
 
@@ -381,9 +403,9 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
       if (block + 1 < block1) load(block + 1);
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
-        const int p0 = __builtin_amdgcn_readfirstlane(pos_lds[buffer][sub * 32]), p1 = __builtin_amdgcn_readfirstlane(pos_lds[buffer][sub * 32 + 31]);
-        // whether every row sees every key of the wave's
-        const bool whole = p1 >= text && (!a.causal || key0 + 32 * kTiles - 1 <= p0) && (a.window == 0 || key0 > p1 - a.window);
+        // whether every row sees every key of the wave's (positions ascend with the rows)
+        const int r0 = block * kRows + sub * 32, p0 = text + (int)divide((uint32_t)r0, a.share), p1 = text + (int)divide((uint32_t)(r0 + 31), a.share);
+        const bool whole = r0 + 32 <= rows && (!a.causal || key0 + 32 * kTiles - 1 <= p0) && (a.window == 0 || key0 > p1 - a.window);
         f32x16 sc[kTiles];
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) sc[u] = f32x16{0.0f};
@@ -396,26 +418,28 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
 #pragma unroll
             for (int u = 0; u < kTiles; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, k[u][st], sc[u], 0, 0, 0);
           }
-#pragma unroll
-        for (int u = 0; u < kTiles; ++u) {
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          const int j = key0 + u * 32 + col;
+        auto work = [&](auto all) {
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[buffer][sub * 32 + i4 * 8 + half * 4]);
+            const int r = sub * 32 + i4 * 8 + half * 4;
+            const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[buffer][r]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float p = __builtin_amdgcn_exp2f(fmaf(sc[u][i4 * 4 + i], a.scale_log2, -l[i]));
-              if (!whole) {
-                const int pos = pos_lds[buffer][sub * 32 + i4 * 8 + half * 4 + i];
-                const bool see = pos != kNoRow && (!a.causal || j <= pos) && (a.window == 0 || j > pos - a.window);
-                p = see ? p : 0.0f;
+            for (int u = 0; u < kTiles; ++u) {
+              const int j = key0 + u * 32 + col;
+              float p[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(fmaf(sc[u][i4 * 4 + i], a.scale_log2, -l[i]));
+                if (!decltype(all)::value) p[i] = Seen(lo_lds[buffer][r + i], many_lds[buffer][r + i]).holds(j) ? p[i] : 0.0f;
               }
-              part[i] += p;
+              sum[u] += (p[0] + p[1]) + (p[2] + p[3]);
             }
           }
-          sum[u] += (part[0] + part[1]) + (part[2] + part[3]);
-        }
+        };
+        if (whole)
+          work(std::true_type());
+        else
+          work(std::false_type());
       }
       if (block + 1 < block1) write(buffer ^ 1);
     }
