@@ -302,8 +302,9 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
   constexpr int kParts = kRows * (DP / 8) / 256;                               // 8-channel parts of a block that a thread stages
   const Cache& c = a.c;
   __shared__ __align__(16) uint8_t rows_lds[2][NT][kRows * Sh::kRow];
-  __shared__ __align__(16) float lse_lds[2][kRows];
-  __shared__ __align__(16) int lo_lds[2][kRows], many_lds[2][kRows];
+  // (three: the last rows of a block are weighed while the next is multiplied and the one after that written)
+  __shared__ __align__(16) float lse_lds[3][kRows];
+  __shared__ __align__(16) int lo_lds[3][kRows], many_lds[3][kRows];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -329,18 +330,30 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
     const int block0 = t0 * share / kRows, block1 = t1 > t0 ? (int)(((int64_t)t1 * share + kRows - 1) / kRows) : block0;
     if (block0 >= block1 && !a.fresh && last_key < text) continue;  // nothing is added
 
+    // A thread stages the same channels of every (256 / (DP / 8))-th row; from block to block its rows move on by kRows.
     Raw8<NT == 3> staged[kParts];
+    const int ch = tid % (DP / 8) * 8;
+    const int dt = (int)divide((uint32_t)kRows, a.share), dg = kRows - dt * share;  // in tokens and heads
+    const int64_t step = (int64_t)dt * a.q_token + (int64_t)dg * a.q_head, wrap = a.q_token - (int64_t)share * a.q_head;
+    int part_g[kParts], part_row[kParts];
+    int64_t part_at[kParts];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const int row = part_row[i] = block0 * kRows + (i * 256 + tid) / (DP / 8);
+      const int t = (int)divide((uint32_t)row, a.share);
+      part_g[i] = row - t * share;
+      part_at[i] = (int64_t)(s.first + t) * a.q_token + (int64_t)(head * share + part_g[i]) * a.q_head;
+    }
     float staged_lse = 0.0f;
     int staged_lo = 0, staged_many = 0;
     auto load = [&](int block) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
-        const int part = i * 256 + tid, r = part / (DP / 8), ch = part % (DP / 8) * 8;
-        const int row = block * kRows + r;
-        const bool live = row < rows;
-        const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
-        const int64_t from = (int64_t)(s.first + t) * a.q_token + (int64_t)(head * share + (live ? row - t * share : 0)) * a.q_head;
-        staged[i] = raw_query<NT == 3>(a, from, ch, live);
+        staged[i] = raw_query<NT == 3>(a, part_at[i], ch, part_row[i] < rows);
+        part_row[i] += kRows;
+        part_g[i] += dg;
+        part_at[i] += step;
+        if (part_g[i] >= share) part_g[i] -= share, part_at[i] += wrap;
       }
       if (tid < kRows) {
         const int row = block * kRows + tid;
@@ -352,26 +365,26 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
         staged_many = (int)seen.many;
       }
     };
-    auto write = [&](int buffer) {
+    auto write = [&](int buffer, int slot) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
-        const int part = i * 256 + tid, r = part / (DP / 8), ch = part % (DP / 8) * 8;
+        const int r = (i * 256 + tid) / (DP / 8);
         bf16x8 terms[NT];
         query_terms<NT>(staged[i], terms);
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<bf16x8*>(&rows_lds[buffer][n][r * Sh::kRow + ch * 2]) = terms[n];
       }
       if (tid < kRows) {
-        lse_lds[buffer][tid] = staged_lse * kLog2e;
-        lo_lds[buffer][tid] = staged_lo;
-        many_lds[buffer][tid] = staged_many;
+        lse_lds[slot][tid] = staged_lse * kLog2e;
+        lo_lds[slot][tid] = staged_lo;
+        many_lds[slot][tid] = staged_many;
       }
     };
 
     if (block0 < block1) load(block0);
     // the keys
     float* to[kTiles];
-    float old[kTiles], sum[kTiles];
+    float old[kTiles], sum[kTiles][4];
     bf16x8 k[kTiles][kSteps];
 #pragma unroll
     for (int u = 0; u < kTiles; ++u) {
@@ -385,7 +398,8 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
       key.scales(c, words);
       to[u] = key.weight;
       old[u] = key.weight && !a.fresh && j < text ? *key.weight : 0.0f;
-      sum[u] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[u][i] = 0.0f;
       nan_scales<KIND, Key::kWords>(words);
 #pragma unroll
       for (int m = 0; m < kChunks; ++m) {
@@ -396,57 +410,123 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
       }
     }
     __syncthreads();  // (the tile before has been worked through)
-    if (block0 < block1) write(0);
+    if (block0 < block1) write(0, 0);
+    // The products of 32 rows run beside the exponentials of the 32 before them.
+    f32x16 scores[2][kTiles];
+    auto products = [&](int buffer, int sub, f32x16* sc) {
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) sc[u] = f32x16{0.0f};
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n) {
+          const bf16x8 qf = *reinterpret_cast<const bf16x8*>(
+              &rows_lds[buffer][n][(sub * 32 + col) * Sh::kRow + channel_of<KIND, 2>(st, half) * 2]);
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, k[u][st], sc[u], 0, 0, 0);
+        }
+    };
+    auto weigh = [&](auto all, int slot, int sub, const f32x16* sc) {
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const int r = sub * 32 + i4 * 8 + half * 4;
+        const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[slot][r]);
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) {
+          const int j = key0 + u * 32 + col;
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(fmaf(sc[u][i4 * 4 + i], a.scale_log2, -l[i]));
+            if (!decltype(all)::value) p[i] = Seen(lo_lds[slot][r + i], many_lds[slot][r + i]).holds(j) ? p[i] : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[u][i] += p[i];
+        }
+      }
+    };
+    // Both, for rows that all see all keys: after each matrix instruction a share of the exponentials, in an order that is
+    // pinned, since the two waves of a SIMD fall into step and do not overlap the one's products with the other's sums
+    auto both = [&](int buffer, int sub, f32x16* sc, int slot, int last, const f32x16* old_sc) {
+      constexpr int kAhead = 2, kPer = 16 / kSteps, kAll = kSteps * kTiles;
+      const uint8_t* from = &rows_lds[buffer][0][(sub * 32 + col) * Sh::kRow];
+      auto operand = [&](int st, int n) {
+        return *reinterpret_cast<const bf16x8*>(from + n * kRows * Sh::kRow + channel_of<KIND, 2>(st, half) * 2);
+      };
+      bf16x8 qf[kAhead][NT];
+      f32x4 l[4];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) qf[i][n] = operand(i, n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[i] = *reinterpret_cast<const f32x4*>(&lse_lds[slot][last * 32 + i * 8 + half * 4]);
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) sc[u] = f32x16{0.0f};
+      float p[kPer];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < kAll; ++m) {
+        const int st = m / kTiles, u = m % kTiles;
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[st % kAhead][n], k[u][st], sc[u], 0, 0, 0);
+        if (u == kTiles - 1 && st + kAhead < kSteps) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) qf[st % kAhead][n] = operand(st + kAhead, n);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {  // (added a step after their exponential)
+          const int e = (m - 1) * kPer + i;
+          if (m > 0) sum[e / 16][e & 3] += p[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int e = m * kPer + i;
+          p[i] = __builtin_amdgcn_exp2f(fmaf(old_sc[e / 16][e % 16], a.scale_log2, -l[e % 16 / 4][e & 3]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum[kTiles - 1][((kAll - 1) * kPer + i) & 3] += p[i];
+    };
+    // whether every one of 32 rows sees every key of the wave's (positions ascend with the rows)
+    auto whole = [&](int r0) {
+      const int p0 = text + (int)divide((uint32_t)r0, a.share), p1 = text + (int)divide((uint32_t)(r0 + 31), a.share);
+      return r0 + 32 <= rows && (!a.causal || key0 + 32 * kTiles - 1 <= p0) && (a.window == 0 || key0 > p1 - a.window);
+    };
+    enum { kNone, kWhole, kMasked } before = kNone;
+    int slot = 0, slot_before = 0;
     for (int block = block0; block < block1; ++block) {
       const int buffer = (block - block0) & 1;
       __syncthreads();
       if (block + 1 < block1) load(block + 1);
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
-        // whether every row sees every key of the wave's (positions ascend with the rows)
-        const int r0 = block * kRows + sub * 32, p0 = text + (int)divide((uint32_t)r0, a.share), p1 = text + (int)divide((uint32_t)(r0 + 31), a.share);
-        const bool whole = r0 + 32 <= rows && (!a.causal || key0 + 32 * kTiles - 1 <= p0) && (a.window == 0 || key0 > p1 - a.window);
-        f32x16 sc[kTiles];
-#pragma unroll
-        for (int u = 0; u < kTiles; ++u) sc[u] = f32x16{0.0f};
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-          for (int n = NT - 1; n >= 0; --n) {
-            const bf16x8 qf = *reinterpret_cast<const bf16x8*>(
-                &rows_lds[buffer][n][(sub * 32 + col) * Sh::kRow + channel_of<KIND, 2>(st, half) * 2]);
-#pragma unroll
-            for (int u = 0; u < kTiles; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, k[u][st], sc[u], 0, 0, 0);
-          }
-        auto work = [&](auto all) {
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const int r = sub * 32 + i4 * 8 + half * 4;
-            const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[buffer][r]);
-#pragma unroll
-            for (int u = 0; u < kTiles; ++u) {
-              const int j = key0 + u * 32 + col;
-              float p[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(fmaf(sc[u][i4 * 4 + i], a.scale_log2, -l[i]));
-                if (!decltype(all)::value) p[i] = Seen(lo_lds[buffer][r + i], many_lds[buffer][r + i]).holds(j) ? p[i] : 0.0f;
-              }
-              sum[u] += (p[0] + p[1]) + (p[2] + p[3]);
-            }
-          }
-        };
-        if (whole)
-          work(std::true_type());
-        else
-          work(std::false_type());
+        const int last = (sub + kSub - 1) % kSub;  // the 32 rows before
+        f32x16 *sc = scores[kSub == 1 ? 0 : sub & 1], *old_sc = scores[kSub == 1 ? 0 : last & 1];
+        if (kSub > 1 && before == kWhole) {
+          both(buffer, sub, sc, slot_before, last, old_sc);
+        } else {
+          if (kSub > 1 && before == kMasked) weigh(std::false_type(), slot_before, last, old_sc);
+          products(buffer, sub, sc);
+        }
+        before = whole(block * kRows + sub * 32) ? kWhole : kMasked;
+        slot_before = slot;
+        if (kSub == 1) {
+          if (before == kWhole)
+            weigh(std::true_type(), slot, 0, sc);
+          else
+            weigh(std::false_type(), slot, 0, sc);
+        }
       }
-      if (block + 1 < block1) write(buffer ^ 1);
+      slot = slot == 2 ? 0 : slot + 1;
+      if (block + 1 < block1) write(buffer ^ 1, slot);
     }
+    if (kSub > 1 && before != kNone) weigh(std::false_type(), slot_before, kSub - 1, scores[(kSub - 1) & 1]);
     // what the new tokens' places held is of earlier tokens
 #pragma unroll
     for (int u = 0; u < kTiles; ++u) {
-      const float got = half_sum(sum[u]);
+      const float got = half_sum((sum[u][0] + sum[u][1]) + (sum[u][2] + sum[u][3]));
       if (half == 0 && to[u]) *to[u] = old[u] + got;
     }
   }
