@@ -58,23 +58,21 @@ struct Raw8 {
   u32x4 w[F32 ? 2 : 1];
 };
 template <bool F32>
-__device__ __forceinline__ Raw8<F32> raw_query(const WeighArgs& a, int64_t at, int ch, bool live) {
+__device__ __forceinline__ Raw8<F32> raw_query(const uint8_t* from, bool vec, bool live) {
   Raw8<F32> r;
   r.w[0] = u32x4{0, 0, 0, 0};
   if constexpr (F32) r.w[1] = r.w[0];
-  if (!live || ch >= a.c.dim) return r;
-  if (a.q_vec) {
-    const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.q) + (at + ch) * (F32 ? 4 : 2));
-    r.w[0] = from[0];
-    if constexpr (F32) r.w[1] = from[1];
+  if (!live) return r;
+  if (vec) {
+    r.w[0] = reinterpret_cast<const u32x4*>(from)[0];
+    if constexpr (F32) r.w[1] = reinterpret_cast<const u32x4*>(from)[1];
   } else if constexpr (F32) {
-    const uint32_t* from = static_cast<const uint32_t*>(a.q) + at + ch;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i / 4][i & 3] = from[i];
+    for (int i = 0; i < 8; ++i) r.w[i / 4][i & 3] = reinterpret_cast<const uint32_t*>(from)[i];
   } else {
-    const uint16_t* from = static_cast<const uint16_t*>(a.q) + at + ch;
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.w[0][i] = from[2 * i] | (uint32_t)from[2 * i + 1] << 16;
+    for (int i = 0; i < 4; ++i) r.w[0][i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
   }
   return r;
 }
@@ -205,7 +203,8 @@ __global__ __launch_bounds__(256) void k_weigh_few(WeighArgs a) {
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       bf16x8 terms[NT];
-      query_terms<NT>(raw_query<NT == 3>(a, at, channel_of<KIND, 4>(st, g), live), terms);
+      const int ch = channel_of<KIND, 4>(st, g);
+      query_terms<NT>(raw_query<NT == 3>(static_cast<const uint8_t*>(a.q) + (at + ch) * (NT == 3 ? 4 : 2), a.q_vec, live && ch < c.dim), terms);
 #pragma unroll
       for (int n = 0; n < NT; ++n) q[n][rt][st] = terms[n];
     }
@@ -330,39 +329,62 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
     const int block0 = t0 * share / kRows, block1 = t1 > t0 ? (int)(((int64_t)t1 * share + kRows - 1) / kRows) : block0;
     if (block0 >= block1 && !a.fresh && last_key < text) continue;  // nothing is added
 
-    // A thread stages the same channels of every (256 / (DP / 8))-th row; from block to block its rows move on by kRows.
+    // A thread stages the same channels of every (256 / (DP / 8))-th row, and one of the first threads a row's log-sum; from
+    // block to block all of them move on by kRows rows, dt tokens and dg heads.
+    constexpr int kSize = NT == 3 ? 4 : 2;
     Raw8<NT == 3> staged[kParts];
     const int ch = tid % (DP / 8) * 8;
-    const int dt = (int)divide((uint32_t)kRows, a.share), dg = kRows - dt * share;  // in tokens and heads
-    const int64_t step = (int64_t)dt * a.q_token + (int64_t)dg * a.q_head, wrap = a.q_token - (int64_t)share * a.q_head;
-    int part_g[kParts], part_row[kParts];
-    int64_t part_at[kParts];
+    const int dt = (int)divide((uint32_t)kRows, a.share), dg = kRows - dt * share;
+    const int64_t step = ((int64_t)dt * a.q_token + (int64_t)dg * a.q_head) * kSize, wrap = (a.q_token - (int64_t)share * a.q_head) * kSize;
+    const uint8_t* part_at[kParts];
+    int part_g[kParts];
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-      const int row = part_row[i] = block0 * kRows + (i * 256 + tid) / (DP / 8);
-      const int t = (int)divide((uint32_t)row, a.share);
+      const int row = block0 * kRows + (i * 256 + tid) / (DP / 8), t = (int)divide((uint32_t)row, a.share);
       part_g[i] = row - t * share;
-      part_at[i] = (int64_t)(s.first + t) * a.q_token + (int64_t)(head * share + part_g[i]) * a.q_head;
+      part_at[i] = static_cast<const uint8_t*>(a.q) +
+                   ((int64_t)(s.first + t) * a.q_token + (int64_t)(head * share + part_g[i]) * a.q_head + ch) * kSize;
+    }
+    int row_t, row_g;
+    {
+      const int row = block0 * kRows + tid;
+      row_t = (int)divide((uint32_t)row, a.share);
+      row_g = row - row_t * share;
     }
     float staged_lse = 0.0f;
     int staged_lo = 0, staged_many = 0;
+    const bool simple = a.q_vec && c.dim == DP;
     auto load = [&](int block) {
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) {
-        staged[i] = raw_query<NT == 3>(a, part_at[i], ch, part_row[i] < rows);
-        part_row[i] += kRows;
-        part_g[i] += dg;
-        part_at[i] += step;
-        if (part_g[i] >= share) part_g[i] -= share, part_at[i] += wrap;
-      }
-      if (tid < kRows) {
-        const int row = block * kRows + tid;
-        const bool live = row < rows;
-        const int t = live ? (int)divide((uint32_t)row, a.share) : 0;
-        staged_lse = live ? a.lse[(int64_t)(s.first + t) * heads + head * share + (row - t * share)] : 0.0f;
-        const Seen seen(a, text + t, live);
+      const bool every = (block + 1) * kRows <= rows;
+      if (tid < kRows) {  // (a row that is none takes the first one's: no key is seen by it)
+        const bool live = every || block * kRows + tid < rows;
+        staged_lse = a.lse[(int64_t)(s.first + (live ? row_t : 0)) * heads + head * share + (live ? row_g : 0)];
+        const Seen seen(a, text + row_t, live);
         staged_lo = seen.lo;
         staged_many = (int)seen.many;
+      }
+      if (simple && every) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+#pragma unroll
+          for (int n = 0; n < kSize / 2; ++n) staged[i].w[n] = reinterpret_cast<const u32x4*>(part_at[i])[n];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          staged[i] = raw_query<NT == 3>(part_at[i], a.q_vec, ch < c.dim && block * kRows + (i * 256 + tid) / (DP / 8) < rows);
+      }
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) part_at[i] += step;
+      row_t += dt;
+      if (dg) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          part_g[i] += dg;
+          if (part_g[i] >= share) part_g[i] -= share, part_at[i] += wrap;
+        }
+        row_g += dg;
+        if (row_g >= share) row_g -= share, ++row_t;
       }
     };
     auto write = [&](int buffer, int slot) {
@@ -445,49 +467,56 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
         }
       }
     };
-    // Both, for rows that all see all keys: after each matrix instruction a share of the exponentials, in an order that is
-    // pinned, since the two waves of a SIMD fall into step and do not overlap the one's products with the other's sums
-    auto both = [&](int buffer, int sub, f32x16* sc, int slot, int last, const f32x16* old_sc) {
-      constexpr int kAhead = 2, kPer = 16 / kSteps, kAll = kSteps * kTiles;
-      const uint8_t* from = &rows_lds[buffer][0][(sub * 32 + col) * Sh::kRow];
-      auto operand = [&](int st, int n) {
-        return *reinterpret_cast<const bf16x8*>(from + n * kRows * Sh::kRow + channel_of<KIND, 2>(st, half) * 2);
+    // Both, for a whole block whose rows, and the 32 before it, all see all keys (its last 32 are weighed with the next):
+    // after each matrix instruction a share of the exponentials, in an order that is pinned, since the two waves of a SIMD fall
+    // into step and do not overlap the one's products with the other's sums
+    auto both = [&](int buffer, int slot, int slot_before) {
+      constexpr int kAhead = NT == 1 ? 3 : 2, kPer = 16 / kSteps, kAll = kSteps * kTiles, kGroup = 4 * kTiles;
+      const uint8_t* from = &rows_lds[buffer][0][col * Sh::kRow];
+      auto operand = [&](int i, int n) {  // of step i, counted over the block
+        return *reinterpret_cast<const bf16x8*>(from + (n * kRows + i / kSteps * 32) * Sh::kRow + channel_of<KIND, 2>(i % kSteps, half) * 2);
+      };
+      auto sums_of = [&](int i) {  // four log-sums of the 4 i-th row on, counted over the 32 before and the block
+        return *reinterpret_cast<const f32x4*>(i < 4 ? &lse_lds[slot_before][(kSub - 1) * 32 + i * 8 + half * 4]
+                                                     : &lse_lds[slot][(i - 4) * 8 + half * 4]);
       };
       bf16x8 qf[kAhead][NT];
-      f32x4 l[4];
+      f32x4 l[2];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n) qf[i][n] = operand(i, n);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) l[i] = *reinterpret_cast<const f32x4*>(&lse_lds[slot][last * 32 + i * 8 + half * 4]);
-#pragma unroll
-      for (int u = 0; u < kTiles; ++u) sc[u] = f32x16{0.0f};
+      l[0] = sums_of(0);
       float p[kPer];
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < kAll; ++m) {
-        const int st = m / kTiles, u = m % kTiles;
+      for (int m = 0; m < kSub * kAll; ++m) {
+        const int i = m / kTiles, u = m % kTiles, sub = m / kAll;
+        f32x16& sc = scores[kSub == 1 ? 0 : sub & 1][u];
+        if (i % kSteps == 0) sc = f32x16{0.0f};
 #pragma unroll
-        for (int n = NT - 1; n >= 0; --n) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[st % kAhead][n], k[u][st], sc[u], 0, 0, 0);
-        if (u == kTiles - 1 && st + kAhead < kSteps) {
+        for (int n = NT - 1; n >= 0; --n) sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[i % kAhead][n], k[u][i % kSteps], sc, 0, 0, 0);
+        if (u == kTiles - 1 && i + kAhead < kSub * kSteps) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) qf[st % kAhead][n] = operand(st + kAhead, n);
+          for (int n = 0; n < NT; ++n) qf[i % kAhead][n] = operand(i + kAhead, n);
+        }
+        // an element: rows by four, of each the tiles (added an instruction after their exponential)
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          const int e = (m - 1) * kPer + x;
+          if (m > 0) sum[e % kGroup / 4][e & 3] += p[x];
         }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {  // (added a step after their exponential)
-          const int e = (m - 1) * kPer + i;
-          if (m > 0) sum[e / 16][e & 3] += p[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int e = m * kPer + i;
-          p[i] = __builtin_amdgcn_exp2f(fmaf(old_sc[e / 16][e % 16], a.scale_log2, -l[e % 16 / 4][e & 3]));
+        for (int x = 0; x < kPer; ++x) {
+          const int e = m * kPer + x, i4 = e / kGroup;
+          if (e % kGroup == 0 && i4 + 1 < 4 * kSub) l[(i4 + 1) & 1] = sums_of(i4 + 1);
+          const f32x16& old = scores[(sub + kSub - 1) % kSub & 1][e % kGroup / 4];
+          p[x] = __builtin_amdgcn_exp2f(fmaf(old[i4 % 4 * 4 + (e & 3)], a.scale_log2, -l[i4 & 1][e & 3]));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) sum[kTiles - 1][((kAll - 1) * kPer + i) & 3] += p[i];
+      for (int x = 0; x < kPer; ++x) sum[kTiles - 1][((kSub * kAll - 1) * kPer + x) & 3] += p[x];
     };
     // whether every one of 32 rows sees every key of the wave's (positions ascend with the rows)
     auto whole = [&](int r0) {
@@ -500,25 +529,28 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
       const int buffer = (block - block0) & 1;
       __syncthreads();
       if (block + 1 < block1) load(block + 1);
+      bool fast = kSub > 1 && before == kWhole;
 #pragma unroll
-      for (int sub = 0; sub < kSub; ++sub) {
-        const int last = (sub + kSub - 1) % kSub;  // the 32 rows before
-        f32x16 *sc = scores[kSub == 1 ? 0 : sub & 1], *old_sc = scores[kSub == 1 ? 0 : last & 1];
-        if (kSub > 1 && before == kWhole) {
-          both(buffer, sub, sc, slot_before, last, old_sc);
-        } else {
-          if (kSub > 1 && before == kMasked) weigh(std::false_type(), slot_before, last, old_sc);
-          products(buffer, sub, sc);
-        }
-        before = whole(block * kRows + sub * 32) ? kWhole : kMasked;
-        slot_before = slot;
-        if (kSub == 1) {
-          if (before == kWhole)
-            weigh(std::true_type(), slot, 0, sc);
-          else
-            weigh(std::false_type(), slot, 0, sc);
+      for (int sub = 0; sub < kSub - 1; ++sub) fast = fast && whole(block * kRows + sub * 32);
+      if (fast) {
+        both(buffer, slot, slot_before);
+      } else {
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          const int last = (sub + kSub - 1) % kSub;  // the 32 rows before
+          if (kSub > 1 && before != kNone) weigh(std::false_type(), sub == 0 ? slot_before : slot, last, scores[last & 1]);
+          products(buffer, sub, scores[kSub == 1 ? 0 : sub & 1]);
+          before = kMasked;
+          if (kSub == 1) {
+            if (whole(block * kRows))
+              weigh(std::true_type(), slot, 0, scores[0]);
+            else
+              weigh(std::false_type(), slot, 0, scores[0]);
+          }
         }
       }
+      before = whole(block * kRows + (kSub - 1) * 32) ? kWhole : kMasked;
+      slot_before = slot;
       slot = slot == 2 ? 0 : slot + 1;
       if (block + 1 < block1) write(buffer ^ 1, slot);
     }
