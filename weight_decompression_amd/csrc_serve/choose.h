@@ -1,11 +1,11 @@
 // The choice of the cached tokens that stay: of a sequence of m > budget tokens the first `sinks`, the last `recent`, and
 // of those between the budget - sinks - recent of the largest weight, the lowest place of equals; each key head for itself.
 //
-// One workgroup a (sequence, key head).  The weights become 32-bit numbers of the same order; the smallest that stays is
-// found digit by digit from the top (11, 11 and 10 bits: a histogram in LDS, its sums from the top, the bin that the wanted
-// count falls into), and everything above it stays, of its equals the first.  The places are then written in order: every
-// wave counts its 64 places of each round of 1024, one scan over the rounds and waves gives each wave where it writes.
-// Nothing is sorted, and the order of the histogram's atomics changes nothing.
+// One workgroup a (sequence, key head), which holds the weights of up to 32768 (or 4096) places in registers as 32-bit numbers
+// of the same order.  The smallest that stays is found digit by digit from the top (11, 11 and 10 bits: a histogram in LDS, its
+// sums from the top, the bin that the wanted count falls into); everything above it stays, of its equals the first.  The
+// places are then written in order: each wave counts its 64 places of every round of 1024, one scan over all of these counts
+// tells each wave where it writes.  Nothing is sorted, and the order of the histogram's atomics changes nothing.
 #pragma once
 
 #include "serve_common.h"
@@ -31,22 +31,23 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 constexpr int kChooseThreads = 1024, kChooseWaves = kChooseThreads / kWave;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
 
-// Exclusive sums over the workgroup of one number a thread, in the threads' order; *all: the sum of all.
-__device__ __forceinline__ int scan_block(int x, int* waves, int* all) {
+// Exclusive sums over the workgroup of one number a thread, in the threads' order; *all: the sum of all.  A T may hold two
+// counts side by side.
+template <typename T>
+__device__ __forceinline__ T scan_block(T x, T* waves, T* all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int sum = x;
+  T sum = x;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
-    const int y = __shfl_up(sum, d);
+    const T y = __shfl_up(sum, d);
     if (lane >= d) sum += y;
   }
-  __syncthreads();
   if (lane == kWave - 1) waves[wave] = sum;
   __syncthreads();
-  int before = 0, total = 0;
+  T before = 0, total = 0;
 #pragma unroll
   for (int i = 0; i < kChooseWaves; ++i) {
-    const int w = waves[i];
+    const T w = waves[i];
     before += i < wave ? w : 0;
     total += w;
   }
@@ -54,10 +55,12 @@ __device__ __forceinline__ int scan_block(int x, int* waves, int* all) {
   return before + sum - x;
 }
 
-// HELD: places a thread holds; longer sequences are read again in each round.
-template <int HELD>
+// HELD: places a thread holds.  LONG: sequences that pass that are read again for each digit, HELD rounds at a time.
+template <int HELD, bool LONG>
 __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
-  __shared__ int bins[kBins], waves[kChooseWaves], found[2];
+  using Pair = unsigned long long;  // places that stay for sure, and from bit 32 on those equal to the least
+  __shared__ int bins[kBins], waves[3][kChooseWaves], found[3][2];
+  __shared__ Pair counts[HELD * kChooseWaves], pair_waves[kChooseWaves];
   const Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = (int)blockIdx.x % c.heads, b = (int)blockIdx.x / c.heads;
@@ -76,97 +79,113 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
   }
   bool lost = false;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
-  auto weight_at = [&](int j) -> uint32_t {
-    const uint32_t page = divide((uint32_t)j, c.page);
-    const int32_t id = table[page];
-    if (id < 0 || id >= c.pages) {  // (counts as NaN does)
-      lost = true;
-      return order_of(-INFINITY);
-    }
-    return order_of(a.weights[((int64_t)id * c.heads + head) * c.page.by + (j - page * c.page.by)]);
-  };
   const int low = a.sinks, high = len - a.recent;  // those between are chosen from
   int want = a.budget - a.sinks - a.recent;
   uint32_t held[HELD];
   const int rounds = (len + kChooseThreads - 1) / kChooseThreads;
-  const bool all_held = rounds <= HELD;
-  if (all_held) {
+  // all page numbers, then all weights under way at once (past the last place: that one's again)
+  auto hold = [&](int r0) {
+    int32_t ids[HELD];
+    int slots[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const int j = i * kChooseThreads + tid;
-      held[i] = j >= low && j < high ? weight_at(j) : 0;
+      const uint32_t j = (uint32_t)min((r0 + i) * kChooseThreads + tid, len - 1), page = divide(j, c.page);
+      slots[i] = (int)(j - page * c.page.by);
+      ids[i] = table[page];
     }
-  }
-  // runs f(place, weight's number) over this thread's places between
-  auto each = [&](auto f) {
-    if (all_held) {
+    float w[HELD];
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
-        const int j = i * kChooseThreads + tid;
-        if (j >= low && j < high) f(j, held[i]);
-      }
-    } else {
-      for (int i = 0; i < rounds; ++i) {
-        const int j = i * kChooseThreads + tid;
-        if (j >= low && j < high) f(j, weight_at(j));
-      }
+    for (int i = 0; i < HELD; ++i) {
+      const bool ok = ids[i] >= 0 && ids[i] < c.pages;
+      lost |= !ok;
+      w[i] = a.weights[((int64_t)(ok ? ids[i] : 0) * c.heads + head) * c.page.by + slots[i]];
+      if (!ok) slots[i] = -1;
     }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) held[i] = order_of(slots[i] < 0 ? -INFINITY : w[i]);  // (no place counts as NaN does)
   };
-  uint32_t least = 0, known = 0;  // digits found so far
-  int equal = 0;                  // of those with `least`, how many stay
+  if (!LONG) hold(0);
+  uint32_t least = 0xffffffffu;  // the least that stays (nothing between does where nothing is wanted)
   if (want > 0) {
-#pragma unroll
+    uint32_t known = 0;  // digits found so far
+    least = 0;
+#pragma unroll LONG ? 1 : 3
     for (int digit = 0; digit < 3; ++digit) {
       const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
       const uint32_t mask = digit == 2 ? 1023u : 2047u;
       for (int i = tid; i < kBins; i += kChooseThreads) bins[i] = 0;
       __syncthreads();
-      each([&](int, uint32_t u) {
-        if ((u & known) == least) atomicAdd(&bins[u >> shift & mask], 1);
-      });
+      auto count = [&](int j, uint32_t u) {
+        if (j >= low && j < high && (u & known) == least) atomicAdd(&bins[u >> shift & mask], 1);
+      };
+      for (int r0 = 0; r0 < (LONG ? rounds : 1); r0 += HELD) {
+        if (LONG) hold(r0);
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+          if (r0 + i < rounds) count((r0 + i) * kChooseThreads + tid, held[i]);
+      }
       __syncthreads();
       // two bins a thread, from the top
       const int top = kBins - 1 - 2 * tid, first = bins[top], second = bins[top - 1];
       int all;
-      const int above = scan_block(first + second, waves, &all);
-      if (above < want && want <= above + first) found[0] = top, found[1] = want - above;
-      if (above + first < want && want <= above + first + second) found[0] = top - 1, found[1] = want - above - first;
+      const int above = scan_block(first + second, waves[digit], &all);
+      if (above < want && want <= above + first) found[digit][0] = top, found[digit][1] = want - above;
+      if (above + first < want && want <= above + first + second) found[digit][0] = top - 1, found[digit][1] = want - above - first;
       __syncthreads();
-      least |= (uint32_t)found[0] << shift;
+      least |= (uint32_t)found[digit][0] << shift;
       known |= mask << shift;
-      want = found[1];
+      want = found[digit][1];
     }
-    equal = want;
-  } else {
-    least = 0xffffffffu;  // nothing between stays
-    known = 0xffffffffu;
   }
-  // the places, in order, a round of 1024 at a time
-  int done = 0, same = 0;  // kept, and equal to the least, in the rounds before
-  auto write = [&](int i, uint32_t u) {
-    const int j = i * kChooseThreads + tid;
+  // the places in order, HELD rounds at a time; `want` of those equal to the least stay
+  Pair before = 0;
+  auto of = [&](int j, uint32_t u, uint64_t* sure, uint64_t* same) {
     const bool between = j >= low && j < high;
-    const bool is_same = between && u == least && equal > 0;
-    const bool sure = j < len && (!between || u > least);
-    int all, all_same;
-    const int before_same = same + scan_block(is_same ? 1 : 0, waves, &all_same);
-    const bool stays = sure || (is_same && before_same < equal);
-    const int at = done + scan_block(stays ? 1 : 0, waves, &all);
-    if (stays && at < a.budget) keep[at] = j;
-    done += all;
-    same += all_same;
+    *sure = __ballot(j < len && (!between || u > least));
+    *same = __ballot(between && u == least && want > 0);
   };
-  if (all_held) {
+  for (int r0 = 0; r0 < (LONG ? rounds : 1); r0 += HELD) {
+    if (LONG) hold(r0);
 #pragma unroll
-    for (int i = 0; i < HELD; ++i)
-      if (i < rounds) write(i, held[i]);
-  } else {
-    for (int i = 0; i < rounds; ++i) {
-      const int j = i * kChooseThreads + tid;
-      write(i, j >= low && j < high ? weight_at(j) : 0);
+    for (int i = 0; i < HELD; ++i) {
+      if (r0 + i < rounds) {
+        uint64_t sure, same;
+        of((r0 + i) * kChooseThreads + tid, held[i], &sure, &same);
+        if (lane == 0) counts[i * kChooseWaves + wave] = (Pair)__popcll(sure) | (Pair)__popcll(same) << 32;
+      } else if (lane == 0) {
+        counts[i * kChooseWaves + wave] = 0;
+      }
     }
+    __syncthreads();
+    constexpr int kEach = (HELD * kChooseWaves + kChooseThreads - 1) / kChooseThreads;
+    static_assert(kEach == 1, "a thread has one count");
+    // (the masks are made again: kept, they would take more registers than there are)
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) asm volatile("" : "+v"(held[i]));
+    Pair all;
+    const Pair mine = tid < HELD * kChooseWaves ? counts[tid] : 0, at = before + scan_block(mine, pair_waves, &all);
+    if (tid < HELD * kChooseWaves) counts[tid] = at;
+    before += all;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (r0 + i < rounds) {
+        const int j = (r0 + i) * kChooseThreads + tid;
+        uint64_t sure, same;
+        of(j, held[i], &sure, &same);
+        const Pair from = counts[i * kChooseWaves + wave];
+        const int same_before = (int)(from >> 32);
+        const uint64_t below = (1ull << lane) - 1;
+        // of the equals of this wave and round, the first few
+        const bool taken = (same >> lane & 1) && same_before + __popcll(same & below) < want;
+        const bool stays = (sure >> lane & 1) || taken;
+        const int place = (int)(uint32_t)from + min(same_before, want) + __popcll(__ballot(stays) & below);
+        if (stays && place < a.budget) keep[place] = j;
+      }
+    }
+    __syncthreads();
   }
-  if (a.err && __any(lost) && lane == 0 && wave >= 0) atomicAdd(a.err, 1);
+  if (a.err && __any(lost) && lane == 0) atomicAdd(a.err, 1);
 }
 
 }  // namespace serve

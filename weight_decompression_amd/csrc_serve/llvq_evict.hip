@@ -146,7 +146,15 @@ LLVQ_API int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const l
   a.recent = recent;
   a.err = err_count;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL((k_choose<32>), dim3((unsigned)(c.batch * c.heads)), dim3(kChooseThreads), 0, s, a);
+  const dim3 grid((unsigned)(c.batch * c.heads));
+  // by the longest sequence that the table holds
+  const int64_t places = (int64_t)c.max_pages * c.page.by;
+  if (places <= 4 * kChooseThreads)
+    hipLaunchKernelGGL((k_choose<4, false>), grid, dim3(kChooseThreads), 0, s, a);
+  else if (places <= 32 * kChooseThreads)
+    hipLaunchKernelGGL((k_choose<32, false>), grid, dim3(kChooseThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_choose<16, true>), grid, dim3(kChooseThreads), 0, s, a);
   return launch_status();
 }
 
