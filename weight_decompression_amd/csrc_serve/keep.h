@@ -3,10 +3,11 @@
 //
 // What moves is read once and written once; HBM bounds it for long lists, the launch for short ones.  A token's parts (key and
 // value codes, their scale bytes, its weight) never meet, so a workgroup has one part of a (sequence, key head), of the
-// codes 64 bytes of each row, and takes the list in order, a batch of entries at a time: all of a batch is read, then, after
+// codes 64 or 128 bytes of each row, and takes the list in order, a batch of entries at a time: all of a batch is read, then, after
 // a barrier, written.  That is enough for moves in place: keep[i] >= i, so what a batch writes (its own i) lies before
 // anything that later batches read (at or past their own, larger i), and what earlier batches read is past the barrier.  The
-// loads of the next batch are under way while a batch is written.
+// loads of the next batch are under way while a batch is written.  Where entries lie is worked out for 1024 at a time, into LDS:
+// left to each batch, list, page and codes are three loads that wait for each other.
 #pragma once
 
 #include "serve_common.h"
@@ -21,87 +22,99 @@ struct KeepArgs {
   int32_t lists, width;   // lists: 1, or one for each key head
   bool from_new;          // entries count from the first new token, not from the first of all
   int32_t* err;
-  int32_t slices;         // of a row of codes
+  int32_t side, slices;   // 16-byte chunks of a slice, and slices of a row of codes
   int32_t parts;          // workgroups a (sequence, key head): slices of keys, slices of values, scales, weights
 };
 
-constexpr int kKeepThreads = 256, kKeepAhead = 4;
+constexpr int kKeepThreads = 512, kKeepAhead = 8, kKeepList = 1024;
 
-// The places of a list: of entry i where it comes from and where it goes, or nothing.
+// The list of a (sequence, key head), and where its entries lie: (page * heads + head) and slot, from and to (-1: nothing moves).
 struct Moves {
   const int32_t* keep;
   const int32_t* table;
-  int count, first, len;
+  int count, first, len, head;
 };
-__device__ __forceinline__ bool move_of(const Cache& c, const Moves& m, int i, int head, int64_t* from, int* from_slot, int64_t* to,
-                                        int* to_slot, bool* bad) {
-  if (i >= m.count) return false;
-  const int k = m.keep[i];
-  if (k == i || k == -1) return false;
-  const bool fits = k > i && (i == 0 || k > m.keep[i - 1]) && k < m.len - m.first;
-  if (!fits) {
+using Entry = int __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Entry entry_of(const Cache& c, const Moves& m, int i, bool* bad) {
+  const Entry none = {-1, 0, 0, 0};
+  if (i >= m.count) return none;
+  const int k = m.keep[i], last = i > 0 ? m.keep[i - 1] : -1;
+  if (k == i || k == -1) return none;
+  if (k < i || (i > 0 && k <= last) || k >= m.len - m.first) {
     *bad = true;
-    return false;
+    return none;
   }
   const uint32_t src = (uint32_t)(m.first + k), dst = (uint32_t)(m.first + i);
   const uint32_t sp = divide(src, c.page), dp = divide(dst, c.page);
   const int32_t s = m.table[sp], d = m.table[dp];
   if (s < 0 || s >= c.pages || d < 0 || d >= c.pages) {
     *bad = true;
-    return false;
+    return none;
   }
-  *from = (int64_t)s * c.heads + head;
-  *to = (int64_t)d * c.heads + head;
-  *from_slot = (int)(src - sp * c.page.by);
-  *to_slot = (int)(dst - dp * c.page.by);
-  return true;
+  return Entry{s, (int)(src - sp * c.page.by), d, (int)(dst - dp * c.page.by)};
 }
 
-// Moves `per` elements of T of every entry's row: element e of a token lies at base + block * stride + slot * row + e.
-template <typename T>
-__device__ __forceinline__ bool move_part(const Cache& c, const Moves& m, int head, uint8_t* base, int64_t stride, int row, int per) {
+// Moves `per` elements of T of every entry's row, `side` threads an entry: element e of a token lies at base + block * stride +
+// slot * row + e.  Returns whether an entry was bad.
+template <typename T, int AHEAD>
+__device__ __forceinline__ bool move_part(const Cache& c, const Moves& m, Entry* list, uint8_t* base, int64_t stride, int row, int per,
+                                          int side) {
   const int tid = threadIdx.x;
-  // elements of a row side by side: 1, 2 or 4 threads an entry, more elements one after the other
-  const int side = per >= 4 ? 4 : per >= 2 ? 2 : 1;
-  const int entry = tid / side, lane = tid % side, entries = kKeepThreads / side;
+  const int entry = tid / side, lane = tid % side, entries = (int)blockDim.x / side, step = entries * AHEAD;
   bool bad = false;
-  for (int e0 = 0; e0 < per; e0 += side) {
-    const int e = e0 + lane;
-    T data[2][kKeepAhead];
-    int64_t to[2][kKeepAhead];
-    auto load = [&](int round, int i0) {
+  for (int i0 = 0; i0 < m.count; i0 += kKeepList) {
+    const int n = min(m.count - i0, kKeepList);
+    __syncthreads();  // (the list before has been used)
+    for (int i = tid; i < n; i += (int)blockDim.x) list[i] = entry_of(c, m, i0 + i, &bad);
+    __syncthreads();
+    for (int e0 = 0; e0 < per; e0 += side) {
+      const int e = e0 + lane;
+      T data[2][AHEAD];
+      int64_t to[2][AHEAD];
+      auto load = [&](int round, int at) {
 #pragma unroll
-      for (int u = 0; u < kKeepAhead; ++u) {
-        int64_t sb, db;
-        int ss, ds;
-        to[round][u] = -1;
-        if (move_of(c, m, i0 + u * entries + entry, head, &sb, &ss, &db, &ds, &bad) && e < per) {
-          data[round][u] = *reinterpret_cast<const T*>(base + sb * stride + (int64_t)ss * row + e * (int)sizeof(T));
-          to[round][u] = db * stride + (int64_t)ds * row + e * (int)sizeof(T);
+        for (int u = 0; u < AHEAD; ++u) {
+          // (what does not move reads the pool's start: a load that may be left out would have all waits be for all loads)
+          const int i = at + u * entries + entry;
+          const Entry x = list[min(i, n - 1)];
+          const bool go = i < n && e < per && x[0] >= 0;
+          const int64_t from = ((int64_t)x[0] * c.heads + m.head) * stride + (int64_t)x[1] * row + e * (int)sizeof(T);
+          data[round][u] = *reinterpret_cast<const T*>(base + (go ? from : 0));
+          to[round][u] = go ? ((int64_t)x[2] * c.heads + m.head) * stride + (int64_t)x[3] * row + e * (int)sizeof(T) : -1;
         }
-      }
-    };
-    auto store = [&](int round) {
+      };
+      auto store = [&](int round) {
 #pragma unroll
-      for (int u = 0; u < kKeepAhead; ++u)
-        if (to[round][u] >= 0) *reinterpret_cast<T*>(base + to[round][u]) = data[round][u];
-    };
-    const int step = entries * kKeepAhead;
-    load(0, 0);
-    for (int i0 = 0; i0 < m.count; i0 += 2 * step) {
-      load(1, i0 + step);
-      __syncthreads();
-      store(0);
-      load(0, i0 + 2 * step);
-      __syncthreads();
-      store(1);
+        for (int u = 0; u < AHEAD; ++u)
+          if (to[round][u] >= 0) *reinterpret_cast<T*>(base + to[round][u]) = data[round][u];
+      };
+      load(0, 0);
+      for (int at = 0; at < n; at += 2 * step) {
+        load(1, at + step);
+        __syncthreads();
+        store(0);
+        load(0, at + 2 * step);
+        __syncthreads();
+        store(1);
+      }
     }
   }
   return bad;
 }
 
+// The scale bytes of a row, as wide as their place allows.
+__device__ __forceinline__ void move_scales(const Cache& c, const Moves& m, Entry* list, uint8_t* base) {
+  if (c.groups % 4 == 0)
+    move_part<uint32_t, 4>(c, m, list, base, c.block, c.groups, c.groups / 4, 1);
+  else if (c.groups % 2 == 0)
+    move_part<uint16_t, 4>(c, m, list, base, c.block, c.groups, c.groups / 2, 1);
+  else
+    move_part<uint8_t, 4>(c, m, list, base, c.block, c.groups, c.groups, 1);
+}
+
 static __global__ __launch_bounds__(kKeepThreads) void k_keep(KeepArgs a) {
   const Cache& c = a.c;
+  __shared__ Entry list[kKeepList];
   int id = blockIdx.x;
   const int part = id % a.parts;
   id /= a.parts;
@@ -126,28 +139,18 @@ static __global__ __launch_bounds__(kKeepThreads) void k_keep(KeepArgs a) {
   }
   m.keep = a.keep + ((int64_t)b * a.lists + (a.lists > 1 ? head : 0)) * a.width;
   m.table = c.table + (int64_t)b * c.max_pages;
+  m.head = head;
   const int chunks = c.row / 16, codes = 2 * a.slices;
   if (part < codes) {
     const bool is_v = part >= a.slices;
     const int slice = is_v ? part - a.slices : part;
-    uint8_t* base = c.pool + (is_v ? c.v_off : 0) + slice * 64;
-    bad |= move_part<u32x4>(c, m, head, base, c.block, c.row, min(4, chunks - slice * 4));
+    uint8_t* base = c.pool + (is_v ? c.v_off : 0) + slice * a.side * 16;
+    bad |= move_part<u32x4, kKeepAhead>(c, m, list, base, c.block, c.row, min(a.side, chunks - slice * a.side), a.side);
   } else if (part == codes && c.groups > 0) {
-    uint8_t* ks = c.pool + c.ks_off;
-    uint8_t* vs = c.pool + c.vs_off;
-    if (c.groups % 4 == 0) {
-      move_part<uint32_t>(c, m, head, ks, c.block, c.groups, c.groups / 4);
-      move_part<uint32_t>(c, m, head, vs, c.block, c.groups, c.groups / 4);
-    } else if (c.groups % 2 == 0) {
-      move_part<uint16_t>(c, m, head, ks, c.block, c.groups, c.groups / 2);
-      move_part<uint16_t>(c, m, head, vs, c.block, c.groups, c.groups / 2);
-    } else {
-      move_part<uint8_t>(c, m, head, ks, c.block, c.groups, c.groups);
-      move_part<uint8_t>(c, m, head, vs, c.block, c.groups, c.groups);
-    }
+    move_scales(c, m, list, c.pool + c.ks_off);
+    move_scales(c, m, list, c.pool + c.vs_off);
   } else {
-    uint8_t* w = reinterpret_cast<uint8_t*>(a.weights);
-    move_part<uint32_t>(c, m, head, w, (int64_t)c.page.by * 4, 4, 1);
+    move_part<uint32_t, 4>(c, m, list, reinterpret_cast<uint8_t*>(a.weights), (int64_t)c.page.by * 4, 4, 1, 1);
   }
   if (a.err && part == 0 && __syncthreads_or(bad) && threadIdx.x == 0) atomicAdd(a.err, 1);
 }

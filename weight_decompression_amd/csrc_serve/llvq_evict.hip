@@ -176,11 +176,14 @@ LLVQ_API int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, con
   a.width = width;
   a.from_new = batch->starts != nullptr;
   a.err = err_count;
-  a.slices = (c.row + 63) / 64;
+  // 128 bytes of a row a workgroup where that fills the chip, so that no two of them share a line; else 64
+  const int64_t seqs = (int64_t)c.batch * c.heads;
+  a.side = seqs * 2 * ((c.row + 127) / 128) >= 128 && c.row > 64 ? 8 : 4;
+  a.slices = (c.row / 16 + a.side - 1) / a.side;
   a.parts = 2 * a.slices + (c.groups > 0) + (weights != nullptr);
-  const int64_t grid = (int64_t)c.batch * c.heads * a.parts;
+  const int64_t grid = seqs * a.parts;
   if (grid * kKeepThreads >= (1ll << 32)) return LLVQ_EINVAL;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(k_keep, dim3((unsigned)grid), dim3(kKeepThreads), 0, s, a);
+  hipLaunchKernelGGL(k_keep, dim3((unsigned)grid), dim3(width <= 32 ? 256 : kKeepThreads), 0, s, a);
   return launch_status();
 }
