@@ -557,7 +557,7 @@ int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const llvq_batch
  *   counts  : [batch] or NULL (width for all).
  *   err_count : nullable; + 1 for a (sequence, key head) with an entry that is out of order or past the length, or a page number
  *             outside the pool (the entry moves nothing), with a count, starts or a length that had to be cut.
- * No page may belong to two sequences of the call.  batch * kv_heads * (head_dim / 16 + 2) below 2^23.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+ * No page may belong to two sequences of the call.  batch * kv_heads * (head_dim / 32 + 4) below 2^22.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, const llvq_batch* batch, const int32_t* keep, int32_t lists,
                  int32_t width, const int32_t* counts, int32_t* err_count, void* stream);
 

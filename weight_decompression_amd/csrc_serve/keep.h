@@ -3,7 +3,7 @@
 //
 // What moves is read once and written once; HBM bounds it for long lists, the launch for short ones.  A token's parts (key and
 // value codes, their scale bytes, its weight) never meet, so a workgroup has one part of a (sequence, key head), of the
-// codes 64 or 128 bytes of each row, and takes the list in order, a batch of entries at a time: all of a batch is read, then, after
+// codes 64 to 256 bytes of each row, and takes the list in order, a batch of entries at a time: all of a batch is read, then, after
 // a barrier, written.  That is enough for moves in place: keep[i] >= i, so what a batch writes (its own i) lies before
 // anything that later batches read (at or past their own, larger i), and what earlier batches read is past the barrier.  The
 // loads of the next batch are under way while a batch is written.  Where entries lie is worked out for 1024 at a time, into LDS:
@@ -26,7 +26,7 @@ struct KeepArgs {
   int32_t parts;          // workgroups a (sequence, key head): slices of keys, slices of values, scales, weights
 };
 
-constexpr int kKeepThreads = 512, kKeepAhead = 8, kKeepList = 1024;
+constexpr int kKeepThreads = 1024, kKeepAhead = 4, kKeepList = 1024;
 
 // The list of a (sequence, key head), and where its entries lie: (page * heads + head) and slot, from and to (-1: nothing moves).
 struct Moves {

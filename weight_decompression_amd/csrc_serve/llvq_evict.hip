@@ -176,9 +176,11 @@ LLVQ_API int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, con
   a.width = width;
   a.from_new = batch->starts != nullptr;
   a.err = err_count;
-  // 128 bytes of a row a workgroup where that fills the chip, so that no two of them share a line; else 64
+  // A workgroup takes whole rows of up to 256 bytes where that leaves 128 workgroups, else 128 bytes: half a line each costs
+  // more than the workgroups bring (8 x 8 heads, 256 bytes: 128 us whole, 134 in halves, 161 in quarters; 4 x 8 heads 92, 66
+  // and 109)
   const int64_t seqs = (int64_t)c.batch * c.heads;
-  a.side = seqs * 2 * ((c.row + 127) / 128) >= 128 && c.row > 64 ? 8 : 4;
+  a.side = c.row <= 64 ? 4 : c.row > 128 && seqs * 2 * ((c.row + 255) / 256) >= 128 ? 16 : 8;
   a.slices = (c.row / 16 + a.side - 1) / a.side;
   a.parts = 2 * a.slices + (c.groups > 0) + (weights != nullptr);
   const int64_t grid = seqs * a.parts;
