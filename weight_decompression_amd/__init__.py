@@ -694,24 +694,40 @@ def tree_verify(target, starts, tokens, parents, uniforms, noise, accepted, path
     import torch
     call = "llvq_tree_verify"
     i32, f32 = torch.int32, torch.float32
-    dtype = target.dtype if isinstance(target, torch.Tensor) else None
-    at = _buffer(target, call, "target")
-    if dtype is not f32 and dtype is not torch.bfloat16:
-        raise TypeError(f"{call}: target must have dtype torch.float32 or torch.bfloat16, got {dtype}")
-    _buffer(noise, call, "noise", f32)
-    _buffer(path, call, "path", i32)
-    if target.dim() != 2 or noise.dim() != 2 or path.dim() != 2:
-        raise ValueError(f"{call}: target, noise and path must be [nodes][vocab], [B][vocab] and [B][width], got "
-                         f"{tuple(target.shape)}, {tuple(noise.shape)} and {tuple(path.shape)}")
-    (n, v), (b, width), device = target.shape, path.shape, target.get_device()
-    each = [_vector(t, call, name, kind, shape, device) for t, name, kind, shape in (
-        (starts, "starts", i32, (b + 1,)), (tokens, "tokens", i32, (n,)), (parents, "parents", i32, (n,)),
-        (uniforms, "uniforms", f32, (n,)), (noise, "noise", f32, (b, v)), (accepted, "accepted", i32, (b,)),
-        (path, "path", i32, (b, width)), (out, "out", i32, (b, width)))]
-    ws, size = _space(workspace, device, call)
+    try:
+        (n, v), (b, width), dtype, device = target.shape, path.shape, target.dtype, target.get_device()
+        good = (0 <= device == starts.get_device() == tokens.get_device() == parents.get_device() == uniforms.get_device() ==
+                noise.get_device() == accepted.get_device() == path.get_device() == out.get_device() == workspace.get_device() and
+                (dtype is f32 or dtype is torch.bfloat16) and starts.dtype is i32 and tokens.dtype is i32 and parents.dtype is i32 and
+                uniforms.dtype is f32 and noise.dtype is f32 and accepted.dtype is i32 and path.dtype is i32 and out.dtype is i32 and
+                starts.shape == (b + 1,) and tokens.shape == parents.shape == uniforms.shape == (n,) and noise.shape == (b, v) and
+                accepted.shape == (b,) and out.shape == (b, width) and target.is_contiguous() and starts.is_contiguous() and
+                tokens.is_contiguous() and parents.is_contiguous() and uniforms.is_contiguous() and noise.is_contiguous() and
+                accepted.is_contiguous() and path.is_contiguous() and out.is_contiguous() and workspace.is_contiguous())
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        dtype = target.dtype if isinstance(target, torch.Tensor) else None
+        _buffer(target, call, "target")
+        if dtype is not f32 and dtype is not torch.bfloat16:
+            raise TypeError(f"{call}: target must have dtype torch.float32 or torch.bfloat16, got {dtype}")
+        _buffer(noise, call, "noise", f32)
+        _buffer(path, call, "path", i32)
+        if target.dim() != 2 or noise.dim() != 2 or path.dim() != 2:
+            raise ValueError(f"{call}: target, noise and path must be [nodes][vocab], [B][vocab] and [B][width], got "
+                             f"{tuple(target.shape)}, {tuple(noise.shape)} and {tuple(path.shape)}")
+        (n, v), (b, width), device = target.shape, path.shape, target.get_device()
+        for t, name, kind, shape in (
+                (starts, "starts", i32, (b + 1,)), (tokens, "tokens", i32, (n,)), (parents, "parents", i32, (n,)),
+                (uniforms, "uniforms", f32, (n,)), (noise, "noise", f32, (b, v)), (accepted, "accepted", i32, (b,)),
+                (path, "path", i32, (b, width)), (out, "out", i32, (b, width))):
+            _vector(t, call, name, kind, shape, device)
+        _space(workspace, device, call)
+    size = workspace.numel() * workspace.element_size()
     err = None if err_count is None else _count(err_count, device, call)
-    code = _launch(load_library().llvq_tree_verify, device, stream, at, X_F32 if dtype is f32 else X_BF16, *each[:5], b, n, v, width,
-                   *each[5:], ws, size, err)
+    code = _launch(load_library().llvq_tree_verify, device, stream, target.data_ptr(), X_F32 if dtype is f32 else X_BF16,
+                   starts.data_ptr(), tokens.data_ptr(), parents.data_ptr(), uniforms.data_ptr(), noise.data_ptr(), b, n, v, width,
+                   accepted.data_ptr(), path.data_ptr(), out.data_ptr(), workspace.data_ptr(), size, err)
     if code:
         need = tree_workspace_bytes(b, v)
         if size < need:
@@ -731,11 +747,18 @@ def _lists(lens, table, starts, device, call):
     """llvq_batch of lens [B], table [B][max_pages] and, if any, starts [B + 1] (int32)."""
     import torch
     i32 = torch.int32
-    _buffer(lens, call, "lens", i32)
-    _buffer(table, call, "table", i32)
-    if starts is not None:
-        _buffer(starts, call, "starts", i32)
-    _one_device(call, device, lens, table, *(() if starts is None else (starts,)))
+    try:
+        good = (lens.get_device() == table.get_device() == device and lens.dtype is i32 and table.dtype is i32 and
+                lens.is_contiguous() and table.is_contiguous() and
+                (starts is None or (starts.get_device() == device and starts.dtype is i32 and starts.is_contiguous())))
+    except AttributeError:
+        good = False
+    if not good:
+        _buffer(lens, call, "lens", i32)
+        _buffer(table, call, "table", i32)
+        if starts is not None:
+            _buffer(starts, call, "starts", i32)
+        _one_device(call, device, lens, table, *(() if starts is None else (starts,)))
     n, shape = lens.shape, table.shape
     if len(n) != 1 or len(shape) != 2 or shape[0] != n[0] or (starts is not None and starts.shape != (n[0] + 1,)):
         raise ValueError(f"{call}: lens, table and starts must be [B], [B][max_pages] and [B + 1] or None, got {tuple(n)}, {tuple(shape)} "

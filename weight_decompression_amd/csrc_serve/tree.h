@@ -94,7 +94,8 @@ __device__ __forceinline__ Walk walk_of(const TreeArgs& a, int b) {
 }
 
 // A workgroup's best of entries [from, end) of the row, in every thread.  The refused tokens are looked for only where an
-// entry may be the best so far.
+// entry may be the best so far and shares its last six bits with one of them: the first entries of every thread may all be
+// (without the bits, 96 trees of up to 32 nodes over 100003 entries take 31 us instead of 24).
 template <bool F32, int THREADS>
 __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Walk& w, bool without, int64_t from, int64_t end) {
   constexpr int kAhead = THREADS == 1024 ? 16 : 8;
@@ -105,7 +106,11 @@ __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Wa
   __syncthreads();  // (an earlier call's shared values have been read)
   if (tid < kWave && (w.refused >> tid & 1)) gone[__popcll(w.refused & ((1ull << tid) - 1))] = w.token;
   __syncthreads();
+  uint64_t bits = without && (w.refused >> (tid & 63) & 1) ? 1ull << (w.token & 63) : 0;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) bits |= (uint64_t)__shfl_xor((unsigned long long)bits, d);
   auto refused = [&](int v) {
+    if (!(bits >> (v & 63) & 1)) return false;
     for (int i = 0; i < many; ++i)
       if (gone[i] == v) return true;
     return false;
@@ -116,13 +121,16 @@ __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Wa
     float p[kAhead], e[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int64_t v = v0 + THREADS * i;
-      p[i] = v < end ? prob<F32>(a.target, w.row + v) : 0.0f;
-      e[i] = v < end ? noise[v] : 1.0f;
+      const int64_t v = min(v0 + THREADS * i, end - 1);  // (loads that may be left out would be waited for one by one)
+      p[i] = prob<F32>(a.target, w.row + v);
+      e[i] = noise[v];
     }
     bool any = false;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) any |= mine.may(p[i], e[i]);
+    for (int i = 0; i < kAhead; ++i) {
+      p[i] = v0 + THREADS * i < end ? p[i] : 0.0f;
+      any |= mine.may(p[i], e[i]);
+    }
     if (any) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
