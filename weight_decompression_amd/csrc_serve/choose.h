@@ -3,9 +3,9 @@
 //
 // One workgroup a (sequence, key head), which holds the weights of up to 32768 (or 4096) places in registers as 32-bit numbers
 // of the same order.  The smallest that stays is found digit by digit from the top (11, 11 and 10 bits: a histogram in LDS, its
-// sums from the top, the bin that the wanted count falls into); everything above it stays, of its equals the first.  The
-// places are then written in order: each wave counts its 64 places of every round of 1024, one scan over all of these counts
-// tells each wave where it writes.  Nothing is sorted, and the order of the histogram's atomics changes nothing.
+// sums from the top, the bin that the wanted count falls into); everything above it stays, of its equals the first.  A wave
+// holds consecutive places, 64 a round, so the places that stay are written in order after one scan over the waves' counts.
+// Nothing is sorted, and the order of the histogram's atomics changes nothing.
 #pragma once
 
 #include "serve_common.h"
@@ -28,39 +28,33 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
+constexpr uint32_t kAlways = 0xffffffffu, kNever = 0;  // of places that stay in any case, and of none: no weight has these
+
 constexpr int kChooseThreads = 1024, kChooseWaves = kChooseThreads / kWave;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
 
-// Exclusive sums over the workgroup of one number a thread, in the threads' order; *all: the sum of all.  A T may hold two
-// counts side by side.
-template <typename T>
-__device__ __forceinline__ T scan_block(T x, T* waves, T* all) {
+// Exclusive sums over the workgroup of one number a thread, in the threads' order.
+__device__ __forceinline__ int scan_block(int x, int* waves) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  T sum = x;
+  int sum = x;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
-    const T y = __shfl_up(sum, d);
+    const int y = __shfl_up(sum, d);
     if (lane >= d) sum += y;
   }
   if (lane == kWave - 1) waves[wave] = sum;
   __syncthreads();
-  T before = 0, total = 0;
+  int before = 0;
 #pragma unroll
-  for (int i = 0; i < kChooseWaves; ++i) {
-    const T w = waves[i];
-    before += i < wave ? w : 0;
-    total += w;
-  }
-  *all = total;
+  for (int i = 0; i < kChooseWaves; ++i) before += i < wave ? waves[i] : 0;
   return before + sum - x;
 }
 
 // HELD: places a thread holds.  LONG: sequences that pass that are read again for each digit, HELD rounds at a time.
 template <int HELD, bool LONG>
 __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
-  using Pair = unsigned long long;  // places that stay for sure, and from bit 32 on those equal to the least
   __shared__ int bins[kBins], waves[3][kChooseWaves], found[3][2];
-  __shared__ Pair counts[HELD * kChooseWaves], pair_waves[kChooseWaves];
+  __shared__ int sure_of[2][kChooseWaves], same_of[2][kChooseWaves];  // (two: a wave may be a block of rounds ahead)
   const Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = (int)blockIdx.x % c.heads, b = (int)blockIdx.x / c.heads;
@@ -83,13 +77,15 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
   int want = a.budget - a.sinks - a.recent;
   uint32_t held[HELD];
   const int rounds = (len + kChooseThreads - 1) / kChooseThreads;
-  // all page numbers, then all weights under way at once (past the last place: that one's again)
+  // A block of up to HELD rounds from r0 on: this thread's place in round i, and all their numbers.  All page numbers, then
+  // all weights are under way at once (past the last place: that one's again).
+  auto place_of = [&](int r0, int i) { return r0 * kChooseThreads + (wave * min(rounds - r0, HELD) + i) * kWave + lane; };
   auto hold = [&](int r0) {
     int32_t ids[HELD];
     int slots[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const uint32_t j = (uint32_t)min((r0 + i) * kChooseThreads + tid, len - 1), page = divide(j, c.page);
+      const uint32_t j = (uint32_t)min(place_of(r0, i), len - 1), page = divide(j, c.page);
       slots[i] = (int)(j - page * c.page.by);
       ids[i] = table[page];
     }
@@ -102,10 +98,14 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
       if (!ok) slots[i] = -1;
     }
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) held[i] = order_of(slots[i] < 0 ? -INFINITY : w[i]);  // (no place counts as NaN does)
+    for (int i = 0; i < HELD; ++i) {
+      const int j = place_of(r0, i);
+      const uint32_t u = order_of(slots[i] < 0 ? -INFINITY : w[i]);  // (no page counts as NaN does)
+      held[i] = i >= rounds - r0 || j >= len ? kNever : j < low || j >= high ? kAlways : u;
+    }
   };
   if (!LONG) hold(0);
-  uint32_t least = 0xffffffffu;  // the least that stays (nothing between does where nothing is wanted)
+  uint32_t least = kAlways - 1;  // the least that stays (nothing between does where nothing is wanted)
   if (want > 0) {
     uint32_t known = 0;  // digits found so far
     least = 0;
@@ -115,20 +115,17 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
       const uint32_t mask = digit == 2 ? 1023u : 2047u;
       for (int i = tid; i < kBins; i += kChooseThreads) bins[i] = 0;
       __syncthreads();
-      auto count = [&](int j, uint32_t u) {
-        if (j >= low && j < high && (u & known) == least) atomicAdd(&bins[u >> shift & mask], 1);
-      };
       for (int r0 = 0; r0 < (LONG ? rounds : 1); r0 += HELD) {
         if (LONG) hold(r0);
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
-          if (r0 + i < rounds) count((r0 + i) * kChooseThreads + tid, held[i]);
+          if (i < rounds - r0 && (held[i] & known) == least && (digit > 0 || (held[i] != kNever && held[i] != kAlways)))
+            atomicAdd(&bins[held[i] >> shift & mask], 1);
       }
       __syncthreads();
       // two bins a thread, from the top
       const int top = kBins - 1 - 2 * tid, first = bins[top], second = bins[top - 1];
-      int all;
-      const int above = scan_block(first + second, waves[digit], &all);
+      const int above = scan_block(first + second, waves[digit]);
       if (above < want && want <= above + first) found[digit][0] = top, found[digit][1] = want - above;
       if (above + first < want && want <= above + first + second) found[digit][0] = top - 1, found[digit][1] = want - above - first;
       __syncthreads();
@@ -138,52 +135,45 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
     }
   }
   // the places in order, HELD rounds at a time; `want` of those equal to the least stay
-  Pair before = 0;
-  auto of = [&](int j, uint32_t u, uint64_t* sure, uint64_t* same) {
-    const bool between = j >= low && j < high;
-    *sure = __ballot(j < len && (!between || u > least));
-    *same = __ballot(between && u == least && want > 0);
-  };
-  for (int r0 = 0; r0 < (LONG ? rounds : 1); r0 += HELD) {
+  int sure_before = 0, same_before = 0;
+  for (int r0 = 0, turn = 0; r0 < (LONG ? rounds : 1); r0 += HELD, turn ^= 1) {
     if (LONG) hold(r0);
+    int sure = 0, same = 0;  // of this wave
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      if (r0 + i < rounds) {
-        uint64_t sure, same;
-        of((r0 + i) * kChooseThreads + tid, held[i], &sure, &same);
-        if (lane == 0) counts[i * kChooseWaves + wave] = (Pair)__popcll(sure) | (Pair)__popcll(same) << 32;
-      } else if (lane == 0) {
-        counts[i * kChooseWaves + wave] = 0;
+      if (i < rounds - r0) {
+        sure += __popcll(__ballot(held[i] > least));
+        same += __popcll(__ballot(held[i] == least));
       }
     }
+    if (lane == 0) sure_of[turn][wave] = sure, same_of[turn][wave] = same;
     __syncthreads();
-    constexpr int kEach = (HELD * kChooseWaves + kChooseThreads - 1) / kChooseThreads;
-    static_assert(kEach == 1, "a thread has one count");
+    int sure_at = sure_before, same_at = same_before;
+#pragma unroll
+    for (int i = 0; i < kChooseWaves; ++i) {
+      const int x = sure_of[turn][i], y = same_of[turn][i];
+      sure_at += i < wave ? x : 0;
+      same_at += i < wave ? y : 0;
+      sure_before += x;
+      same_before += y;
+    }
+    sure_at = __builtin_amdgcn_readfirstlane(sure_at);
+    same_at = __builtin_amdgcn_readfirstlane(same_at);
     // (the masks are made again: kept, they would take more registers than there are)
 #pragma unroll
     for (int i = 0; i < HELD; ++i) asm volatile("" : "+v"(held[i]));
-    Pair all;
-    const Pair mine = tid < HELD * kChooseWaves ? counts[tid] : 0, at = before + scan_block(mine, pair_waves, &all);
-    if (tid < HELD * kChooseWaves) counts[tid] = at;
-    before += all;
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      if (r0 + i < rounds) {
-        const int j = (r0 + i) * kChooseThreads + tid;
-        uint64_t sure, same;
-        of(j, held[i], &sure, &same);
-        const Pair from = counts[i * kChooseWaves + wave];
-        const int same_before = (int)(from >> 32);
-        const uint64_t below = (1ull << lane) - 1;
-        // of the equals of this wave and round, the first few
-        const bool taken = (same >> lane & 1) && same_before + __popcll(same & below) < want;
-        const bool stays = (sure >> lane & 1) || taken;
-        const int place = (int)(uint32_t)from + min(same_before, want) + __popcll(__ballot(stays) & below);
-        if (stays && place < a.budget) keep[place] = j;
+      if (i < rounds - r0) {
+        const uint64_t above = __ballot(held[i] > least), equal = __ballot(held[i] == least), below = (1ull << lane) - 1;
+        // of the equals the first `want`: those before this lane, all of them kept, move it on
+        const int mine = sure_at + __popcll(above & below), equals = same_at + __popcll(equal & below);
+        const int at = mine + min(equals, want);
+        if (((above >> lane & 1) || ((equal >> lane & 1) && equals < want)) && at < a.budget) keep[at] = place_of(r0, i);
+        sure_at += __popcll(above);
+        same_at += __popcll(equal);
       }
     }
-    __syncthreads();
   }
   if (a.err && __any(lost) && lane == 0) atomicAdd(a.err, 1);
 }
