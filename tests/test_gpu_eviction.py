@@ -136,6 +136,58 @@ def test_weights_of_every_type_and_width(kind, dim, dtype, new):
     assert torch.equal(weights, other)
 
 
+# name: (sequences, key heads, query heads of each, most new tokens, longest length)
+FORMS = {
+    "up to 16 rows, many pieces a wave": (70, 8, 4, 4, 1500),
+    "up to 32 rows": (40, 8, 4, 8, 400),
+    "many rows, a wave's own keys": (33, 8, 3, 70, 600),
+    "many rows, a team's keys": (3, 2, 5, 70, 900),
+    "many rows, heads that 64 rows do not hold whole": (2, 1, 96, 9, 500),
+}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 256])
+def test_weights_in_every_form(form, kind, dim):
+    """Every form in which the call is launched, at sizes that select it; some sequences against the oracle."""
+    batch, kv_heads, share, chunk, longest = FORMS[form]
+    rng = np.random.RandomState(dim + len(form))
+    lens = rng.randint(1, longest + 1, batch)
+    new = np.minimum(rng.randint(1, chunk + 1, batch), lens)
+    lens[0], new[0] = longest, chunk
+    lens[1], new[1] = chunk - 1, chunk                     # a row that sees nothing
+    page = int(rng.choice([7, 16, 48]))
+    su = Setup(kind, kv_heads, dim, page, new.tolist(), lens.tolist(), seed=dim, max_pages=-(-max(longest, chunk) // page) + 1)
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    k, v = (torch.randn(int(lens.sum()), kv_heads, dim, device="cuda", generator=gen) for _ in range(2))
+    ends = np.concatenate(([0], np.cumsum(lens)))
+    wd.kv_write(su.desc, su.pool, k, v, *su.plan(starts=ends))
+    sample = sorted({0, 1, batch // 2, batch - 1})
+    caches = [(sv.held(k[ends[b]:ends[b + 1]].cpu().numpy(), su.kind), None) if b in sample else None for b in range(batch)]
+    for dtype in (torch.bfloat16, torch.float32):
+        q = (1.5 * torch.randn(int(new.sum()), kv_heads * share, dim, device="cuda", generator=gen)).to(dtype)
+        q64 = f64(q)
+        for window, causal in ((0, True), (29, True), (0, False)):
+            _, lse = run_lse(su, q, window, causal)
+            before = torch.rand(su.pages, kv_heads, page, device="cuda", generator=gen)
+            weights, err = before.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+            run_weigh(su, weights, q, lse, window, causal, err=err)
+            again = before.clone()
+            run_weigh(su, again, q, lse, window, causal)
+            assert err.item() == 0 and torch.equal(weights, again)
+            old, got, lse64 = f64(before), f64(weights), f64(lse)
+            for b in sample:
+                a, e, m = su.starts[b], su.starts[b + 1], int(lens[b])
+                see = seen(e - a, m, window, causal)
+                sums, slack = ev.weigh(q64[a:e], caches[b][0], np.where(np.isfinite(lse64[a:e]), lse64[a:e], 0.0), see, 1.0 / math.sqrt(dim))
+                page_at, slot = places(su, b, m)
+                want = np.where((np.arange(m) >= m - (e - a))[:, None], 0.0, old[page_at, :, slot]) + sums
+                bound = slack + sums * ((e - a) * share + 8) * 2.0 ** -24 + 2.0 ** -24 * np.abs(want)
+                ok = bool((np.abs(got[page_at, :, slot] - want) <= bound).all())
+                assert ok, (b, (np.abs(got[page_at, :, slot] - want) - bound).max())
+
+
 @pytest.mark.parametrize("new", [1, 64, 200])
 def test_each_row_gives_a_weight_of_one_in_all(new):
     su = Setup("fp8", 2, 128, 16, [new, 1], [700, 90], seed=41)

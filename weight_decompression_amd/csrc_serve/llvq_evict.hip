@@ -18,22 +18,29 @@ LLVQ_API int llvq_attn_lse(const llvq_kv_desc* d, const void* pool, const void* 
 
 namespace {
 
-// Row tiles of 16 that the kernel for few rows takes (0: the kernel for many), workgroups that share out a sequence's keys.
+// Row tiles of 16 that the kernel for few rows takes (0: the kernel for many), waves that share out the rows of the same keys
+// there, workgroups that share out a sequence's keys.
 struct WeighCut {
-  int tiles, groups;
+  int tiles, team, groups;
 };
 
 inline WeighCut weigh_cut(int64_t rows, int dim, bool f32, int64_t seqs, int32_t max_len) {
   WeighCut w;
+  w.team = 1;
   w.tiles = rows <= 16 ? 1 : rows <= 32 && !(f32 && dim > 128) ? 2 : 0;
   const int64_t pieces = ((int64_t)max_len + 127) / 128;  // of four waves
   if (w.tiles) {
     // up to 16 pieces a wave, fewer while that leaves places on the chip empty
-    int64_t each = pieces * seqs / 2048;
+    int64_t each = pieces * seqs / 1024;
     each = each < 1 ? 1 : each > 16 ? 16 : each;
     w.groups = (int)((pieces + each - 1) / each);
   } else {
     w.groups = (int)(dim <= 128 ? (pieces + 1) / 2 : pieces);
+    // Where 256 keys a workgroup leave compute units idle, its waves share out the rows of 64 (2048 tokens of 32 heads over 8
+    // of 128 channels in e4m3, their own keys: 64 workgroups 174 us, 256 of a quarter 73; 1024 over 4096: 128 99 us, 53; 2048 over
+    // 8192: 256 177 us, 180)
+    w.team = w.groups * seqs >= 256 ? 1 : !f32 ? 4 : dim <= 128 ? 2 : 1;
+    w.groups *= w.team;
   }
   // (a launch has fewer than 2^32 threads)
   const int64_t most = ((1ll << 24) - 1) / seqs;
@@ -42,30 +49,37 @@ inline WeighCut weigh_cut(int64_t rows, int dim, bool f32, int64_t seqs, int32_t
 }
 
 template <int KIND, int DP, int NT>
-int launch_weigh_nt(const WeighArgs& a, int tiles, hipStream_t s) {
+int launch_weigh_nt(const WeighArgs& a, const WeighCut& cut, hipStream_t s) {
   const dim3 grid((unsigned)a.units);
   if constexpr (NT == 1 || DP <= 128) {
-    if (tiles == 2) {
+    if (cut.tiles == 2) {
       hipLaunchKernelGGL((k_weigh_few<KIND, DP, NT, 2>), grid, dim3(256), 0, s, a);
       return launch_status();
     }
   }
-  if (tiles == 1)
+  constexpr int kTeam = NT == 1 ? 4 : 2;
+  if constexpr (NT == 1 || DP <= 128) {
+    if (cut.tiles == 0 && cut.team > 1) {
+      hipLaunchKernelGGL((k_weigh_many<KIND, DP, NT, kTeam>), grid, dim3(256), 0, s, a);
+      return launch_status();
+    }
+  }
+  if (cut.tiles == 1)
     hipLaunchKernelGGL((k_weigh_few<KIND, DP, NT, 1>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_weigh_many<KIND, DP, NT>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_weigh_many<KIND, DP, NT, 1>), grid, dim3(256), 0, s, a);
   return launch_status();
 }
 template <int KIND, int DP>
-int launch_weigh(const WeighArgs& a, bool f32, int tiles, hipStream_t s) {
-  return f32 ? launch_weigh_nt<KIND, DP, 3>(a, tiles, s) : launch_weigh_nt<KIND, DP, 1>(a, tiles, s);
+int launch_weigh(const WeighArgs& a, bool f32, const WeighCut& cut, hipStream_t s) {
+  return f32 ? launch_weigh_nt<KIND, DP, 3>(a, cut, s) : launch_weigh_nt<KIND, DP, 1>(a, cut, s);
 }
 template <int KIND>
-int launch_weigh_dim(const WeighArgs& a, bool f32, int tiles, hipStream_t s) {
+int launch_weigh_dim(const WeighArgs& a, bool f32, const WeighCut& cut, hipStream_t s) {
   switch (padded_dim(a.c.dim)) {
-    case 64: return launch_weigh<KIND, 64>(a, f32, tiles, s);
-    case 128: return launch_weigh<KIND, 128>(a, f32, tiles, s);
-    default: return launch_weigh<KIND, 256>(a, f32, tiles, s);
+    case 64: return launch_weigh<KIND, 64>(a, f32, cut, s);
+    case 128: return launch_weigh<KIND, 128>(a, f32, cut, s);
+    default: return launch_weigh<KIND, 256>(a, f32, cut, s);
   }
 }
 
@@ -120,9 +134,9 @@ LLVQ_API int llvq_kv_weigh(const llvq_kv_desc* d, const void* pool, float* weigh
   a.units = (int32_t)(seqs * cut.groups);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (d->kind) {
-    case LLVQ_KV_BF16: return launch_weigh_dim<LLVQ_KV_BF16>(a, f32, cut.tiles, s);
-    case LLVQ_KV_FP8: return launch_weigh_dim<LLVQ_KV_FP8>(a, f32, cut.tiles, s);
-    default: return launch_weigh_dim<LLVQ_KV_FP4>(a, f32, cut.tiles, s);
+    case LLVQ_KV_BF16: return launch_weigh_dim<LLVQ_KV_BF16>(a, f32, cut, s);
+    case LLVQ_KV_FP8: return launch_weigh_dim<LLVQ_KV_FP8>(a, f32, cut, s);
+    default: return launch_weigh_dim<LLVQ_KV_FP4>(a, f32, cut, s);
   }
 }
 

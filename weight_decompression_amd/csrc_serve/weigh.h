@@ -282,18 +282,21 @@ __global__ __launch_bounds__(256) void k_weigh_few(WeighArgs a) {
 
 // Many rows.  A workgroup's four waves hold 64 keys each (32 of wide heads) and walk the rows that see them, in blocks that the
 // workgroup stages in LDS: a block's rows are loaded while the one before is worked on, and written to the other buffer after it.
-template <int DP, int NT>
+// TEAM: waves that hold the same keys and share out a block's rows, 32 each, for few keys and heads: they leave compute units
+// idle, and the rows are a long way.
+template <int DP, int NT, int TEAM>
 struct WeighShape {
   static constexpr int kTiles = DP <= 128 ? 2 : 1;     // of 32 keys that a wave holds
-  static constexpr int kKeys = 4 * 32 * kTiles;        // of a workgroup
-  static constexpr int kSub = NT == 1 ? 2 : 1;         // pieces of 32 rows of a block
-  static constexpr int kRows = 32 * kSub;
+  static constexpr int kKeys = 4 / TEAM * 32 * kTiles; // of a workgroup
+  static constexpr int kSub = NT == 1 && TEAM == 1 ? 2 : 1;  // pieces of 32 rows of a block that a wave takes
+  static constexpr int kRows = 32 * kSub * TEAM;
   static constexpr int kRow = DP * 2 + 16;             // bytes of a row in LDS, padded as attention's keys are
+  static constexpr int kWaves = 4 * NT * kRows * kRow > 150 * 1024 ? 1 : 2;  // a SIMD, by two workgroups' double buffers
 };
 
-template <int KIND, int DP, int NT>
-__global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_many(WeighArgs a) {
-  using Sh = WeighShape<DP, NT>;
+template <int KIND, int DP, int NT, int TEAM>
+__global__ __launch_bounds__(256, (WeighShape<DP, NT, TEAM>::kWaves)) void k_weigh_many(WeighArgs a) {
+  using Sh = WeighShape<DP, NT, TEAM>;
   using Key = KeyPlace<KIND, DP>;
   constexpr int kSteps = DP / 16, kTiles = Sh::kTiles, kSub = Sh::kSub, kRows = Sh::kRows;
   constexpr int kOf = KIND == LLVQ_KV_BF16 ? 1 : KIND == LLVQ_KV_FP8 ? 2 : 4;  // steps of a 16-byte chunk
@@ -306,7 +309,7 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
   __shared__ __align__(16) int lo_lds[3][kRows], many_lds[3][kRows];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), mate = wave % TEAM;  // (which of a team's waves)
   const int half = lane >> 5, col = lane & 31;
   int id = blockIdx.x;
   const int head = id % c.heads;
@@ -317,10 +320,11 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
   if (a.err && tid == 0 && head == 0 && tile0 == 0 && (s.bad || s.n > a.max_rows)) atomicAdd(a.err, 1);
   if (s.n == 0) return;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  __shared__ float mates[TEAM == 1 ? 1 : 4][TEAM == 1 ? 1 : 32 * kTiles];
   bool lost = false;
 
   for (int tile = tile0; (int64_t)tile * Sh::kKeys < s.len; tile += a.tiles) {
-    const int first_key = tile * Sh::kKeys, key0 = first_key + wave * 32 * kTiles;
+    const int first_key = tile * Sh::kKeys, key0 = first_key + wave / TEAM * 32 * kTiles;
     const int last_key = min(first_key + Sh::kKeys, s.len) - 1;
     // the tokens that see any key of the workgroup's: [t0, t1)
     const int t0 = a.causal ? max(first_key - text, 0) : 0;
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n) {
           const bf16x8 qf = *reinterpret_cast<const bf16x8*>(
-              &rows_lds[buffer][n][(sub * 32 + col) * Sh::kRow + channel_of<KIND, 2>(st, half) * 2]);
+              &rows_lds[buffer][n][((sub + mate) * 32 + col) * Sh::kRow + channel_of<KIND, 2>(st, half) * 2]);
 #pragma unroll
           for (int u = 0; u < kTiles; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf, k[u][st], sc[u], 0, 0, 0);
         }
@@ -451,7 +455,7 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
     auto weigh = [&](auto all, int slot, int sub, const f32x16* sc) {
 #pragma unroll
       for (int i4 = 0; i4 < 4; ++i4) {
-        const int r = sub * 32 + i4 * 8 + half * 4;
+        const int r = (sub + mate) * 32 + i4 * 8 + half * 4;
         const f32x4 l = *reinterpret_cast<const f32x4*>(&lse_lds[slot][r]);
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) {
@@ -542,7 +546,7 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
           products(buffer, sub, scores[kSub == 1 ? 0 : sub & 1]);
           before = kMasked;
           if (kSub == 1) {
-            if (whole(block * kRows))
+            if (whole(block * kRows + mate * 32))
               weigh(std::true_type(), slot, 0, scores[0]);
             else
               weigh(std::false_type(), slot, 0, scores[0]);
@@ -556,11 +560,24 @@ __global__ __launch_bounds__(256, NT == 3 && DP == 256 ? 1 : 2) void k_weigh_man
     }
     if (kSub > 1 && before != kNone) weigh(std::false_type(), slot_before, kSub - 1, scores[(kSub - 1) & 1]);
     // what the new tokens' places held is of earlier tokens
+    float got[kTiles];
 #pragma unroll
-    for (int u = 0; u < kTiles; ++u) {
-      const float got = half_sum((sum[u][0] + sum[u][1]) + (sum[u][2] + sum[u][3]));
-      if (half == 0 && to[u]) *to[u] = old[u] + got;
+    for (int u = 0; u < kTiles; ++u) got[u] = half_sum((sum[u][0] + sum[u][1]) + (sum[u][2] + sum[u][3]));
+    if constexpr (TEAM > 1) {  // the team's sums, in the waves' order
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u)
+        if (half == 0) mates[wave][u * 32 + col] = got[u];
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+        got[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TEAM; ++i) got[u] += mates[wave - mate + i][u * 32 + col];
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u)
+      if (mate == 0 && half == 0 && to[u]) *to[u] = old[u] + got[u];
   }
   if (a.err && lost) atomicAdd(a.err, 1);
 }
