@@ -529,8 +529,10 @@ int64_t llvq_tree_workspace_bytes(int32_t batch, int32_t vocab);
  *            length: it decides only how the keys are shared out.
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (nothing is added there), starts or lengths had to
  *            be cut, or a sequence has more rows than max_chunk.
- * Sums are f32, in a fixed order: deterministic.  A key that is not finite makes its own weight NaN, no other.  weights overlaps
- * none of the inputs.  The limits on heads, tokens and launches are those of llvq_attn.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
+ * Sums are f32, in a fixed order: deterministic.  A key that is not finite, given the log-sums, spoils its own weight and no other;
+ * but a row that sees such a key has no finite log-sum, and a row whose log-sum is NaN makes NaN of all that it sees.  No page may
+ * belong to two sequences of the call; weights overlaps none of the inputs.  The limits are those of llvq_attn, and max_chunk *
+ * heads / kv_heads up to 2^31 - 256, batch * kv_heads below 2^24.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_kv_weigh(const llvq_kv_desc* d, const void* pool, float* weights, const void* q, int64_t q_token, int64_t q_head,
                   int32_t dtype, int32_t heads, const float* lse, const llvq_batch* batch, int32_t max_chunk, int32_t max_len,
                   float scale, int32_t causal, int32_t window, int32_t fresh, int32_t* err_count, void* stream);

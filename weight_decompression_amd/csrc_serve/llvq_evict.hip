@@ -112,6 +112,7 @@ LLVQ_API int llvq_kv_weigh(const llvq_kv_desc* d, const void* pool, float* weigh
   const int size = f32 ? 4 : 2;
   if (!q || !lse || !weights || !aligned(q, size) || !aligned(lse, 4) || !aligned(weights, 4)) return LLVQ_EINVAL;
   if (q_token < 0 || q_head < 0) return LLVQ_EINVAL;
+  if ((int64_t)max_chunk * (heads / d->kv_heads) > 0x7fffff00) return LLVQ_EINVAL;  // (row numbers, a block past the last one)
   WeighArgs a = {};
   a.c = c;
   a.q = q;

@@ -95,7 +95,8 @@ __device__ __forceinline__ Walk walk_of(const TreeArgs& a, int b) {
 
 // A workgroup's best of entries [from, end) of the row, in every thread.  The refused tokens are looked for only where an
 // entry may be the best so far and shares its last six bits with one of them: the first entries of every thread may all be
-// (without the bits, 96 trees of up to 32 nodes over 100003 entries take 31 us instead of 24).
+// (without the bits, 96 trees of up to 32 nodes over 100003 entries take 31 us instead of 25).  After its first entries a lane
+// only looks at what may pass the best of its wave (3 us of 25): entries come in ascending order, so an equal one has lost.
 template <bool F32, int THREADS>
 __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Walk& w, bool without, int64_t from, int64_t end) {
   constexpr int kAhead = THREADS == 1024 ? 16 : 8;
@@ -116,7 +117,7 @@ __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Wa
     return false;
   };
   const float* noise = a.noise + (int64_t)b * a.vocab;
-  Best mine;
+  Best mine, wave_best;
   for (int64_t v0 = from + tid; v0 < end; v0 += THREADS * kAhead) {
     float p[kAhead], e[kAhead];
 #pragma unroll
@@ -129,12 +130,17 @@ __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Wa
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       p[i] = v0 + THREADS * i < end ? p[i] : 0.0f;
-      any |= mine.may(p[i], e[i]);
+      any |= wave_best.may(p[i], e[i]);
     }
     if (any) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (mine.may(p[i], e[i]) && !refused((int)(v0 + THREADS * i))) mine.take(p[i], e[i], (int)(v0 + THREADS * i));
+        if (wave_best.may(p[i], e[i]) && !refused((int)(v0 + THREADS * i))) mine.take(p[i], e[i], (int)(v0 + THREADS * i));
+    }
+    if (__any(mine.score > wave_best.score)) {
+      wave_best.score = mine.score;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) wave_best.score = fmaxf(wave_best.score, __shfl_xor(wave_best.score, d));
     }
   }
   const uint64_t k = wave_max(mine.key());
@@ -145,16 +151,15 @@ __device__ __forceinline__ uint64_t best_left(const TreeArgs& a, int b, const Wa
   return top;
 }
 
-// The answer of sequence b: its path and tokens.  Where nothing but the refused is left, the draw is from all of p.
-template <bool F32, int THREADS>
-__device__ __forceinline__ void tree_answer(const TreeArgs& a, int b, const Walk& w, uint64_t k) {
-  if (w.any && k == 0) k = best_left<F32, THREADS>(a, b, w, false, 0, a.vocab);
+// The path and tokens of sequence b, all but the drawn one.
+__device__ __forceinline__ void write_path(const TreeArgs& a, int b, const Walk& w, int threads) {
   const int tid = threadIdx.x, length = __popcll(w.path);
   const int64_t at = (int64_t)b * a.width;
-  for (int i = tid; i < a.width; i += THREADS) {
-    if (i >= length) a.path[at + i] = -1, a.out[at + i] = -1;
-    if (i == length - 1) a.out[at + i] = k ? (int)(0xffffffffu - (uint32_t)k) : -1;
-  }
+  for (int i = tid; i < a.width; i += threads)
+    if (i >= length) {
+      a.path[at + i] = -1;
+      a.out[at + i] = -1;
+    }
   if (tid < kWave && (w.path >> tid & 1)) {
     const int i = __popcll(w.path & ((1ull << tid) - 1));
     a.path[at + i] = tid;
@@ -162,37 +167,53 @@ __device__ __forceinline__ void tree_answer(const TreeArgs& a, int b, const Walk
   }
   if (tid == 0) {
     a.accepted[b] = w.any ? length - 1 : 0;
-    if (a.err && (w.bad || (w.any && !k))) atomicAdd(a.err, 1);
+    if (a.err && w.bad) atomicAdd(a.err, 1);
   }
 }
+// The drawn token of a sequence that accepted that many drafts.
+__device__ __forceinline__ void write_drawn(const TreeArgs& a, int b, int accepted, uint64_t k) {
+  if (threadIdx.x != 0) return;
+  a.out[(int64_t)b * a.width + accepted] = k ? (int)(0xffffffffu - (uint32_t)k) : -1;
+  if (a.err && !k) atomicAdd(a.err, 1);
+}
 
+// Where nothing but the refused is left, the draw is from all of p.
 template <bool F32>
 __global__ __launch_bounds__(1024) void k_tree_one(TreeArgs a) {
   const int b = blockIdx.x;
   const Walk w = walk_of<F32>(a, b);
-  tree_answer<F32, 1024>(a, b, w, w.any ? best_left<F32, 1024>(a, b, w, true, 0, a.vocab) : 0);
+  write_path(a, b, w, 1024);
+  if (!w.any) return;
+  uint64_t k = best_left<F32, 1024>(a, b, w, true, 0, a.vocab);
+  if (k == 0) k = best_left<F32, 1024>(a, b, w, false, 0, a.vocab);
+  write_drawn(a, b, __popcll(w.path) - 1, k);
 }
 
 template <bool F32>
 __global__ __launch_bounds__(256) void k_tree_part(TreeArgs a) {
   const int b = blockIdx.y;
   const Walk w = walk_of<F32>(a, b);
+  if (blockIdx.x == 0) write_path(a, b, w, 256);
   if (!w.any) return;
   const int64_t from = (int64_t)blockIdx.x * a.per;
   const uint64_t k = best_left<F32, 256>(a, b, w, true, from, min(from + a.per, (int64_t)a.vocab));
   if (threadIdx.x == 0) a.keys[(int64_t)b * a.parts + blockIdx.x] = k;
 }
 
+// The best of the parts; the walk is only taken again where there is none.
 template <bool F32>
 __global__ __launch_bounds__(256) void k_tree_pick(TreeArgs a) {
   const int b = blockIdx.x;
-  const Walk w = walk_of<F32>(a, b);
+  if (a.path[(int64_t)b * a.width] < 0) return;  // no nodes
+  const int accepted = a.accepted[b];
   uint64_t k = 0;
-  for (int i = threadIdx.x & 63; w.any && i < a.parts; i += 64) {
+  for (int i = threadIdx.x & 63; i < a.parts; i += 64) {
     const uint64_t x = a.keys[(int64_t)b * a.parts + i];
     k = x > k ? x : k;
   }
-  tree_answer<F32, 256>(a, b, w, wave_max(k));  // (the same in every wave)
+  k = wave_max(k);  // (the same in every wave)
+  if (k == 0) k = best_left<F32, 256>(a, b, walk_of<F32>(a, b), false, 0, a.vocab);
+  write_drawn(a, b, accepted, k);
 }
 
 }  // namespace serve
