@@ -49,7 +49,10 @@ struct AttnArgs {
 };
 
 // Forms of the kernels.  kTree: a sequence's new tokens are the nodes of a tree, and a node sees the text before them
-// and the nodes above it.  kLse: log sum_j exp(scale q_i . k_j) of every row is written as well.
+// and the nodes above it; only the pieces that hold nodes look at its set (8 trees of 64 nodes of 64 heads over up to 16384 keys in
+// e2m1: 250 us, 238 for as many causal rows; 16 of up to 32 of 32 heads over up to 4096 in e4m3, f32: 100 and 99).  kLse: log sum_j
+// exp(scale q_i . k_j) of every row is written as well (a decode step costs nothing more, chunks of 2 x 2048 over 8192 502 us
+// instead of 480: the sum of p before it is rounded is kept beside the other).
 enum { kPlain, kTree, kLse };
 
 // What each node of a sequence's tree sees of the others, itself included: lane i holds node i's set, and its depth.

@@ -8,6 +8,10 @@
 // anything that later batches read (at or past their own, larger i), and what earlier batches read is past the barrier.  The
 // loads of the next batch are under way while a batch is written.  Where entries lie is worked out for 1024 at a time, into LDS:
 // left to each batch, list, page and codes are three loads that wait for each other.
+//
+// Measured: 8192 of up to 32768 tokens of 8 sequences and 8 heads of 128 channels in bf16, weights too: 128 us, 4.2 TB/s read and
+// written, where a large copy reaches 5.1; 2048 of 2304 of one sequence 11 us; accepted paths of 16 trees 4.1 us, a launch and
+// the chain of loads.
 #pragma once
 
 #include "serve_common.h"

@@ -12,8 +12,12 @@
 // agree, so a lane's 16 raw bytes (8, 16 or 32 channels) are one, two or four steps, and the rows are read from LDS in that
 // order.  Scores, exponentials and sums are f32; f32 queries are three bf16 terms, as in attention.
 //
-// A decode step reads each key once for a handful of rows: HBM bounds it.  A chunk of a prompt walks thousands of rows over
-// each key: the matrix instructions and the exponentials, a fused multiply-add, an exp and an add a score, share the time.
+// A decode step reads each key once for a handful of rows: HBM bounds it (64 tokens of 64 heads over 8 of 128 channels, up to
+// 16384 keys in e4m3: 168 us, 4.2 TB/s, a large copy 5.1; with a workgroup for 256 keys and no loads ahead 367).  A chunk of a prompt
+// walks thousands of rows over each key: the matrix instructions and the exponentials, a fused multiply-add, an exp and an add a
+// score, share the time (chunks of 2 x 2048 over 8192, 32 heads, e4m3: 248 us, 970 TFLOP/s of 1250 that a large library product
+// reaches; 187 us of it are left without exponentials and staging, 216 without the staging, 234 without the exponentials).  One
+// token of 32 heads over 777 keys in bf16: 5.5 us.
 #pragma once
 
 #include <type_traits>
@@ -473,7 +477,8 @@ __global__ __launch_bounds__(256, (WeighShape<DP, NT, TEAM>::kWaves)) void k_wei
     };
     // Both, for a whole block whose rows, and the 32 before it, all see all keys (its last 32 are weighed with the next):
     // after each matrix instruction a share of the exponentials, in an order that is pinned, since the two waves of a SIMD fall
-    // into step and do not overlap the one's products with the other's sums
+    // into step and do not overlap the one's products with the other's sums (chunks of 2 x 2048 over 8192: 293 us one after
+    // the other, 321 in the compiler's order, 265 so)
     auto both = [&](int buffer, int slot, int slot_before) {
       constexpr int kAhead = NT == 1 ? 3 : 2, kPer = 16 / kSteps, kAll = kSteps * kTiles, kGroup = 4 * kTiles;
       const uint8_t* from = &rows_lds[buffer][0][col * Sh::kRow];
