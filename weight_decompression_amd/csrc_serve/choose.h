@@ -4,12 +4,14 @@
 // One workgroup a (sequence, key head), which holds the weights of up to 32768 (or 4096) places in registers as 32-bit numbers
 // of the same order.  The smallest that stays is found digit by digit from the top (11, 11 and 10 bits: a histogram in LDS, its
 // sums from the top, the bin that the wanted count falls into); everything above it stays, of its equals the first.  A wave
-// holds consecutive places, 64 a round, so the places that stay are written in order after one scan over the waves' counts.
+// holds consecutive places, four a lane and 256 in four rounds (a page number and, where pages allow it, one load serve four), so
+// the places that stay are written in order after one scan over the waves' counts.
 // Nothing is sorted, and the order of the histogram's atomics changes nothing.
 //
-// Measured: 4096 of up to 32768 places of 32 sequences and 8 heads 29 us (page numbers and weights 8 of them, the digits 12, the
-// places 6; the bytes alone are worth 5), a compute unit each; 2048 of 2304 for 8 heads 8 us.  What bounds it is the chain of
-// barriers and scans behind one workgroup's loads, not the memory.
+// Measured: 4096 of up to 32768 places of 32 sequences and 8 heads 26 us, a compute unit each (12 of them the digits, 6 the
+// places; the bytes alone are worth 5): what bounds it is the chain of barriers and scans behind one workgroup's loads, and their
+// addresses; with a load a place it took 29.  2048 of 2304 for 8 heads 8 us.  Past 32768 places each digit reads all of them again:
+// 4096 of 131000 for 8 heads 135 us.
 #pragma once
 
 #include "serve_common.h"
@@ -22,6 +24,7 @@ struct ChooseArgs {
   int32_t* keep;         // [batch][heads][budget]
   int32_t* counts;       // [batch]
   int32_t budget, sinks, recent;
+  bool fours;            // weights are aligned to 16 bytes and pages hold a multiple of four
   int32_t* err;
 };
 
@@ -83,29 +86,55 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
   const int rounds = (len + kChooseThreads - 1) / kChooseThreads;
   // A block of up to HELD rounds from r0 on: this thread's place in round i, and all their numbers.  All page numbers, then
   // all weights are under way at once (past the last place: that one's again).
-  auto place_of = [&](int r0, int i) { return r0 * kChooseThreads + (wave * min(rounds - r0, HELD) + i) * kWave + lane; };
+  static_assert(HELD % 4 == 0, "four places a lane");
+  auto rounds_of = [&](int r0) { return min((rounds - r0 + 3) & ~3, HELD); };  // of a block
+  auto place_of = [&](int r0, int i) { return r0 * kChooseThreads + (wave * rounds_of(r0) + (i & ~3)) * kWave + lane * 4 + (i & 3); };
   auto hold = [&](int r0) {
-    int32_t ids[HELD];
-    int slots[HELD];
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      const uint32_t j = (uint32_t)min(place_of(r0, i), len - 1), page = divide(j, c.page);
-      slots[i] = (int)(j - page * c.page.by);
-      ids[i] = table[page];
-    }
     float w[HELD];
+    bool gone[HELD / 4];
+    if (a.fours) {
+      int32_t ids[HELD / 4];
+      int slots[HELD / 4];
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      const bool ok = ids[i] >= 0 && ids[i] < c.pages;
-      lost |= !ok;
-      w[i] = a.weights[((int64_t)(ok ? ids[i] : 0) * c.heads + head) * c.page.by + slots[i]];
-      if (!ok) slots[i] = -1;
+      for (int q = 0; q < HELD / 4; ++q) {
+        const uint32_t j = (uint32_t)min(place_of(r0, 4 * q), (len - 1) & ~3), page = divide(j, c.page);
+        slots[q] = (int)(j - page * c.page.by);
+        ids[q] = table[page];
+      }
+#pragma unroll
+      for (int q = 0; q < HELD / 4; ++q) {
+        gone[q] = ids[q] < 0 || ids[q] >= c.pages;
+        lost |= gone[q];
+        const f32x4 x = *reinterpret_cast<const f32x4*>(a.weights + ((int64_t)(gone[q] ? 0 : ids[q]) * c.heads + head) * c.page.by + slots[q]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[4 * q + k] = x[k];
+      }
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) w[i] = gone[i / 4] ? -INFINITY : w[i];
+    } else {
+      int32_t ids[HELD];
+      int slots[HELD];
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) {
+        const uint32_t j = (uint32_t)min(place_of(r0, i), len - 1), page = divide(j, c.page);
+        slots[i] = (int)(j - page * c.page.by);
+        ids[i] = table[page];
+      }
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) {
+        const bool ok = ids[i] >= 0 && ids[i] < c.pages;
+        lost |= !ok;
+        w[i] = a.weights[((int64_t)(ok ? ids[i] : 0) * c.heads + head) * c.page.by + slots[i]];
+        if (!ok) slots[i] = -1;
+      }
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) w[i] = slots[i] < 0 ? -INFINITY : w[i];  // (no page counts as NaN does)
     }
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       const int j = place_of(r0, i);
-      const uint32_t u = order_of(slots[i] < 0 ? -INFINITY : w[i]);  // (no page counts as NaN does)
-      held[i] = i >= rounds - r0 || j >= len ? kNever : j < low || j >= high ? kAlways : u;
+      const uint32_t u = order_of(w[i]);
+      held[i] = i >= rounds_of(r0) || j >= len ? kNever : j < low || j >= high ? kAlways : u;
     }
   };
   if (!LONG) hold(0);
@@ -123,7 +152,7 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
         if (LONG) hold(r0);
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
-          if (i < rounds - r0 && (held[i] & known) == least && (digit > 0 || (held[i] != kNever && held[i] != kAlways)))
+          if (i < rounds_of(r0) && (held[i] & known) == least && (digit > 0 || (held[i] != kNever && held[i] != kAlways)))
             atomicAdd(&bins[held[i] >> shift & mask], 1);
       }
       __syncthreads();
@@ -145,7 +174,7 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
     int sure = 0, same = 0;  // of this wave
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      if (i < rounds - r0) {
+      if (i < rounds_of(r0)) {
         sure += __popcll(__ballot(held[i] > least));
         same += __popcll(__ballot(held[i] == least));
       }
@@ -167,15 +196,29 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) asm volatile("" : "+v"(held[i]));
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      if (i < rounds - r0) {
-        const uint64_t above = __ballot(held[i] > least), equal = __ballot(held[i] == least), below = (1ull << lane) - 1;
-        // of the equals the first `want`: those before this lane, all of them kept, move it on
-        const int mine = sure_at + __popcll(above & below), equals = same_at + __popcll(equal & below);
-        const int at = mine + min(equals, want);
-        if (((above >> lane & 1) || ((equal >> lane & 1) && equals < want)) && at < a.budget) keep[at] = place_of(r0, i);
-        sure_at += __popcll(above);
-        same_at += __popcll(equal);
+    for (int q = 0; q < HELD / 4; ++q) {
+      if (4 * q < rounds_of(r0)) {
+        const uint64_t below = (1ull << lane) - 1;
+        uint64_t above[4], equal[4];
+        int mine = sure_at, equals = same_at;  // kept, and equal to the least, before this lane's first place
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          above[k] = __ballot(held[4 * q + k] > least);
+          equal[k] = __ballot(held[4 * q + k] == least);
+          mine += __popcll(above[k] & below);
+          equals += __popcll(equal[k] & below);
+          sure_at += __popcll(above[k]);
+          same_at += __popcll(equal[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // of the equals the first `want`: those before, all of them kept, move it on
+          const bool is_above = held[4 * q + k] > least, is_equal = held[4 * q + k] == least;
+          const int at = mine + min(equals, want);
+          if ((is_above || (is_equal && equals < want)) && at < a.budget) keep[at] = place_of(r0, 4 * q + k);
+          mine += is_above;
+          equals += is_equal;
+        }
       }
     }
   }

@@ -159,6 +159,7 @@ LLVQ_API int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const l
   a.budget = budget;
   a.sinks = sinks;
   a.recent = recent;
+  a.fours = d->page_tokens % 4 == 0 && aligned(weights, 16);
   a.err = err_count;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)(c.batch * c.heads));
