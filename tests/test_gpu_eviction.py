@@ -289,6 +289,15 @@ def test_choices(kv_heads, page, lens, budget, sinks, recent, what):
             assert got[b, h].tolist() == want + [-1] * (budget - len(want))
 
 
+def test_choices_from_weights_off_16_bytes():
+    su = Setup("fp8", 2, 32, 16, [0, 0], [3000, 40000], seed=52)
+    buffer = torch.rand(su.pages * 2 * 16 + 3, device="cuda")
+    for shift in (1, 2, 3):
+        view = buffer[shift:shift + su.pages * 32].view(su.pages, 2, 16)
+        got, want = run_choose(su, view, 1500, 4, 100), run_choose(su, view.clone(), 1500, 4, 100)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_choices_with_bad_arrays_are_bounded_and_counted():
     su = Setup("fp8", 2, 32, 16, [0, 0], [40, 100], seed=51)
     w = dev(np.exp(su.rng.randn(su.pages, 2, 16)).astype(np.float32))
