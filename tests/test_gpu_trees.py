@@ -248,3 +248,15 @@ def test_trees_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert len(caches) == 2
+
+
+def test_rows_of_no_sequence_are_left():
+    su = Setup("fp8", 1, 64, 16, [5, 3], [50, 70], seed=26)
+    caches = su.fill()
+    parents = [random_tree(su.rng, n) for n in su.new] + [[3, -7, 0, 1]]
+    q = dev(su.rng.randn(12, 2, 64).astype(np.float32))
+    for max_len in (1, 100000):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = run_tree(su, q, parents, torch.float32, max_len=max_len, err=err, max_chunk=6)
+        assert (out[8:] == 9.0).all() and err.item() == 0
+        check_tree(su, caches, parents, q, out, torch.float32)

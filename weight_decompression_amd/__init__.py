@@ -773,17 +773,28 @@ def kv_weigh(desc, pool, weights, q, lse, starts, lens, table, max_chunk, max_le
     zero, with fresh=True those of all.  q: [tokens][heads][head_dim], fp32 or bf16; lse: fp32 [tokens][heads], as attn gives it for
     the same rows, scale and mask; max_chunk: at least any sequence's new tokens; max_len: about the longest length."""
     import torch
-    call = "llvq_kv_weigh"
-    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-    if heads < 1 or desc.kv_heads < 1 or heads % desc.kv_heads:
-        raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
-    rows = _rows(q, call, "q", heads, desc.head_dim)
-    device = q.get_device()
-    at, batch = _paged(desc, pool, starts, lens, table, q.shape[0], device, call)
+    call, f32 = "llvq_kv_weigh", torch.float32
+    try:
+        shape, stride, dtype, device = q.shape, q.stride(), q.dtype, q.get_device()
+        heads, kv_heads = shape[1], desc.kv_heads
+        good = (0 <= device == weights.get_device() == lse.get_device() and len(shape) == 3 and heads >= 1 and kv_heads >= 1 and
+                heads % kv_heads == 0 and shape[2] == desc.head_dim and stride[2] == 1 and (dtype is torch.bfloat16 or dtype is f32) and
+                weights.dtype is f32 and lse.dtype is f32 and weights.shape == (desc.pages, kv_heads, desc.page_tokens) and
+                lse.shape == (shape[0], heads) and weights.is_contiguous() and lse.is_contiguous())
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        if heads < 1 or desc.kv_heads < 1 or heads % desc.kv_heads:
+            raise ValueError(f"{call}: q must be [tokens][heads][{desc.head_dim}] with a multiple of {desc.kv_heads} heads")
+        _rows(q, call, "q", heads, desc.head_dim)
+        shape, stride, dtype, device = q.shape, q.stride(), q.dtype, q.get_device()
+        _vector(weights, call, "weights", f32, (desc.pages, desc.kv_heads, desc.page_tokens), device)
+        _vector(lse, call, "lse", f32, (shape[0], heads), device)
+    at, batch = _paged(desc, pool, starts, lens, table, shape[0], device, call)
     err = None if err_count is None else _count(err_count, device, call)
-    code = _launch(load_library().llvq_kv_weigh, device, stream, desc, at, _weights(desc, weights, device, call), *rows,
-                   X_F32 if q.dtype is torch.float32 else X_BF16, heads,
-                   _vector(lse, call, "lse", torch.float32, (q.shape[0], heads), device), batch, max_chunk, max_len,
+    code = _launch(load_library().llvq_kv_weigh, device, stream, desc, at, weights.data_ptr(), q.data_ptr(), stride[0], stride[1],
+                   X_F32 if dtype is f32 else X_BF16, heads, lse.data_ptr(), batch, max_chunk, max_len,
                    desc.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, 1 if fresh else 0, err)
     if code:
         raise LlvqError(code, call)
