@@ -804,15 +804,30 @@ def kv_choose(desc, weights, lens, table, keep, counts, sinks=0, recent=0, err_c
     """keep [B][kv_heads][budget] (int32): the positions that stay of each sequence and key head, ascending, then -1: the first
     `sinks`, the last `recent`, and between them the largest weights, the lowest position of equals.  counts [B] (int32): how many."""
     import torch
-    call = "llvq_kv_choose"
-    _buffer(keep, call, "keep", torch.int32)
-    device = keep.get_device()
-    batch = _lists(lens, table, None, device, call)
-    if keep.dim() != 3 or keep.shape[:2] != (batch.batch, desc.kv_heads):
-        raise ValueError(f"{call}: keep must be [{batch.batch}][{desc.kv_heads}][budget], got {tuple(keep.shape)}")
+    call, i32, f32 = "llvq_kv_choose", torch.int32, torch.float32
+    try:
+        shape, device, (n, pages), heads = keep.shape, keep.get_device(), table.shape, desc.kv_heads
+        good = (0 <= device == lens.get_device() == table.get_device() == counts.get_device() == weights.get_device() and
+                keep.dtype is i32 and lens.dtype is i32 and table.dtype is i32 and counts.dtype is i32 and weights.dtype is f32 and
+                len(shape) == 3 and shape[0] == n and shape[1] == heads and lens.shape == counts.shape == (n,) and
+                weights.shape == (desc.pages, heads, desc.page_tokens) and keep.is_contiguous() and lens.is_contiguous() and
+                table.is_contiguous() and counts.is_contiguous() and weights.is_contiguous())
+    except (AttributeError, ValueError):
+        good = False
+    if good:
+        batch = Batch(None, lens.data_ptr(), table.data_ptr(), n, pages, 0)
+    else:
+        _buffer(keep, call, "keep", i32)
+        device = keep.get_device()
+        batch = _lists(lens, table, None, device, call)
+        if keep.dim() != 3 or keep.shape[:2] != (batch.batch, desc.kv_heads):
+            raise ValueError(f"{call}: keep must be [{batch.batch}][{desc.kv_heads}][budget], got {tuple(keep.shape)}")
+        shape = keep.shape
+        _weights(desc, weights, device, call)
+        _vector(counts, call, "counts", i32, (batch.batch,), device)
     err = None if err_count is None else _count(err_count, device, call)
-    code = _launch(load_library().llvq_kv_choose, device, stream, desc, _weights(desc, weights, device, call), batch, keep.shape[2],
-                   sinks, recent, keep.data_ptr(), _vector(counts, call, "counts", torch.int32, (batch.batch,), device), err)
+    code = _launch(load_library().llvq_kv_choose, device, stream, desc, weights.data_ptr(), batch, shape[2], sinks, recent,
+                   keep.data_ptr(), counts.data_ptr(), err)
     if code:
         raise LlvqError(code, call)
 
@@ -823,17 +838,38 @@ def kv_keep(desc, pool, keep, lens, table, counts=None, starts=None, weights=Non
     starts [B + 1], places count from the sequence's first new token, so that tree_verify's path[:, None] moves the accepted
     nodes together.  weights: moved along if given."""
     import torch
-    call = "llvq_kv_keep"
-    _buffer(keep, call, "keep", torch.int32)
-    device = keep.get_device()
-    at = _buffer(pool, call, "pool", torch.uint8, _pool_nbytes(desc))
-    _one_device(call, device, pool)
-    batch = _lists(lens, table, starts, device, call)
-    if keep.dim() != 3 or keep.shape[0] != batch.batch or keep.shape[1] not in (1, desc.kv_heads):
-        raise ValueError(f"{call}: keep must be [{batch.batch}][{desc.kv_heads} or 1][entries], got {tuple(keep.shape)}")
+    call, i32, f32 = "llvq_kv_keep", torch.int32, torch.float32
+    need = _pool_nbytes(desc)
+    try:
+        shape, device, (n, pages), heads = keep.shape, keep.get_device(), table.shape, desc.kv_heads
+        good = (0 <= device == pool.get_device() == lens.get_device() == table.get_device() and keep.dtype is i32 and
+                pool.dtype is torch.uint8 and lens.dtype is i32 and table.dtype is i32 and len(shape) == 3 and shape[0] == n and
+                (shape[1] == heads or shape[1] == 1) and lens.shape == (n,) and pool.numel() >= need and keep.is_contiguous() and
+                pool.is_contiguous() and lens.is_contiguous() and table.is_contiguous() and
+                (counts is None or (counts.get_device() == device and counts.dtype is i32 and counts.shape == (n,) and counts.is_contiguous())) and
+                (starts is None or (starts.get_device() == device and starts.dtype is i32 and starts.shape == (n + 1,) and
+                                    starts.is_contiguous())) and
+                (weights is None or (weights.get_device() == device and weights.dtype is f32 and weights.is_contiguous() and
+                                     weights.shape == (desc.pages, heads, desc.page_tokens))))
+    except (AttributeError, ValueError):
+        good = False
+    if good:
+        batch = Batch(None if starts is None else starts.data_ptr(), lens.data_ptr(), table.data_ptr(), n, pages, 0)
+    else:
+        _buffer(keep, call, "keep", i32)
+        device = keep.get_device()
+        _buffer(pool, call, "pool", torch.uint8, need)
+        _one_device(call, device, pool)
+        batch = _lists(lens, table, starts, device, call)
+        if keep.dim() != 3 or keep.shape[0] != batch.batch or keep.shape[1] not in (1, desc.kv_heads):
+            raise ValueError(f"{call}: keep must be [{batch.batch}][{desc.kv_heads} or 1][entries], got {tuple(keep.shape)}")
+        shape = keep.shape
+        if weights is not None:
+            _weights(desc, weights, device, call)
+        if counts is not None:
+            _vector(counts, call, "counts", i32, (batch.batch,), device)
     err = None if err_count is None else _count(err_count, device, call)
-    code = _launch(load_library().llvq_kv_keep, device, stream, desc, at,
-                   None if weights is None else _weights(desc, weights, device, call), batch, keep.data_ptr(), keep.shape[1],
-                   keep.shape[2], None if counts is None else _vector(counts, call, "counts", torch.int32, (batch.batch,), device), err)
+    code = _launch(load_library().llvq_kv_keep, device, stream, desc, pool.data_ptr(), None if weights is None else weights.data_ptr(), batch,
+                   keep.data_ptr(), shape[1], shape[2], None if counts is None else counts.data_ptr(), err)
     if code:
         raise LlvqError(code, call)
