@@ -558,7 +558,9 @@ int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const llvq_batch
  *             entry of -1, and one that equals its index, moves nothing.
  *   counts  : [batch] or NULL (width for all).
  *   err_count : nullable; + 1 for a (sequence, key head) with an entry that is out of order or past the length, or a page number
- *             outside the pool (the entry moves nothing), with a count, starts or a length that had to be cut.
+ *             outside the pool (the entry moves nothing), with a count, starts or a length that had to be cut.  If the batch has
+ *             starts and those of a sequence or its length had to be cut (more new tokens than cached ones among them), F is not
+ *             known and nothing of it moves.
  * No page may belong to two sequences of the call.  batch * kv_heads * (head_dim / 32 + 4) below 2^22.  Returns LLVQ_OK, LLVQ_EINVAL or LLVQ_EHIP. */
 int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, const llvq_batch* batch, const int32_t* keep, int32_t lists,
                  int32_t width, const int32_t* counts, int32_t* err_count, void* stream);

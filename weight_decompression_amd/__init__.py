@@ -836,7 +836,7 @@ def kv_keep(desc, pool, keep, lens, table, counts=None, starts=None, weights=Non
     """Move the cached token at place keep[b][h][i] of sequence b and key head h to place i, in place, for i < counts[b] (all
     entries without counts; -1 moves nothing).  keep: int32 [B][kv_heads][N], or [B][1][N] for all heads alike, ascending.  With
     starts [B + 1], places count from the sequence's first new token, so that tree_verify's path[:, None] moves the accepted
-    nodes together.  weights: moved along if given."""
+    nodes together (of a sequence with more new tokens than cached ones nothing moves).  weights: moved along if given."""
     import torch
     call, i32, f32 = "llvq_kv_keep", torch.int32, torch.float32
     need = _pool_nbytes(desc)

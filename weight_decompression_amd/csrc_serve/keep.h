@@ -129,17 +129,19 @@ static __global__ __launch_bounds__(kKeepThreads) void k_keep(KeepArgs a) {
   m.len = min(max(told, 0), (int)(cap < kMaxLen ? cap : kMaxLen));
   bool bad = m.len != told;
   m.first = 0;
-  if (a.from_new) {
-    const int64_t n = (int64_t)c.starts[b + 1] - c.starts[b];
-    const int cut = (int)(n < 0 ? 0 : n > m.len ? m.len : n);
-    bad |= n != cut;
-    m.first = m.len - cut;
-  }
   m.count = a.width;
   if (a.counts) {
     const int32_t n = a.counts[b];
     m.count = min(max(n, 0), a.width);
     bad |= n != m.count;
+  }
+  if (a.from_new) {
+    // (what had to be cut leaves the first new token's place unknown: nothing moves)
+    const int64_t n = (int64_t)c.starts[b + 1] - c.starts[b];
+    const bool known = m.len == told && n >= 0 && n <= m.len;
+    m.first = known ? m.len - (int)n : 0;
+    m.count = known ? m.count : 0;
+    bad |= !known;
   }
   m.keep = a.keep + ((int64_t)b * a.lists + (a.lists > 1 ? head : 0)) * a.width;
   m.table = c.table + (int64_t)b * c.max_pages;
