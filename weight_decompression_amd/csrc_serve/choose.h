@@ -74,12 +74,17 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(ChooseArgs a) {
     a.counts[b] = kept;
     if (a.err && len != told) atomicAdd(a.err, 1);
   }
-  if (len <= a.budget) {
-    for (int i = tid; i < a.budget; i += kChooseThreads) keep[i] = i < len ? i : -1;
-    return;
-  }
   bool lost = false;
   const int32_t* table = c.table + (int64_t)b * c.max_pages;
+  if (len <= a.budget) {
+    for (int i = tid; i < a.budget; i += kChooseThreads) keep[i] = i < len ? i : -1;
+    if (a.err && head == 0) {  // no weight is read, but pages are counted as for the others
+      const int pages = len > 0 ? (int)divide((uint32_t)(len - 1), c.page) + 1 : 0;
+      for (int i = tid; i < pages; i += kChooseThreads) lost |= table[i] < 0 || table[i] >= c.pages;
+      if (__any(lost) && lane == 0) atomicAdd(a.err, 1);
+    }
+    return;
+  }
   const int low = a.sinks, high = len - a.recent;  // those between are chosen from
   int want = a.budget - a.sinks - a.recent;
   uint32_t held[HELD];
