@@ -514,7 +514,9 @@ int64_t llvq_tree_workspace_bytes(int32_t batch, int32_t vocab);
 /* ---------------------------------------------------------------------------
  * Eviction: a sequence that has passed its budget keeps, in every key head, its first and its newest tokens and those that have
  * received the most attention.  Keys hold their positions (or none), so what stays simply moves together; the
- * sequence is shorter from then on, and its pages' tail is free.
+ * sequence is shorter from then on, and its pages' tail is free.  What stays keeps its order, but places are not positions of the text
+ * from then on: a window > 0 of llvq_attn, its forms and llvq_kv_weigh counts cached places, so it reaches kept tokens that lie farther
+ * back in the text than the window, unless recent >= window - 1 fills it (no later row sees the others: keep none of them).
  *
  * Weights: f32 [pages][kv_heads][page_tokens], one number for each cached token and key head, at the token's place.
  *

@@ -802,7 +802,8 @@ def kv_weigh(desc, pool, weights, q, lse, starts, lens, table, max_chunk, max_le
 
 def kv_choose(desc, weights, lens, table, keep, counts, sinks=0, recent=0, err_count=None, stream=None):
     """keep [B][kv_heads][budget] (int32): the positions that stay of each sequence and key head, ascending, then -1: the first
-    `sinks`, the last `recent`, and between them the largest weights, the lowest position of equals.  counts [B] (int32): how many."""
+    `sinks`, the last `recent`, and between them the largest weights, the lowest position of equals.  counts [B] (int32): how many.
+    A window counts cached places: where attention has one, recent >= window - 1 keeps what later rows see as it was."""
     import torch
     call, i32, f32 = "llvq_kv_choose", torch.int32, torch.float32
     try:
