@@ -518,7 +518,10 @@ int64_t llvq_tree_workspace_bytes(int32_t batch, int32_t vocab);
  * from then on: a window > 0 of llvq_attn, its forms and llvq_kv_weigh counts cached places, so it reaches kept tokens that lie farther
  * back in the text than the window, unless recent >= window - 1 fills it (no later row sees the others: keep none of them).
  *
- * Weights: f32 [pages][kv_heads][page_tokens], one number for each cached token and key head, at the token's place.
+ * Weights: f32 [pages][kv_heads][page_tokens], one number for each cached token and key head, at the token's place.  A place holds what
+ * it held for an earlier token until a call with its own token among the new ones, or with fresh, starts it from zero: where tokens
+ * come in without such a call (a prompt of which only the last rows are weighed), the first call needs fresh.  The accepted nodes of a
+ * tree are weighed after llvq_kv_keep has moved them: as a chain, with their rows of q and the log-sums that llvq_attn_lse gives for them.
  *
  * Add up what the cached tokens receive from the new ones:
  *     weights[j] (+)= sum_i exp(scale * q[i][h] . K_j - lse[i][h])
@@ -526,7 +529,7 @@ int64_t llvq_tree_workspace_bytes(int32_t batch, int32_t vocab);
  * from zero, whatever they held; the others are added to, or start from zero too if fresh != 0.  A sequence without new tokens is
  * left as it is.
  *   q      : [tokens][heads][head_dim] as for llvq_attn.   lse : f32 [tokens][heads], contiguous: what llvq_attn_lse gave for
- *            these rows with the same scale and mask (rows may be left out: the last 32 of a prompt, say).
+ *            these rows with the same scale and mask (rows may be left out: the last 32 of a prompt, say, with fresh).
  *   max_chunk : at least the new tokens of any sequence (rows past it are left out and counted).   max_len : about the longest
  *            length: it decides only how the keys are shared out.
  *   err_count : nullable; + 1 or more if a page number outside the pool was met (nothing is added there), starts or lengths had to

@@ -770,8 +770,9 @@ def kv_weigh(desc, pool, weights, q, lse, starts, lens, table, max_chunk, max_le
              err_count=None, stream=None):
     """weights[j] += sum of exp(scale * q[i][h] . K_j - lse[i][h]) over the new tokens i and heads h of a key head that see the
     cached token j.  weights: fp32 [pages][kv_heads][page_tokens], at the tokens' places; those of the new tokens start from
-    zero, with fresh=True those of all.  q: [tokens][heads][head_dim], fp32 or bf16; lse: fp32 [tokens][heads], as attn gives it for
-    the same rows, scale and mask; max_chunk: at least any sequence's new tokens; max_len: about the longest length."""
+    zero, with fresh=True those of all (needed once where tokens came in that no call has weighed).  q: [tokens][heads][head_dim],
+    fp32 or bf16; lse: fp32 [tokens][heads], as attn gives it for the same rows, scale and mask; max_chunk: at least any sequence's
+    new tokens; max_len: about the longest length."""
     import torch
     call, f32 = "llvq_kv_weigh", torch.float32
     try:
