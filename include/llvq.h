@@ -450,9 +450,9 @@ int llvq_attn_lse(const llvq_kv_desc* d, const void* pool, const void* q, int64_
  * the nodes above it, of all these with window > 0 only those that stand for a position above T + d_i - window.
  *   parents   : [tokens], 4-byte aligned.   max_chunk : 1 .. LLVQ_MAX_NODES.
  *   err_count : as for llvq_attn, and + 1 or more for a sequence with a parent that is no earlier node (then taken as -1) or
- *               more than LLVQ_MAX_NODES new tokens (a node past them is seen by none and sees the text alone).
+ *               more than LLVQ_MAX_NODES new tokens (a node past them is seen by none and sees the text alone, as one of depth 0).
  * The other arguments, the workspace's size, roundings and results are those of llvq_attn; a chain (parents -1, 0, 1, ..) gives
- * what llvq_attn gives with causal. */
+ * what llvq_attn gives with causal (with window > 0 where the keys are split, the last bits may differ). */
 int llvq_attn_tree(const llvq_kv_desc* d, const void* pool, const void* q, int64_t q_token, int64_t q_head, void* out,
                    int64_t out_token, int64_t out_head, int32_t dtype, int32_t heads, const llvq_batch* batch,
                    const int32_t* parents, int32_t max_chunk, int32_t max_len, float scale, int32_t window, void* workspace,
