@@ -27,6 +27,10 @@ struct WeighCut {
 inline WeighCut weigh_cut(int64_t rows, int dim, bool f32, int64_t seqs, int32_t max_len) {
   WeighCut w;
   w.team = 1;
+  // Up to 32 rows the kernel for few is the faster one, with either type of queries (16 sequences of up to 16384 keys, 64 heads
+  // over 8, us of one and the other: 8 rows in e4m3 49 and 97, 32 rows 51 and 83, in bf16 90 and 114, in e2m1 44 and 73; f32
+  // queries, 32 rows 67 and 74, 92 and 100, 61 and 63).  Wider tiles would not leave it the registers for the loads ahead: two of
+  // 256-wide f32 rows do not fit a wave.
   w.tiles = rows <= 16 ? 1 : rows <= 32 && !(f32 && dim > 128) ? 2 : 0;
   const int64_t pieces = ((int64_t)max_len + 127) / 128;  // of four waves
   if (w.tiles) {
@@ -163,7 +167,9 @@ LLVQ_API int llvq_kv_choose(const llvq_kv_desc* d, const float* weights, const l
   a.err = err_count;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)(c.batch * c.heads));
-  // by the longest sequence that the table holds
+  // By the longest sequence that the table holds: a thread holds 4 places, 32, or reads 16 at a time again for each digit.  A form
+  // for more places than a sequence has costs its loads and scans (the kernel alone, 8 heads, by 4, 32 and 16 at a time: 2304
+  // places 7.7, 14.0 and 19.2 us; 32768 places - , 24.0 and 39.5, of 32 sequences 32.3 and 57.4)
   const int64_t places = (int64_t)c.max_pages * c.page.by;
   if (places <= 4 * kChooseThreads)
     hipLaunchKernelGGL((k_choose<4, false>), grid, dim3(kChooseThreads), 0, s, a);
@@ -192,7 +198,8 @@ LLVQ_API int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, con
   a.width = width;
   a.from_new = batch->starts != nullptr;
   a.err = err_count;
-  // A workgroup takes whole rows of up to 256 bytes where that leaves 128 workgroups, else 128 bytes: half a line each costs
+  // A row of up to 64 bytes is a slice (four chunks at most).  Of wider ones
+  // a workgroup takes whole rows of up to 256 bytes where that leaves 128 workgroups, else 128 bytes: half a line each costs
   // more than the workgroups bring (8 x 8 heads, 256 bytes: 128 us whole, 134 in halves, 161 in quarters; 4 x 8 heads 92, 66
   // and 109)
   const int64_t seqs = (int64_t)c.batch * c.heads;
@@ -202,6 +209,9 @@ LLVQ_API int llvq_kv_keep(const llvq_kv_desc* d, void* pool, float* weights, con
   const int64_t grid = seqs * a.parts;
   if (grid * kKeepThreads >= (1ll << 32)) return LLVQ_EINVAL;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  // Short lists: 256 threads leave workgroups less to wait for (the kernel alone, bf16: 16 paths of up to 6 for 8 heads 4.3 us, with
+  // 1024 threads 6.3; 64 lists of 32 8.0 and 28.4); long ones need the loads of 1024 (2048 of 2304 15.5 and 11.2, 8192 of 32768 for 8
+  // x 8 heads 166 and 130).  Lists of 33 to 64 would still do better with 256 (64 lists of 48 8.5 and 28.5; one of 64 4.1 and 5.7)
   hipLaunchKernelGGL(k_keep, dim3((unsigned)grid), dim3(width <= 32 ? 256 : kKeepThreads), 0, s, a);
   return launch_status();
 }

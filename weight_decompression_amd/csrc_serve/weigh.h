@@ -13,11 +13,15 @@
 // order.  Scores, exponentials and sums are f32; f32 queries are three bf16 terms, as in attention.
 //
 // A decode step reads each key once for a handful of rows: HBM bounds it (64 tokens of 64 heads over 8 of 128 channels, up to
-// 16384 keys in e4m3: 168 us, 4.2 TB/s, a large copy 5.1; with a workgroup for 256 keys and no loads ahead 367).  A chunk of a prompt
+// 16384 keys in e4m3: 172 us, 4.2 TB/s, a large copy 5.1; with a workgroup for 256 keys and no loads ahead 367).  A chunk of a prompt
 // walks thousands of rows over each key: the matrix instructions and the exponentials, a fused multiply-add, an exp and an add a
-// score, share the time (chunks of 2 x 2048 over 8192, 32 heads, e4m3: 248 us, 970 TFLOP/s of 1250 that a large library product
+// score, share the time (chunks of 2 x 2048 over 8192, 32 heads, e4m3: 252 us, 950 TFLOP/s of 1250 that a large library product
 // reaches; 187 us of it are left without exponentials and staging, 216 without the staging, 234 without the exponentials).  One
-// token of 32 heads over 777 keys in bf16: 5.5 us.
+// token of 32 heads over 777 keys in bf16: 5.5 us.  f32 queries: 188 us and 621 (three matrix instructions for one, products and
+// exponentials one after the other).
+//
+// The log-sum is taken to log2 units before the difference: that product's rounding is |lse| 2^-24 of a weight, as much as the
+// log-sum's own as f32.
 #pragma once
 
 #include <type_traits>
