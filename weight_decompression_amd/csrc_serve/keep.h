@@ -9,7 +9,7 @@
 // loads of the next batch are under way while a batch is written.  Where entries lie is worked out for 1024 at a time, into LDS:
 // left to each batch, list, page and codes are three loads that wait for each other.
 //
-// Measured: 8192 of up to 32768 tokens of 8 sequences and 8 heads of 128 channels in bf16, weights too: 130 us, 4.1 TB/s read and
+// Measured: 8192 of up to 32768 tokens of 8 sequences and 8 heads of 128 channels in bf16, weights too: 130 us (a call 133), 4.1 TB/s read and
 // written, where a large copy reaches 5.1; in e4m3 71 (3.9), in e2m1 56 (2.6): one workgroup has all scale bytes of a (sequence,
 // key head), so 8192 of one sequence take 36 us in bf16 and 50 in e4m3 and e2m1.  2048 of 2304 of one sequence 11 us (e4m3 15);
 // accepted paths of 16 trees 4.3 us (e4m3 6.4), a launch and the chain of loads.

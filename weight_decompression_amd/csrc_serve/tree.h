@@ -11,7 +11,7 @@
 // row and its noise, read once, are what the check cannot do without (HBM bounds it for many sequences, two launches and a
 // chain of four loads, starts -> parents and tokens -> probabilities -> row, for few).  Measured: 96 trees of up to 32 nodes
 // over 100003 entries in f32 19.5 us, 3.9 TB/s, where a large copy reaches 5.1 (17 us are left when the row is not read); one of
-// 16 over 32000: 6.8 us and the second launch 2.
+// 16 over 32000: 7 us and the second launch 2.
 #pragma once
 
 #include "draft.h"
